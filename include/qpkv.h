@@ -56,6 +56,7 @@ typedef int32_t qpkv_status;
 #define QPKV_DEV_ERR_BAD_PAGE 2  /* a block_table entry outside [0, num_pages) was skipped */
 #define QPKV_DEV_ERR_BAD_INDEX 4 /* a sparse index outside [0, L_kv) was skipped */
 #define QPKV_DEV_ERR_BAD_LENGTH 8 /* a sequence length does not fit the arrays described; skipped */
+#define QPKV_DEV_ERR_NO_PAGES 16 /* qpkv_assign_pages: the free list ran out; requests were refused */
 
 /* Text of a status code (static storage, never NULL). */
 const char* qpkv_status_string(qpkv_status status);
@@ -97,7 +98,9 @@ int32_t qpkv_version(void);
 /* sizeof of the parameter structs below, so that bindings in other
  * languages can check their mirror of the layout:
  * which = 0 -> qpkv_write_params, 1 -> qpkv_prefill_params,
- * 2 -> qpkv_mla_params.  Unknown `which` returns 0. */
+ * 2 -> qpkv_mla_params, 3 -> qpkv_assign_params, 4 -> qpkv_rope_axes_params,
+ * 5 -> qpkv_write_page8_params, 6 -> qpkv_attend_page8_params.  Unknown
+ * `which` returns 0. */
 size_t qpkv_struct_size(int32_t which);
 
 /* -------------------------------------------------------------- RoPE table
@@ -560,6 +563,238 @@ typedef struct qpkv_mla_params {
 size_t qpkv_mla_workspace_bytes(int32_t num_tokens, int32_t sparse_size);
 
 qpkv_status qpkv_mla_sparse_decode(const qpkv_mla_params* params, void* stream);
+
+/* ------------------------------------------------- a serving step on device
+ * The four entry points below make one step of a continuous batch whose
+ * lengths, pages and slots live on the device (nothing of it is read back or
+ * planned on the host, so a step may be captured in a CUDA graph and
+ * replayed while requests grow):
+ *   qpkv_assign_pages   request lengths -> block_table rows, slots, positions
+ *   qpkv_rope_axes      rotary positions of q and k with one or several axes
+ *   qpkv_write_page8    append k, v to a cache in 8 bits, one scale per page
+ *   qpkv_attend_page8   attention of the new tokens over that cache
+ * All of them may be launched while the kernel before them on the stream is
+ * finishing (programmatic dependent launch); they wait for it before they
+ * read or write anything. */
+
+/* Element types of q, k, v and o, and formats of 8-bit codes. */
+#define QPKV_DTYPE_BF16 0
+#define QPKV_DTYPE_F16 1
+#define QPKV_DTYPE_F32 2       /* qpkv_rope_axes only */
+#define QPKV_FORMAT_E4M3 0     /* largest magnitude 448 */
+#define QPKV_FORMAT_INT8 1     /* symmetric, [-127, 127] */
+
+/* Pages and slots for the tokens of one step.  Request b has seqlens[b] = L
+ * tokens cached in its first ceil(L / page_size) block_table entries and
+ * brings new_lens[b] = n tokens, packed in request order.  Its new pages are
+ * taken from the top of the free list: the i-th page of the whole demand
+ * (requests in order, pages in order) is free_pages[free_count - 1 - i].
+ * Out (device; an _out array may be its input array, then updated in place):
+ *   block_table_out  int32 [B, bt_stride]: the pages held, the new ones, then -1
+ *   seqlens_out      int32 [B]: L + n
+ *   free_count_out   int32 [1]: pages left; push pages of a finished request
+ *                    by writing them at free_pages[free_count ...]
+ *   cu_seqlens       int32 [B]: inclusive prefix sums of new_lens (at most T)
+ *   slot_mapping     int32 [num_tokens]: page * page_size + offset of each token
+ *   positions        int32 [num_tokens]: L, L + 1, ... of its request
+ * Rows of slot_mapping / positions behind the last token get -1, so that T
+ * may be the fixed size of a captured graph.  A request is refused (its
+ * length and row stay, its tokens get slot and position -1) when the demand
+ * up to and with it exceeds free_count and it needs a page
+ * (QPKV_DEV_ERR_NO_PAGES), when it does not fit its table row, when its
+ * tokens do not fit num_tokens, or for a negative length
+ * (QPKV_DEV_ERR_BAD_LENGTH).  A request refused for want of pages still
+ * counts in the demand of those behind it, so a smaller one does not
+ * overtake it.  Page ids outside [0, num_pages) give slot -1 (and -1 in a
+ * new table entry) and QPKV_DEV_ERR_BAD_PAGE.
+ * Errors: INVALID_ARG (null pointer, B < 1, non-positive sizes, num_tokens
+ * or num_free negative), UNSUPPORTED (B > 8192, bt_stride or num_pages times
+ * page_size above 2^31 - 1 - page_size), CUDA. */
+typedef struct qpkv_assign_params {
+  int32_t num_seqs;      /* B */
+  int32_t num_tokens;    /* T: rows of slot_mapping and positions */
+  int32_t page_size;     /* >= 1 */
+  int32_t num_pages;     /* P */
+  int32_t bt_stride;
+  int32_t num_free;      /* entries of free_pages */
+  const int32_t* new_lens;
+  const int32_t* seqlens;
+  const int32_t* block_table;
+  const int32_t* free_pages;
+  const int32_t* free_count;
+  int32_t* block_table_out;
+  int32_t* seqlens_out;
+  int32_t* free_count_out;
+  int32_t* cu_seqlens;
+  int32_t* slot_mapping;
+  int32_t* positions;
+  int32_t* error_word;
+} qpkv_assign_params;
+
+qpkv_status qpkv_assign_pages(const qpkv_assign_params* params, void* stream);
+
+/* Rotate-half rotary positions with up to four axes (time, height, width of
+ * images and video; one axis is plain RoPE).  Pair i of a head, elements i
+ * and i + rot_dim/2, is rotated by the angle of table row
+ * positions[pair_axis[i]][t], column i (tables from qpkv_rope_table; other
+ * frequency layouts are other tables).  Products and sums are rounded to
+ * float32 one by one, the result once to the type.  Elements from rot_dim on
+ * are copied.  inverse != 0 rotates back (the transposed rotation, which
+ * takes gradients of the outputs to gradients of the inputs).
+ *   positions   device int32, axis x at positions + x * axis_stride, [T] each
+ *               (axis_stride 0: all axes share one array)
+ *   pair_axis   HOST uint8 [rot_dim / 2], each below num_axes; read in the call
+ *   q, k        device [T, H, D] of dtype with strides (elements) per token
+ *               and head, the last dimension contiguous; k may be NULL
+ *   q_out, k_out  the same; may be q / k themselves with equal strides
+ * A token whose first position is -1 is padding: its output row is not
+ * written.  Any other position outside the tables leaves the row unwritten
+ * too and sets QPKV_DEV_ERR_BAD_LENGTH.
+ * Errors: INVALID_ARG (null pointers, negative sizes, an axis out of range,
+ * a pointer not aligned to its element), UNSUPPORTED (num_axes outside 1..4, rot_dim odd, above D or
+ * above 256, dtype), CUDA. */
+typedef struct qpkv_rope_axes_params {
+  int32_t num_tokens;    /* T */
+  int32_t num_heads_q;
+  int32_t num_heads_kv;  /* ignored without k */
+  int32_t head_dim;      /* D */
+  int32_t rot_dim;
+  int32_t num_axes;
+  int32_t rope_max_pos;  /* rows of the tables */
+  int32_t dtype;         /* QPKV_DTYPE_* */
+  int32_t inverse;
+  int32_t pad0;
+  int64_t axis_stride;
+  int64_t q_stride_t, q_stride_h, k_stride_t, k_stride_h;
+  int64_t q_out_stride_t, q_out_stride_h, k_out_stride_t, k_out_stride_h;
+  const int32_t* positions;
+  const uint8_t* pair_axis;
+  const float* rope_cos;   /* [rope_max_pos, rot_dim / 2] */
+  const float* rope_sin;
+  const void* q;
+  const void* k;
+  void* q_out;
+  void* k_out;
+  int32_t* error_word;
+} qpkv_rope_axes_params;
+
+qpkv_status qpkv_rope_axes(const qpkv_rope_axes_params* params, void* stream);
+
+/* Append k, v to a paged cache in 8 bits with one float scale per (page, kv
+ * head), K and V each.  New token t of sequence b goes to position p =
+ * start_pos[b] + (t - begin_b), page block_table[b, p / page_size].  Per
+ * page, head and tensor, with amax the largest magnitude of the new tokens
+ * in it:
+ *   a page without earlier tokens of the sequence:  s = amax / QMAX
+ *   a partly filled page:  s = max(s_old, amax / QMAX); when it grows, the
+ *     earlier tokens' codes become RNE((code * s_old) / s)
+ *   new codes RNE(x / s); s = 0 gives zero codes
+ * QMAX = 448 (E4M3) or 127 (INT8); divisions are IEEE float32.  k and v must
+ * be finite.  Slots behind the new tokens, other pages and their scales are
+ * left as they are.  A page may be written for one sequence only per call.
+ * Pools: u8 (E4M3) or int8 [P, page_size, Hkv, D] (NHD) or [P, Hkv,
+ * page_size, D] (HND); scales float [P, Hkv].  k, v: [T, Hkv, D] with strides
+ * per token and head.  start_pos int32 [B] or NULL (all zero).
+ * Page ids outside [0, num_pages) are skipped (QPKV_DEV_ERR_BAD_PAGE), so are
+ * positions past the table row and lengths that do not fit
+ * (QPKV_DEV_ERR_BAD_LENGTH).
+ * Errors: INVALID_ARG (null pointers, non-positive sizes, pointers not
+ * 16-byte aligned or strides not multiples of 8 elements), UNSUPPORTED (D
+ * not 64 or 128, page_size not a multiple of 16, dtype, format, layout), CUDA. */
+typedef struct qpkv_write_page8_params {
+  int32_t num_seqs;      /* B */
+  int32_t num_tokens;    /* T */
+  int32_t num_heads_kv;
+  int32_t head_dim;      /* 64 or 128 */
+  int32_t page_size;
+  int32_t num_pages;
+  int32_t bt_stride;
+  int32_t dtype;         /* of k and v: QPKV_DTYPE_BF16 or _F16 */
+  int32_t format;        /* QPKV_FORMAT_* */
+  int32_t kv_layout;     /* QPKV_KV_LAYOUT_* */
+  int64_t k_stride_t, k_stride_h, v_stride_t, v_stride_h;
+  const int32_t* cu_seqlens_q;
+  const int32_t* start_pos;
+  const int32_t* block_table;
+  const void* k;
+  const void* v;
+  void* k_pool;
+  void* v_pool;
+  float* k_scale;        /* [P, Hkv] */
+  float* v_scale;
+  int32_t* error_word;
+} qpkv_write_page8_params;
+
+qpkv_status qpkv_write_page8(const qpkv_write_page8_params* params, void* stream);
+
+/* Attention of varlen queries over the cache qpkv_write_page8 writes, from
+ * single tokens to whole prompts.  Query i of sequence b (n rows, L cached
+ * tokens, the new ones among them) has position at = L - n + i;
+ *   x(i, j) = sm_scale * q_i . K_j, then cap * tanh(x / cap) with logit_cap > 0,
+ *             then + alibi_slopes[head] * (j - at) when given
+ *   o_i = sum_j softmax_j(x(i, .)) V_j,  lse_i = ln sum_j exp(x(i, j))
+ * over the keys j with
+ *   j < L, and when causal j <= at or j < prefix_lens[b] (a prefix whose
+ *   tokens see one another), and with window > 0 also j > at - window.
+ * Rows that see no key get o = 0 and lse = -inf; rows of o and lse behind the
+ * last sequence are left as they are.  kv head of q head h: h / (Hq / Hkv).
+ *   q, o          [T, Hq, D] of dtype, contiguous; lse float [T, Hq] or NULL
+ *   cu_seqlens_q  int32 [B] inclusive prefix sums; seqlens_kv int32 [B] (L)
+ *   block_table   int32 [B, bt_stride]; entries past L are never read
+ *   alibi_slopes  float [Hq] or NULL; prefix_lens int32 [B] or NULL
+ *   workspace     qpkv_attend_page8_workspace_bytes bytes, 16-byte aligned,
+ *                 overwritten; calls that may overlap need one each
+ * Queries enter the product with every bit (bf16 values below 2^-31 of their
+ * row's largest flush), P as f16, sums in float32.  Value scales below 2^-100
+ * count as 2^-100; scales must not be negative.
+ * A key whose page id lies outside [0, num_pages) is skipped
+ * (QPKV_DEV_ERR_BAD_PAGE).  A sequence whose rows or length do not fit the
+ * arrays has no rows or no keys (QPKV_DEV_ERR_BAD_LENGTH).
+ * max_seqlen_q (a host bound on any n, <= 0: unknown) only picks the kernels.
+ * sm_scale <= 0 selects 1/sqrt(D).
+ * Errors: INVALID_ARG (null or misaligned pointers, negative sizes, a cap
+ * that is negative or not finite), UNSUPPORTED (D not 64 or 128, page_size
+ * not a multiple of 16, Hq % Hkv, dtype, format, layout, T * Hq / Hkv or
+ * bt_stride * page_size above 2^31 - 65), WORKSPACE_TOO_SMALL, CUDA. */
+typedef struct qpkv_attend_page8_params {
+  int32_t num_seqs;      /* B */
+  int32_t num_tokens;    /* T */
+  int32_t max_seqlen_q;
+  int32_t num_heads_q;
+  int32_t num_heads_kv;
+  int32_t head_dim;      /* 64 or 128 */
+  int32_t page_size;
+  int32_t num_pages;
+  int32_t bt_stride;
+  int32_t dtype;         /* of q and o: QPKV_DTYPE_BF16 or _F16 */
+  int32_t format;        /* QPKV_FORMAT_* */
+  int32_t kv_layout;     /* QPKV_KV_LAYOUT_* */
+  int32_t causal;
+  int32_t window;        /* 0: no window */
+  float sm_scale;
+  float logit_cap;       /* 0: no cap */
+  const int32_t* cu_seqlens_q;
+  const int32_t* seqlens_kv;
+  const int32_t* block_table;
+  const int32_t* prefix_lens;
+  const float* alibi_slopes;
+  const void* q;
+  const void* k_pool;
+  const void* v_pool;
+  const float* k_scale;  /* [P, Hkv] */
+  const float* v_scale;
+  void* o;
+  float* lse;
+  void* workspace;
+  size_t workspace_bytes;
+  int32_t* error_word;
+} qpkv_attend_page8_params;
+
+/* Device workspace bytes of qpkv_attend_page8 (0 for arguments it refuses). */
+size_t qpkv_attend_page8_workspace_bytes(int32_t num_seqs, int32_t num_tokens, int32_t num_heads_q,
+                                         int32_t num_heads_kv, int32_t head_dim);
+
+qpkv_status qpkv_attend_page8(const qpkv_attend_page8_params* params, void* stream);
 
 #ifdef __cplusplus
 }

@@ -17,6 +17,8 @@ import os
 __all__ = [
     "QpkvError", "load", "check_errors", "selftest_wait_timeout", "rope_table", "write_cache_fp8", "write_cache_int8_block128_rope",
     "write_cache_mla", "DecodePlan", "PAGE_ROW_MLA",
+    "assign_pages", "axis_sections", "rope_axes", "write_cache_page8", "attend_page8",
+    "attend_page8_workspace",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -36,6 +38,7 @@ DEV_ERR_TIMEOUT = 1
 DEV_ERR_BAD_PAGE = 2
 DEV_ERR_BAD_INDEX = 4
 DEV_ERR_BAD_LENGTH = 8
+DEV_ERR_NO_PAGES = 16
 
 ERR_UNSUPPORTED = 2
 ERR_CUDA = 4
@@ -98,6 +101,53 @@ class MlaParams(ctypes.Structure):
             "lse", "workspace")] + [
         ("workspace_bytes", ctypes.c_size_t), ("error_word", _p)]
 
+
+
+class AssignParams(ctypes.Structure):
+    """Mirror of ``qpkv_assign_params`` (include/qpkv.h)."""
+    _fields_ = [(n, _i32) for n in (
+        "num_seqs", "num_tokens", "page_size", "num_pages", "bt_stride", "num_free")] + [
+        (n, _p) for n in (
+            "new_lens", "seqlens", "block_table", "free_pages", "free_count", "block_table_out",
+            "seqlens_out", "free_count_out", "cu_seqlens", "slot_mapping", "positions",
+            "error_word")]
+
+
+class RopeAxesParams(ctypes.Structure):
+    """Mirror of ``qpkv_rope_axes_params`` (include/qpkv.h)."""
+    _fields_ = [(n, _i32) for n in (
+        "num_tokens", "num_heads_q", "num_heads_kv", "head_dim", "rot_dim", "num_axes",
+        "rope_max_pos", "dtype", "inverse", "pad0")] + [
+        (n, ctypes.c_int64) for n in (
+            "axis_stride", "q_stride_t", "q_stride_h", "k_stride_t", "k_stride_h",
+            "q_out_stride_t", "q_out_stride_h", "k_out_stride_t", "k_out_stride_h")] + [
+        ("positions", _p), ("pair_axis", ctypes.c_char_p)] + [
+        (n, _p) for n in ("rope_cos", "rope_sin", "q", "k", "q_out", "k_out", "error_word")]
+
+
+class WritePage8Params(ctypes.Structure):
+    """Mirror of ``qpkv_write_page8_params`` (include/qpkv.h)."""
+    _fields_ = [(n, _i32) for n in (
+        "num_seqs", "num_tokens", "num_heads_kv", "head_dim", "page_size", "num_pages",
+        "bt_stride", "dtype", "format", "kv_layout")] + [
+        (n, ctypes.c_int64) for n in ("k_stride_t", "k_stride_h", "v_stride_t", "v_stride_h")] + [
+        (n, _p) for n in (
+            "cu_seqlens_q", "start_pos", "block_table", "k", "v", "k_pool", "v_pool", "k_scale",
+            "v_scale", "error_word")]
+
+
+class AttendPage8Params(ctypes.Structure):
+    """Mirror of ``qpkv_attend_page8_params`` (include/qpkv.h)."""
+    _fields_ = [(n, _i32) for n in (
+        "num_seqs", "num_tokens", "max_seqlen_q", "num_heads_q", "num_heads_kv", "head_dim",
+        "page_size", "num_pages", "bt_stride", "dtype", "format", "kv_layout", "causal",
+        "window")] + [("sm_scale", ctypes.c_float), ("logit_cap", ctypes.c_float)] + [
+        (n, _p) for n in (
+            "cu_seqlens_q", "seqlens_kv", "block_table", "prefix_lens", "alibi_slopes", "q",
+            "k_pool", "v_pool", "k_scale", "v_scale", "o", "lse", "workspace")] + [
+        ("workspace_bytes", ctypes.c_size_t), ("error_word", _p)]
+
+
 def _declare(lib):
     S = ctypes.c_size_t
     P64 = ctypes.POINTER(ctypes.c_int64)
@@ -128,6 +178,11 @@ def _declare(lib):
         "qpkv_mla_workspace_bytes": (S, [_i32, _i32]),
         "qpkv_smooth_workspace_bytes": (S, [_i32, _i32, _i32]),
         "qpkv_mla_sparse_decode": (_i32, [ctypes.POINTER(MlaParams), _p]),
+        "qpkv_assign_pages": (_i32, [ctypes.POINTER(AssignParams), _p]),
+        "qpkv_rope_axes": (_i32, [ctypes.POINTER(RopeAxesParams), _p]),
+        "qpkv_write_page8": (_i32, [ctypes.POINTER(WritePage8Params), _p]),
+        "qpkv_attend_page8_workspace_bytes": (S, [_i32, _i32, _i32, _i32, _i32]),
+        "qpkv_attend_page8": (_i32, [ctypes.POINTER(AttendPage8Params), _p]),
         "qpkv_error_status": (_i32, [_i32]),
         "qpkv_error_check": (_i32, [_p, ctypes.POINTER(_i32)]),
         "qpkv_selftest_wait_timeout": (_i32, [ctypes.c_int64, _p, _p]),
@@ -755,4 +810,272 @@ def mla_sparse_decode(q, kv_pool, sparse_indices, block_table, seqlens_kv, cu_se
     prm.workspace, prm.workspace_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
     prm.error_word = _ptr(error_word)
     _check(lib.qpkv_mla_sparse_decode(ctypes.byref(prm), _stream()), "qpkv_mla_sparse_decode")
+    return out
+
+
+# ------------------------------------------- a serving step on the device
+
+def _on_current(t, name):
+    """The kernels run on the current device's stream: so must the tensor."""
+    torch = _torch()
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on the GPU")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} must live on the current device")
+
+
+def _arr(t, name, dtype, shape):
+    """Data pointer of a contiguous GPU tensor of the given dtype and shape."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    _on_current(t, name)
+    return t.data_ptr()
+
+
+def _heads(t, name, dtype, T, D=None, H=None):
+    """Data pointer and (token, head) strides of a [T, H, D] GPU tensor whose
+    last dimension is contiguous."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[0] != T or (D is not None and t.shape[2] != D) or (
+            H is not None and t.shape[1] != H):
+        raise ValueError(f"{name} must be [{T}, {H or 'H'}, {D or 'D'}], got {list(t.shape)}")
+    st, sh, sd = t.stride()
+    if sd != 1 and t.shape[2] > 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    _on_current(t, name)
+    return t.data_ptr(), st, sh
+
+
+def _error_ptr(error_word):
+    return None if error_word is None else _arr(error_word, "error_word", _torch().int32, (1,))
+
+
+def _dtype_code(dtype, f32=False):
+    torch = _torch()
+    code = {torch.bfloat16: 0, torch.float16: 1}.get(dtype, 2 if f32 and dtype == torch.float32
+                                                     else None)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}")
+    return code
+
+
+def _format_code(pool):
+    torch = _torch()
+    if pool.dtype == torch.uint8:
+        return 0                                    # E4M3 codes
+    if pool.dtype == torch.int8:
+        return 1
+    raise TypeError(f"pools must be uint8 (E4M3) or int8, got {pool.dtype}")
+
+
+def assign_pages(new_lens, seqlens, block_table, free_pages, free_count, page_size, num_pages,
+                 num_tokens, block_table_out=None, seqlens_out=None, free_count_out=None,
+                 cu_seqlens=None, slot_mapping=None, positions=None, error_word=None):
+    """Pages and slots for the tokens of one step, from request lengths on the
+    GPU.  new_lens, seqlens int32 [B] (tokens the step brings / tokens cached);
+    block_table int32 [B, W]; free_pages int32 [F], a stack whose first
+    free_count (int32 [1]) entries are free pages, taken from the end;
+    num_tokens: rows of slot_mapping / positions (at least sum(new_lens), or
+    the fixed size of a captured graph).  Returns (block_table, seqlens,
+    free_count, cu_seqlens, slot_mapping, positions); the first three are new
+    tensors, or the given outputs, which may be the inputs themselves.
+    Refused requests (no pages, no room) keep their length and row and get
+    slot and position -1; the device error word says so."""
+    torch = _torch()
+    lib = load()
+    i32 = torch.int32
+    B, W = block_table.shape
+    p = AssignParams(B, num_tokens, page_size, num_pages, W, free_pages.shape[0])
+    p.new_lens = _arr(new_lens, "new_lens", i32, (B,))
+    p.seqlens = _arr(seqlens, "seqlens", i32, (B,))
+    p.block_table = _arr(block_table, "block_table", i32, (B, W))
+    p.free_pages = _arr(free_pages, "free_pages", i32, (free_pages.shape[0],))
+    p.free_count = _arr(free_count, "free_count", i32, (1,))
+    dev = block_table.device
+
+    def out(t, name, shape):
+        if t is None:
+            t = torch.empty(shape, dtype=i32, device=dev)
+            return t, t.data_ptr()
+        return t, _arr(t, name, i32, shape)
+
+    block_table_out, p.block_table_out = out(block_table_out, "block_table_out", (B, W))
+    seqlens_out, p.seqlens_out = out(seqlens_out, "seqlens_out", (B,))
+    free_count_out, p.free_count_out = out(free_count_out, "free_count_out", (1,))
+    cu_seqlens, p.cu_seqlens = out(cu_seqlens, "cu_seqlens", (B,))
+    slot_mapping, p.slot_mapping = out(slot_mapping, "slot_mapping", (num_tokens,))
+    positions, p.positions = out(positions, "positions", (num_tokens,))
+    p.error_word = _error_ptr(error_word)
+    _check(lib.qpkv_assign_pages(ctypes.byref(p), _stream()), "qpkv_assign_pages")
+    return block_table_out, seqlens_out, free_count_out, cu_seqlens, slot_mapping, positions
+
+
+def axis_sections(sections, interleaved=False):
+    """The axis of each rotary pair for ``rope_axes``, as bytes: sections[x]
+    pairs of axis x, in blocks (first sections[0] pairs of axis 0, ...), or
+    interleaved: the axes take turns pair by pair (0, 1, 2, 0, 1, 2, ...).  A
+    turn of an axis that has used up its pairs goes to axis 0, or when that
+    has none left either, to the first axis that has."""
+    if not 1 <= len(sections) <= 4 or any(n < 0 for n in sections):
+        raise ValueError("one to four sections of non-negative length")
+    if not interleaved:
+        return b"".join(bytes([x]) * n for x, n in enumerate(sections))
+    left, axis = list(sections), bytearray()
+    for i in range(sum(sections)):
+        x = i % len(left)
+        if left[x] == 0:
+            x = next(y for y, n in enumerate(left) if n > 0)
+        left[x] -= 1
+        axis.append(x)
+    return bytes(axis)
+
+
+def rope_axes(q, positions, pair_axis, rope_cos, rope_sin, k=None, q_out=None, k_out=None,
+              inverse=False, error_word=None):
+    """Rotate-half rotary positions with one to four axes.  q [T, Hq, D] and k
+    [T, Hkv, D] (bf16, f16 or f32; slices of a fused projection are fine);
+    positions int32 [axes, T] (axes may be expanded); pair_axis: bytes, the
+    axis of each of the R/2 pairs (``axis_sections``); rope_cos / rope_sin
+    float32 [max_pos, R/2] (``rope_table(theta, max_pos, R)``).  Returns q_out,
+    or (q_out, k_out) with k: new contiguous tensors, or the given ones, which
+    may be q and k themselves.  inverse=True rotates back (also the gradient's
+    way through the rotation).  Rows whose first position is -1 are padding
+    and not written."""
+    torch = _torch()
+    lib = load()
+    T, Hq, D = q.shape
+    half = len(pair_axis)
+    p = RopeAxesParams()
+    p.num_tokens, p.num_heads_q, p.head_dim, p.rot_dim = T, Hq, D, 2 * half
+    p.dtype = _dtype_code(q.dtype, f32=True)
+    p.inverse = 1 if inverse else 0
+    p.q, p.q_stride_t, p.q_stride_h = _heads(q, "q", q.dtype, T)
+    if q_out is None:
+        q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
+    p.q_out, p.q_out_stride_t, p.q_out_stride_h = _heads(q_out, "q_out", q.dtype, T, D, Hq)
+    if k is not None:
+        p.k, p.k_stride_t, p.k_stride_h = _heads(k, "k", q.dtype, T, D)
+        Hkv = k.shape[1]
+        p.num_heads_kv = Hkv
+        if k_out is None:
+            k_out = torch.empty((T, Hkv, D), dtype=q.dtype, device=q.device)
+        p.k_out, p.k_out_stride_t, p.k_out_stride_h = _heads(k_out, "k_out", q.dtype, T, D, Hkv)
+    if positions.dtype != torch.int32 or positions.dim() != 2 or positions.shape[1] != T or (
+            T > 1 and positions.stride(1) != 1):
+        raise ValueError("positions must be int32 [axes, T], contiguous along T")
+    _on_current(positions, "positions")
+    p.num_axes, p.axis_stride, p.positions = (positions.shape[0], positions.stride(0),
+                                              positions.data_ptr())
+    p.pair_axis = bytes(pair_axis)
+    p.rope_max_pos = rope_cos.shape[0]
+    p.rope_cos = _arr(rope_cos, "rope_cos", torch.float32, (p.rope_max_pos, half))
+    p.rope_sin = _arr(rope_sin, "rope_sin", torch.float32, (p.rope_max_pos, half))
+    p.error_word = _error_ptr(error_word)
+    _check(lib.qpkv_rope_axes(ctypes.byref(p), _stream()), "qpkv_rope_axes")
+    return q_out if k is None else (q_out, k_out)
+
+
+def _pools(p, k_pool, v_pool, k_scale, v_scale, block_table, B, kv_layout):
+    """Fill in and check the cache's arguments; returns (Hkv, D)."""
+    torch = _torch()
+    if kv_layout not in KV_LAYOUTS:
+        raise ValueError("kv_layout must be 'NHD' or 'HND'")
+    p.format = _format_code(k_pool)
+    if kv_layout == "HND":
+        P, H, ps, D = k_pool.shape
+    else:
+        P, ps, H, D = k_pool.shape
+    p.k_pool = _arr(k_pool, "k_pool", k_pool.dtype, k_pool.shape)
+    p.v_pool = _arr(v_pool, "v_pool", k_pool.dtype, k_pool.shape)
+    p.k_scale = _arr(k_scale, "k_scale", torch.float32, (P, H))
+    p.v_scale = _arr(v_scale, "v_scale", torch.float32, (P, H))
+    p.bt_stride = block_table.shape[1]
+    p.block_table = _arr(block_table, "block_table", torch.int32, (B, p.bt_stride))
+    p.num_seqs, p.num_heads_kv, p.head_dim, p.page_size, p.num_pages = B, H, D, ps, P
+    p.kv_layout = KV_LAYOUTS[kv_layout]
+    return H, D
+
+
+def write_cache_page8(k, v, cu_seqlens, block_table, k_pool, v_pool, k_scale, v_scale,
+                      start_pos=None, kv_layout="NHD", error_word=None):
+    """Append k, v [T, Hkv, D] (bf16 or f16; slices of a fused projection are
+    fine) to a cache in 8 bits with one scale per (page, kv head): pools uint8
+    (E4M3) or int8 [P, page_size, Hkv, D] (kv_layout "HND": [P, Hkv,
+    page_size, D]), scales float32 [P, Hkv].  A partly filled page's earlier
+    codes are rescaled when the new tokens raise its scale."""
+    torch = _torch()
+    lib = load()
+    T, B = k.shape[0], cu_seqlens.shape[0]
+    p = WritePage8Params()
+    H, D = _pools(p, k_pool, v_pool, k_scale, v_scale, block_table, B, kv_layout)
+    p.num_tokens = T
+    p.dtype = _dtype_code(k.dtype)
+    p.k, p.k_stride_t, p.k_stride_h = _heads(k, "k", k.dtype, T, D, H)
+    p.v, p.v_stride_t, p.v_stride_h = _heads(v, "v", k.dtype, T, D, H)
+    p.cu_seqlens_q = _arr(cu_seqlens, "cu_seqlens", torch.int32, (B,))
+    if start_pos is not None:
+        p.start_pos = _arr(start_pos, "start_pos", torch.int32, (B,))
+    p.error_word = _error_ptr(error_word)
+    _check(lib.qpkv_write_page8(ctypes.byref(p), _stream()), "qpkv_write_page8")
+
+
+def attend_page8_workspace(num_seqs, num_tokens, num_heads_q, num_heads_kv, head_dim,
+                           device="cuda"):
+    """A device workspace large enough for ``attend_page8``."""
+    torch = _torch()
+    n = int(load().qpkv_attend_page8_workspace_bytes(int(num_seqs), int(num_tokens),
+                                                     int(num_heads_q), int(num_heads_kv),
+                                                     int(head_dim)))
+    return torch.empty(((n + 15) // 16) * 16, dtype=torch.uint8, device=device)
+
+
+def attend_page8(q, k_pool, v_pool, k_scale, v_scale, block_table, cu_seqlens_q, seqlens_kv,
+                 max_seqlen_q=0, sm_scale=None, causal=True, logit_cap=0.0, window=0,
+                 alibi_slopes=None, prefix_lens=None, kv_layout="NHD", out=None, lse=None,
+                 workspace=None, error_word=None):
+    """Attention of varlen queries (bf16 or f16 [T, Hq, D]) over the cache
+    ``write_cache_page8`` writes, from single tokens to whole prompts; returns
+    o [T, Hq, D] (``lse`` float32 [T, Hq] filled when given).  cu_seqlens_q:
+    inclusive prefix sums of the query counts; seqlens_kv: cached tokens, the
+    new ones among them.  logit_cap c > 0: scores c * tanh(x / c); window w >
+    0: the last w keys only; alibi_slopes float32 [Hq]: slope * (j - i) is
+    added; prefix_lens int32 [B]: keys before it are seen by every row.
+    max_seqlen_q: a bound on the queries of a sequence if known (0: T)."""
+    torch = _torch()
+    lib = load()
+    T, Hq, D = q.shape
+    B = cu_seqlens_q.shape[0]
+    p = AttendPage8Params()
+    H, Dp = _pools(p, k_pool, v_pool, k_scale, v_scale, block_table, B, kv_layout)
+    if D != Dp:
+        raise ValueError(f"q must be [T, Hq, {Dp}]")
+    p.num_tokens, p.max_seqlen_q, p.num_heads_q = T, max_seqlen_q, Hq
+    p.dtype = _dtype_code(q.dtype)
+    p.causal, p.window = 1 if causal else 0, window
+    p.sm_scale, p.logit_cap = (float(sm_scale) if sm_scale else 0.0), float(logit_cap)
+    p.q = _arr(q, "q", q.dtype, q.shape)
+    p.cu_seqlens_q = _arr(cu_seqlens_q, "cu_seqlens_q", torch.int32, (B,))
+    p.seqlens_kv = _arr(seqlens_kv, "seqlens_kv", torch.int32, (B,))
+    if alibi_slopes is not None:
+        p.alibi_slopes = _arr(alibi_slopes, "alibi_slopes", torch.float32, (Hq,))
+    if prefix_lens is not None:
+        p.prefix_lens = _arr(prefix_lens, "prefix_lens", torch.int32, (B,))
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    p.o = _arr(out, "out", q.dtype, q.shape)
+    if lse is not None:
+        p.lse = _arr(lse, "lse", torch.float32, (T, Hq))
+    if workspace is None:
+        n = int(lib.qpkv_attend_page8_workspace_bytes(B, T, Hq, H, D))
+        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+    else:
+        _on_current(workspace, "workspace")
+    p.workspace, p.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    p.error_word = _error_ptr(error_word)
+    _check(lib.qpkv_attend_page8(ctypes.byref(p), _stream()), "qpkv_attend_page8")
     return out

@@ -204,6 +204,10 @@ size_t qpkv_struct_size(int32_t which) {
     case 0: return sizeof(qpkv_write_params);
     case 1: return sizeof(qpkv_prefill_params);
     case 2: return sizeof(qpkv_mla_params);
+    case 3: return sizeof(qpkv_assign_params);
+    case 4: return sizeof(qpkv_rope_axes_params);
+    case 5: return sizeof(qpkv_write_page8_params);
+    case 6: return sizeof(qpkv_attend_page8_params);
     default: return 0;
   }
 }

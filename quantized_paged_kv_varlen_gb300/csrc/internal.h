@@ -77,6 +77,17 @@ cudaError_t launch_prefill_int8(const qpkv_prefill_params& p, cudaStream_t strea
 size_t mla_workspace_bytes(int num_tokens, int sparse_size);
 cudaError_t launch_mla_sparse(const qpkv_mla_params& p, cudaStream_t stream, int* status);
 
+// One serving step on the device: page assignment (assign_pages.cu), rotary
+// positions (rope_axes.cu), the page-scaled 8-bit cache (write_page8.cu,
+// attend_page8.cu).
+constexpr int kAssignMaxSeqs = 8192;    // three int32 each in a CTA's shared memory
+constexpr int kAttendMaxSms = 160;      // SMs the attention workspace is sized for
+cudaError_t launch_assign_pages(const qpkv_assign_params& p, cudaStream_t stream);
+cudaError_t launch_rope_axes(const qpkv_rope_axes_params& p, cudaStream_t stream);
+cudaError_t launch_write_page8(const qpkv_write_page8_params& p, cudaStream_t stream);
+size_t attend_page8_workspace_bytes(int B, int T, int Hq, int Hkv, int D);
+cudaError_t launch_attend_page8(const qpkv_attend_page8_params& p, cudaStream_t stream);
+
 // The library-owned device error word of the current device (errors.cu),
 // used by the entry points when the caller passes no word; NULL on failure.
 int32_t* default_error_word();

@@ -1,0 +1,128 @@
+// What the kernels over the page-scaled 8-bit cache share: their arguments,
+// the keys that a query row sees, and small arithmetic.
+#pragma once
+#include <type_traits>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace qpkv {
+
+// P = 2^(y - m): log2 of the row's largest P when m is set, and the largest
+// it may become before m moves.
+constexpr float kSetP = 7.0f, kMaxP = 15.0f;
+// Value scales below this count as this: log2 and reciprocal stay finite in
+// float32 (values that small are zero beside anything a model computes).
+constexpr float kMinScale = 7.888609e-31f;   // 2^-100
+
+struct Page8Args {
+  int B, T, Hq, Hkv, G, ps, num_pages, bt_stride, causal, window;
+  float scale_log2;        // softmax scale * log2(e)
+  float scale_cap;         // softmax scale / cap
+  float cap_log2;          // cap * log2(e), 0: no cap
+  long long page_stride, tok_stride, head_stride;   // bytes (8-bit codes)
+  const int32_t *cu, *lens, *bt, *prefix;
+  const float *slopes, *ks, *vs;
+  const void* q;
+  const uint8_t *k, *v;
+  void* o;
+  float* lse;
+  int* err;
+};
+
+inline Page8Args page8_args(const qpkv_attend_page8_params& p) {
+  Page8Args a;
+  a.B = p.num_seqs, a.T = p.num_tokens, a.Hq = p.num_heads_q, a.Hkv = p.num_heads_kv;
+  a.G = p.num_heads_q / p.num_heads_kv;
+  a.ps = p.page_size, a.num_pages = p.num_pages, a.bt_stride = p.bt_stride;
+  a.causal = p.causal ? 1 : 0;
+  a.window = p.window;
+  const float scale = p.sm_scale;
+  a.scale_log2 = scale * kLog2e;
+  a.scale_cap = p.logit_cap > 0.f ? scale / p.logit_cap : 0.f;
+  a.cap_log2 = p.logit_cap > 0.f ? p.logit_cap * kLog2e : 0.f;
+  const long long D = p.head_dim;
+  const bool hnd = p.kv_layout == QPKV_KV_LAYOUT_HND;
+  a.page_stride = static_cast<long long>(p.page_size) * p.num_heads_kv * D;
+  a.tok_stride = hnd ? D : p.num_heads_kv * D;
+  a.head_stride = hnd ? p.page_size * D : D;
+  a.cu = p.cu_seqlens_q, a.lens = p.seqlens_kv, a.bt = p.block_table, a.prefix = p.prefix_lens;
+  a.slopes = p.alibi_slopes, a.ks = p.k_scale, a.vs = p.v_scale;
+  a.q = p.q;
+  a.k = static_cast<const uint8_t*>(p.k_pool), a.v = static_cast<const uint8_t*>(p.v_pool);
+  a.o = p.o, a.lse = p.lse, a.err = p.error_word;
+  return a;
+}
+
+// Query rows [t0, t0 + n) of a sequence and its cached tokens.
+struct Rows {
+  int t0, n, len, prefix;
+};
+
+// Lengths that do not fit the arrays are reported (err may be null) and give
+// a sequence without rows, or without keys.
+__device__ __forceinline__ Rows rows_of(const Page8Args& a, int b, int* err) {
+  Rows r;
+  r.t0 = seq_begin(a.cu, b);
+  r.n = __ldg(a.cu + b) - r.t0;
+  r.len = __ldg(a.lens + b);
+  r.prefix = a.prefix != nullptr ? __ldg(a.prefix + b) : 0;
+  if (r.n < 0 || r.t0 < 0 || r.t0 + static_cast<long long>(r.n) > a.T) {
+    report_error(err, kDevErrBadLength);
+    r.n = 0;
+  }
+  if (r.len < 0 || r.len > static_cast<long long>(a.bt_stride) * a.ps) {
+    report_error(err, kDevErrBadLength);
+    r.len = 0;
+  }
+  return r;
+}
+
+// Row i sees keys [row_lo, row_hi); both grow with i.  Its position is
+// len - n + i (negative for the rows of a prompt longer than its cache).
+__device__ __forceinline__ int row_hi(const Page8Args& a, const Rows& r, int i) {
+  if (!a.causal) return r.len;
+  return min(r.len, max(r.len - r.n + i + 1, r.prefix));
+}
+__device__ __forceinline__ int row_lo(const Page8Args& a, const Rows& r, int i) {
+  if (a.window <= 0) return 0;
+  return static_cast<int>(max(0ll, static_cast<long long>(r.len) - r.n + i + 1 - a.window));
+}
+
+// 2^x by the hardware approximation (relative error ~2^-22; -inf -> 0).
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// tanh(x) = 1 - 2 / (1 + e^(2x)): absolute error below 3e-7 (the hardware's
+// tanh is good to 2^-11 only, which a cap of 50 turns into 0.02 of a logit).
+__device__ __forceinline__ float tanh_of(float x) {
+  float r;
+  const float d = 1.f + fast_exp2(x * (2.f * kLog2e));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+  return fmaf(-2.f, r, 1.f);
+}
+
+// The power of two that takes a row of bf16 values with the given largest
+// magnitude to [2^14, 2^15), and its inverse: f16 then holds the row's values
+// (8 significant bits) exactly down to 2^-31 of the largest.
+__device__ __forceinline__ float q_to_f16_scale(float amax, float* inv) {
+  int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
+  e = e < -100 ? -100 : e > 127 ? 127 : e;
+  *inv = __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23);
+  return __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23);
+}
+
+template <typename E>
+__device__ __forceinline__ uint32_t pack_out(float hi, float lo) {
+  if constexpr (std::is_same<E, __half>::value) {
+    return f32x2_to_f16x2(hi, lo);
+  } else {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+}
+
+}  // namespace qpkv

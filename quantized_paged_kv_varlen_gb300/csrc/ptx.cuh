@@ -17,6 +17,7 @@ constexpr int kDevErrTimeout = 1;     // an mbarrier wait ran out
 constexpr int kDevErrBadPage = 2;     // block_table entry outside [0, num_pages)
 constexpr int kDevErrBadIndex = 4;    // sparse index outside [0, L_kv)
 constexpr int kDevErrBadLength = 8;   // sequence lengths exceed the described arrays
+constexpr int kDevErrNoPages = 16;    // the free list ran out of pages
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));

@@ -1,0 +1,511 @@
+"""GPU parity of the serving step on the device: page assignment, rotary
+axes, the page-scaled 8-bit cache write, attention over it, and the four of
+them together, against oracle/step.py.
+
+Tolerances of the attention outputs.  o is rounded once to its type (half a
+step, eps/2 relative), every P to f16 (2^-11 relative to its own p |v|), and
+a score's float32 error d <= 2^-11 scales p by e^d, so
+|got - want| <= eps/2 |want| + 2^-10 sum_j p_j |v_j| (1 + eps); the sum is
+the oracle's output for |v|.  f16 has an end: P = 2^7 ... 2^15 for the key
+with the largest weight w = p s (s its value's scale), and what rounds to a
+multiple of 2^-24 is off by up to 2^-25 = 2^-32 of that P, for each key j on
+its code c_j: another 2^-32 max_j (p_j s_j) sum_j |c_j|, which counts where the
+heaviest keys have zeros in a dimension.  Scores: float32 sums of D exact products and a
+handful of float32 operations, so the lse is within 2^-17 (1 + max |x|),
+max |x| bounded by the largest |lse| of a test plus its spread."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import rope as orope
+from oracle import step
+
+pytestmark = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
+
+
+def i32(x):
+    return torch.as_tensor(np.asarray(x, np.int32)).cuda()
+
+
+def f64(t):
+    return t.detach().cpu().to(torch.float64).numpy()
+
+
+@pytest.fixture
+def err():
+    return torch.zeros(1, dtype=torch.int32, device="cuda")
+
+
+# ------------------------------------------------------------ page assignment
+
+def _assign_case(seed, B, W, ps, hi, new_hi, free):
+    rng = np.random.default_rng(seed)
+    lens = rng.integers(0, min(hi, W * ps) + 1, B).astype(np.int32)
+    new = np.minimum(rng.integers(0, new_hi + 1, B), W * ps - lens).astype(np.int32)
+    held = -(-lens // ps)
+    perm = rng.permutation(int(held.sum()) + free + 3).astype(np.int32)
+    table = np.full((B, W), -1, np.int32)
+    at = 0
+    for b in range(B):
+        table[b, :held[b]] = perm[at:at + held[b]]
+        at += held[b]
+    pages = np.zeros(free + 5, np.int32)
+    pages[:free] = perm[at:at + free]
+    return new, lens, table, pages, free, len(perm)
+
+
+@pytest.mark.parametrize("B,W,ps,hi,new_hi,free,pad", [
+    (1, 1, 16, 0, 1, 1, 0), (1, 9, 1, 3, 5, 20, 3), (64, 513, 16, 8000, 1, 70, 0),
+    (7, 40, 48, 900, 300, 60, 100), (256, 170, 16, 2048, 512, 9000, 5), (1025, 3, 16, 40, 1, 700, 9),
+    (8192, 2, 7, 9, 3, 9000, 1), (33, 20, 16, 200, 60, 40, 0), (5, 6, 16, 80, 0, 4, 2)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_assign_pages(lib, err, B, W, ps, hi, new_hi, free, pad, in_place):
+    new, lens, table, pages, count, P = _assign_case(B + W, B, W, ps, hi, new_hi, free)
+    T = int(new.sum()) + pad
+    want = step.assign_pages(new, lens, table, pages, count, ps, T)
+    d = [i32(x) for x in (new, lens, table, pages, [count])]
+    kw = dict(block_table_out=d[2], seqlens_out=d[1], free_count_out=d[4]) if in_place else {}
+    got = lib.assign_pages(*d, ps, P, T, error_word=err, **kw)
+    for g, w, name in zip(got, want, ("table", "lens", "count", "cu", "slots", "positions")):
+        assert np.array_equal(g.cpu().numpy().reshape(-1), np.asarray(w).reshape(-1)), name
+    assert int(err) == (lib.DEV_ERR_NO_PAGES if want[6] else 0)
+    if not in_place:   # inputs are as they were
+        for x, y in zip(d, (new, lens, table, pages, [count])):
+            assert np.array_equal(x.cpu().numpy(), np.asarray(y))
+
+
+def test_assign_pages_refuses_what_does_not_fit(lib, err):
+    """Too long for its row, tokens past num_tokens, negative lengths, a
+    count outside the list, a bad page id on the stack."""
+    table = np.array([[4, -1], [5, -1], [6, 7], [-1, -1]], np.int32)
+    args = lambda new, lens, count=2, pages=(1, 2): (i32(new), i32(lens), i32(table), i32(list(pages)), i32([count]))  # noqa: E731
+    want = step.assign_pages(np.array([1, 40, 1, 2]), np.array([3, 16, 17, 0], np.int32), table,
+                             np.array([1, 2]), 2, 16, 44)
+    got = lib.assign_pages(*args([1, 40, 1, 2], [3, 16, 17, 0]), 16, 8, 44, error_word=err)
+    for g, w in zip(got, want):
+        assert np.array_equal(g.cpu().numpy().reshape(-1), np.asarray(w).reshape(-1))
+    assert int(err) == lib.DEV_ERR_BAD_LENGTH
+    err.zero_()
+    got = lib.assign_pages(*args([2, 3, 2, 1], [3, 16, 17, 0]), 16, 8, 6, error_word=err)
+    assert got[3].tolist() == [2, 5, 6, 6] and got[1].tolist() == [5, 19, 17, 0]
+    assert got[4].tolist() == [67, 68, 32, 33, 34, -1] and int(err) == lib.DEV_ERR_BAD_LENGTH
+    err.zero_()
+    got = lib.assign_pages(*args([-1, 0, 1, 1], [3, -5, 17, 0]), 16, 8, 4, error_word=err)
+    assert got[1].tolist() == [3, -5, 18, 1] and got[3].tolist() == [0, 0, 1, 2]
+    assert got[0].tolist() == [[4, -1], [5, -1], [6, 7], [2, -1]] and int(err) == lib.DEV_ERR_BAD_LENGTH
+    err.zero_()
+    got = lib.assign_pages(*args([0, 0, 0, 1], [3, 16, 17, 0], count=3), 16, 8, 1, error_word=err)
+    assert got[1].tolist() == [3, 16, 17, 0]
+    assert int(err) == lib.DEV_ERR_BAD_LENGTH | lib.DEV_ERR_NO_PAGES
+    err.zero_()
+    got = lib.assign_pages(*args([0, 0, 0, 1], [3, 16, 17, 0], pages=(1, 8)), 16, 8, 1, error_word=err)
+    assert got[4].tolist() == [-1] and got[0][3].tolist() == [-1, -1] and int(err) == lib.DEV_ERR_BAD_PAGE
+
+
+# ------------------------------------------------------------ rotary positions
+
+@pytest.mark.parametrize("T,Hq,Hkv,D,sections,inter,dtype,fused", [
+    (1, 1, 1, 64, (32,), False, "bf16", False), (5, 28, 4, 128, (16, 24, 24), False, "bf16", True),
+    (33, 3, 2, 80, (16, 12, 12), True, "f16", True), (130, 7, 1, 72, (9, 9), False, "f32", False),
+    (3, 2, 3, 96, (10, 11), True, "bf16", True), (17, 5, 2, 128, (8, 8, 8, 8), False, "f32", True),
+    (9, 1, 1, 10, (3,), False, "f16", False), (40, 2, 2, 256, (64, 32, 32), False, "bf16", False),
+    (2000, 32, 8, 128, (24, 20, 20), True, "bf16", True)])
+def test_rope_axes_bit_exact(lib, err, T, Hq, Hkv, D, sections, inter, dtype, fused):
+    rng = np.random.default_rng(T)
+    half, A = sum(sections), len(sections)
+    dt = DT[dtype]
+    x = torch.tensor(rng.standard_normal((T, Hq + 2 * Hkv, D)).astype(np.float32)).to(dt)
+    dev = x.cuda()
+    q, k = dev[:, :Hq], dev[:, Hq:Hq + Hkv]
+    if not fused:
+        q, k = q.contiguous(), k.contiguous()
+    cos, sin = lib.rope_table(1e4, 70, 2 * half)
+    pos = rng.integers(0, 70, (A, T)).astype(np.int32)
+    axis = lib.axis_sections(sections, interleaved=inter)
+    assert sorted(axis) == sorted(sum(([a] * n for a, n in enumerate(sections)), []))
+    for inverse in (False, True):
+        gq, gk = lib.rope_axes(q, i32(pos), axis, cos, sin, k=k, inverse=inverse, error_word=err)
+        for g, src in ((gq, x[:, :Hq]), (gk, x[:, Hq:Hq + Hkv])):
+            w = step.rope_axes(src.float().numpy(), pos, axis, cos.cpu().numpy(), sin.cpu().numpy(), inverse)
+            assert torch.equal(g.cpu(), torch.tensor(w).to(dt))
+    only_q = lib.rope_axes(q, i32(pos), axis, cos, sin)
+    ref = lib.rope_axes(q, i32(pos), axis, cos, sin, k=k)
+    v = dev[:, Hq + Hkv:].clone()
+    lib.rope_axes(q, i32(pos), axis, cos, sin, k=k, q_out=q, k_out=k)      # in place
+    assert torch.equal(only_q, ref[0]) and torch.equal(q, ref[0]) and torch.equal(k, ref[1])
+    assert torch.equal(dev[:, Hq + Hkv:], v) and int(err) == 0
+
+
+def test_rope_axes_leaves_padding_and_reports_bad_positions(lib, err):
+    cos, sin = lib.rope_table(1e4, 20, 64)
+    q = torch.randn(4, 2, 64, device="cuda")
+    out = torch.full_like(q, 7.0)
+    pos = i32([[3, -1, 20, 19], [3, 5, 1, 2]])
+    lib.rope_axes(q, pos, bytes([0, 1] * 16), cos, sin, q_out=out, error_word=err)
+    assert (out[1:3] == 7.0).all() and (out[[0, 3]] != 7.0).any(dim=2).all()
+    assert int(err) == lib.DEV_ERR_BAD_LENGTH
+    err.zero_()
+    lib.rope_axes(q, i32([[-1] * 4, [99] * 4]), bytes([0, 1] * 16), cos, sin, q_out=out, error_word=err)
+    assert int(err) == 0
+    one = i32([[1, 2, 3, 4]])
+    a = lib.rope_axes(q, one.expand(3, 4), bytes([0] * 8 + [1] * 12 + [2] * 12), cos, sin)
+    assert torch.equal(a, lib.rope_axes(q, one, bytes(32), cos, sin))
+
+
+def test_rope_axes_inverse_is_the_gradient(lib):
+    """For y = R(x) and a loss <w, y>, the gradient is R's transpose of w: the
+    inverse rotation; also against differences (R is linear, so one step of any
+    size gives the derivative up to float32 rounding)."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    cos, sin = lib.rope_table(1e4, 64, 64)
+    pos = torch.randint(0, 64, (3, 11), generator=g, device="cuda").to(torch.int32)
+    axis = lib.axis_sections((12, 10, 10))
+    x, w, d = (torch.randn(11, 3, 64, generator=g, device="cuda") for _ in range(3))
+    grad = lib.rope_axes(w, pos, axis, cos, sin, inverse=True).double()
+    f = lambda z: (lib.rope_axes(z, pos, axis, cos, sin).double() * w.double()).sum()  # noqa: E731
+    got, want = (grad * d.double()).sum(), (f(x + d) - f(x - d)) / 2
+    # 2112 products of values below 6, each off by a few 2^-24
+    assert abs(float(got - want)) < 2112 * 36 * 2.0 ** -22 / 8
+
+
+# ------------------------------------------------------------------- the write
+
+def _pool(P, ps, H, D, fmt, hnd, fill):
+    shape = (P, H, ps, D) if hnd else (P, ps, H, D)
+    return torch.full(shape, fill, dtype=torch.uint8 if fmt == "e4m3" else torch.int8, device="cuda")
+
+
+def _nhd(pool, hnd):
+    return (pool.transpose(1, 2) if hnd else pool).cpu().numpy().copy()
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("lens,H,D,ps,dtype,hnd", [
+    ([(0, 1)], 1, 64, 16, "bf16", False), ([(5, 30), (0, 0), (16, 16), (31, 2), (15, 1), (16, 1)], 3, 128, 16, "bf16", False),
+    ([(40, 100), (0, 7), (47, 1)], 2, 64, 48, "f16", True), ([(100, 300), (0, 129)], 5, 128, 64, "bf16", True),
+    ([(3, 1), (0, 700)], 1, 128, 1024, "f16", False), ([(200, 90)], 2, 64, 256, "bf16", False),
+    ([(n, 1) for n in range(64)], 8, 128, 16, "bf16", False)])
+def test_write_page8_bit_exact(lib, err, lens, H, D, ps, dtype, hnd, fmt):
+    """A first write, then a second one that raises the scales of partly filled
+    pages, lowers or keeps others: codes and scales equal the oracle's."""
+    rng = np.random.default_rng(len(lens) + ps)
+    W = max(-(-(a + n) // ps) for a, n in lens) + 1
+    P = W * len(lens) + 2
+    table = rng.permutation(P - 2)[:W * len(lens)].reshape(len(lens), W).astype(np.int32)
+    fill = 0x7F if fmt == "e4m3" else 99
+    kp, vp = _pool(P, ps, H, D, fmt, hnd, fill), _pool(P, ps, H, D, fmt, hnd, fill)
+    ks, vs = torch.full((P, H), 5.0, device="cuda"), torch.full((P, H), 6.0, device="cuda")
+    pools, scales = [_nhd(kp, hnd), _nhd(vp, hnd)], [ks.cpu().numpy(), vs.cpu().numpy()]
+    for begin, n in (([0] * len(lens), [a for a, _ in lens]), ([a for a, _ in lens], [n for _, n in lens])):
+        T = int(sum(n))
+        if T == 0:
+            continue
+        x = rng.standard_normal((T + 3, 2 * H + 1, D)).astype(np.float32) * np.exp(rng.standard_normal((T + 3, 1, 1)))
+        x[rng.integers(0, T, 3)] = 0.0
+        x = torch.tensor(x.astype(np.float32)).to(DT[dtype])   # three rows behind the last sequence
+        dev = x.cuda()
+        cu = np.cumsum(n).astype(np.int32)
+        lib.write_cache_page8(dev[:, :H], dev[:, H:2 * H], i32(cu), i32(table), kp, vp, ks, vs,
+                              start_pos=i32(begin) if any(begin) else None,
+                              kv_layout="HND" if hnd else "NHD", error_word=err)
+        step.write_page8(x[:, :H].float().numpy(), x[:, H:2 * H].float().numpy(), cu, begin, table, pools, scales, fmt)
+        assert np.array_equal(ks.cpu().numpy(), scales[0]) and np.array_equal(vs.cpu().numpy(), scales[1])
+        # codes; E4M3's two zeros are one value
+        for got, want in ((_nhd(kp, hnd), pools[0]), (_nhd(vp, hnd), pools[1])):
+            same = got == want
+            if fmt == "e4m3":
+                same |= ((got | want) & 0x7F) == 0
+            assert same.all()
+    assert int(err) == 0
+
+
+def test_write_page8_skips_bad_pages_and_lengths(lib, err):
+    kp, vp = _pool(4, 16, 1, 64, "int8", False, 9), _pool(4, 16, 1, 64, "int8", False, 9)
+    ks, vs = torch.full((4, 1), 5.0, device="cuda"), torch.full((4, 1), 5.0, device="cuda")
+    x = torch.ones(40, 1, 64, device="cuda", dtype=torch.bfloat16)
+    lib.write_cache_page8(x, x, i32([20, 40]), i32([[1, 4], [-1, 2]]), kp, vp, ks, vs, error_word=err)
+    assert int(err) == lib.DEV_ERR_BAD_PAGE
+    assert (kp[0] == 9).all() and (kp[3] == 9).all() and (kp[1] == 127).all()
+    assert (kp[2, :4] == 127).all() and (kp[2, 4:] == 9).all() and ks[:, 0].tolist()[0::3] == [5.0, 5.0]
+    err.zero_()   # positions past the row; rows past T
+    lib.write_cache_page8(x, x, i32([20]), i32([[3, 0]]), kp, vp, ks, vs, start_pos=i32([30]), error_word=err)
+    # slots 14, 15 join a page whose scale is 5: RNE(1 / 5) = 0
+    assert int(err) == lib.DEV_ERR_BAD_LENGTH and (kp[3] == 9).all()
+    assert (kp[0, :14] == 9).all() and (kp[0, 14:] == 0).all() and float(ks[0]) == 5.0
+    err.zero_()
+    before = kp.clone()
+    lib.write_cache_page8(x, x, i32([50]), i32([[3, 0]]), kp, vp, ks, vs, error_word=err)
+    assert int(err) == lib.DEV_ERR_BAD_LENGTH and torch.equal(kp, before)
+
+
+# --------------------------------------------------------------- the attention
+
+def _attend_case(seed, reqs, Hq, H, D, ps, fmt, dtype, hnd, slopes=False, prefix=None, size=1.0, pad=0):
+    """reqs: (queries, cached tokens) per sequence.  Unused slots and pages hold
+    NaN codes (E4M3); unused table entries -1."""
+    rng = np.random.default_rng(seed)
+    n_pages = [-(-L // ps) for _, L in reqs]
+    P, W = sum(n_pages) + 2, max(n_pages + [1]) + 1
+    perm = rng.permutation(P)
+    table = np.full((len(reqs), W), -1, np.int32)
+    at = 0
+    for b, n in enumerate(n_pages):
+        table[b, :n] = perm[at:at + n]
+        at += n
+    pools, scales = [], []
+    for _ in range(2):
+        if fmt == "e4m3":
+            c = rng.integers(0, 256, (P, ps, H, D)).astype(np.uint8)
+            c[(c & 0x7F) >= 0x7C] &= 0x87
+        else:
+            c = rng.integers(-127, 128, (P, ps, H, D)).astype(np.int8)
+        used = np.zeros((P, ps), bool)
+        for b, (_, L) in enumerate(reqs):
+            for i in range(n_pages[b]):
+                used[table[b, i], :min(ps, L - i * ps)] = True
+        c[~used] = 0x7F if fmt == "e4m3" else -128
+        unit = (20.0 if fmt == "e4m3" else 50.0)
+        pools.append(c)
+        scales.append((np.exp(rng.standard_normal((P, H))) / unit).astype(np.float32))
+    T = sum(n for n, _ in reqs)
+    q = torch.tensor((size * rng.standard_normal((T + pad, Hq, D))).astype(np.float32)).to(DT[dtype])
+    c = dict(q=q, pools=pools, scales=scales, table=table, cu=np.cumsum([n for n, _ in reqs]).astype(np.int32),
+             lens=np.array([L for _, L in reqs], np.int32), hnd=hnd, T=T,
+             slopes=(2.0 ** (-8.0 * (np.arange(Hq) + 1) / Hq)).astype(np.float32) if slopes else None,
+             prefix=np.array(prefix, np.int32) if prefix is not None else None)
+    put = lambda p: torch.tensor(np.ascontiguousarray(p.swapaxes(1, 2)) if hnd else p).cuda()  # noqa: E731
+    c["dev"] = dict(q=q.cuda(), kp=put(pools[0]), vp=put(pools[1]), ks=torch.tensor(scales[0]).cuda(),
+                    vs=torch.tensor(scales[1]).cuda(), table=i32(table), cu=i32(c["cu"]), lens=i32(c["lens"]),
+                    slopes=torch.tensor(c["slopes"]).cuda() if slopes else None,
+                    prefix=i32(prefix) if prefix is not None else None)
+    return c
+
+
+def _run_attend(lib, c, err, max_q=0, out=None, lse=None, ws=None, **kw):
+    d = c["dev"]
+    return lib.attend_page8(d["q"], d["kp"], d["vp"], d["ks"], d["vs"], d["table"], d["cu"], d["lens"],
+                            max_seqlen_q=max_q, alibi_slopes=d["slopes"], prefix_lens=d["prefix"],
+                            kv_layout="HND" if c["hnd"] else "NHD", out=out, lse=lse, workspace=ws,
+                            error_word=err, **kw)
+
+
+def _check_attend(c, got, lse, causal=True, logit_cap=0.0, window=0, sm_scale=None, skip_page=None, rows=None):
+    q = c["q"][:c["T"]].double().numpy()
+    kw = dict(causal=causal, cap=logit_cap, window=window, slopes=c["slopes"], prefix=c["prefix"], skip_page=skip_page)
+    scale = sm_scale or 1 / np.sqrt(q.shape[2])
+    flush = np.zeros(q.shape)
+    want, want_lse = step.attend_page8(q, c["pools"], c["scales"], c["table"], c["cu"], c["lens"], scale,
+                                       flush=flush, **kw)
+    mag = [c["pools"][0], c["pools"][1] & 0x7F if c["pools"][1].dtype == np.uint8 else np.abs(c["pools"][1])]
+    size, _ = step.attend_page8(q, mag, c["scales"], c["table"], c["cu"], c["lens"], scale, **kw)
+    eps = torch.finfo(c["q"].dtype).eps / 2
+    g, l = f64(got)[:c["T"]], f64(lse)[:c["T"]]
+    finite = bool(np.isfinite(g).all())
+    assert finite
+    tol = eps * np.abs(want) + 2.0 ** -10 * size * (1 + eps) + 2.0 ** -32 * flush + (2.0 ** -25 if c["q"].dtype == torch.float16 else 0)
+    worst = float((np.abs(g - want) / (tol + 1e-300)).max()) if g.size else 0.0
+    assert worst <= 1, worst
+    same_empty = np.array_equal(np.isneginf(l), np.isneginf(want_lse))
+    assert same_empty
+    fin = np.isfinite(want_lse)
+    spread = np.abs(want_lse[fin]).max() if fin.any() else 0.0
+    off = float(np.abs(l[fin] - want_lse[fin]).max()) if fin.any() else 0.0
+    assert off <= 2.0 ** -17 * (4 + 2 * spread), off
+
+
+DECODE = [(1, 1), (1, 15), (1, 16), (1, 17), (1, 100), (1, 0), (1, 333), (1, 64)]
+MIXED = [(1, 40), (5, 5), (0, 30), (3, 130), (20, 70), (2, 1), (7, 0), (1, 200)]
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("Hq,H,D,ps,dtype,hnd", [
+    (4, 1, 64, 16, "bf16", False), (32, 8, 128, 16, "bf16", False), (6, 2, 128, 48, "f16", True),
+    (5, 5, 64, 64, "f16", False), (32, 2, 128, 32, "bf16", True), (40, 2, 64, 16, "bf16", False)])
+@pytest.mark.parametrize("reqs", [DECODE, MIXED], ids=["decode", "mixed"])
+def test_attend_page8(lib, err, reqs, Hq, H, D, ps, dtype, hnd, fmt):
+    c = _attend_case(Hq + ps, reqs, Hq, H, D, ps, fmt, dtype, hnd, pad=2)
+    out = torch.full_like(c["dev"]["q"], 7.0)
+    lse = torch.full(out.shape[:2], 7.0, device="cuda")
+    _run_attend(lib, c, err, max_q=max(n for n, _ in reqs), out=out, lse=lse)
+    assert int(err) == 0 and (out[c["T"]:] == 7.0).all() and (lse[c["T"]:] == 7.0).all()
+    _check_attend(c, out, lse)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(logit_cap=20.0), dict(window=1), dict(window=33), dict(causal=False), dict(causal=False, window=20),
+    dict(logit_cap=50.0, window=64, sm_scale=0.2), dict(sm_scale=3.0)], ids=str)
+@pytest.mark.parametrize("slopes,prefix", [(False, None), (True, None), (False, [0, 50, 1, 90, 3, 9, 2, 10**9])])
+def test_attend_page8_masks_caps_and_biases(lib, err, kw, slopes, prefix):
+    for i, (fmt, dtype) in enumerate((("int8", "f16"), ("e4m3", "bf16"))):
+        c = _attend_case(i, MIXED, 6, 2, (64, 128)[i], 16, fmt, dtype, bool(i), slopes=slopes, prefix=prefix)
+        lse = torch.empty(c["q"].shape[:2], device="cuda")
+        got = _run_attend(lib, c, err, lse=lse, **kw)
+        _check_attend(c, got, lse, **kw)
+    assert int(err) == 0
+
+
+@pytest.mark.parametrize("reqs,Hq,H", [
+    ([(1, 9000)], 4, 1), ([(1, 5000), (1, 3), (1, 7001)], 8, 2), ([(3, 4100)], 8, 8), ([(1, 300)] * 40, 16, 8),
+    ([(1, 0)] * 3, 4, 1), ([(1, 31 * i % 97) for i in range(300)], 2, 1)])
+def test_attend_page8_long_and_many(lib, err, reqs, Hq, H):
+    """Runs that split one request, cover several, and cross empty ones."""
+    c = _attend_case(len(reqs), reqs, Hq, H, 128, 16, "e4m3", "bf16", False)
+    lse = torch.empty(c["q"].shape[:2], device="cuda")
+    got = _run_attend(lib, c, err, max_q=max(n for n, _ in reqs), lse=lse)
+    _check_attend(c, got, lse)
+    assert int(err) == 0
+    again = _run_attend(lib, c, err, max_q=max(n for n, _ in reqs))
+    assert torch.equal(got, again)
+
+
+@pytest.mark.parametrize("size", [1e-30, 1e-3, 300.0, 1e30])
+def test_attend_page8_query_and_value_sizes(lib, err, size):
+    """Query rows of any bf16 size (the softmax scale makes up for it), value
+    scales that differ by 2^40 between pages, and zero scales."""
+    c = _attend_case(2, [(1, 100), (2, 60)], 4, 2, 64, 16, "int8", "bf16", False, size=size)
+    rng = np.random.default_rng(0)
+    for x, name in ((c["scales"][1], "vs"),):
+        x *= (2.0 ** rng.integers(-20, 21, x.shape)).astype(np.float32)
+        c["dev"][name].copy_(torch.tensor(x))
+    page = int(c["table"][0, 1])
+    for p, s, pn, sn in ((c["pools"][0], c["scales"][0], "kp", "ks"), (c["pools"][1], c["scales"][1], "vp", "vs")):
+        p[page] = 0
+        s[page] = 0.0
+        c["dev"][pn][page] = 0
+        c["dev"][sn][page] = 0.0
+    lse = torch.empty(c["q"].shape[:2], device="cuda")
+    scale = 0.125 / size
+    if not np.isfinite(np.float32(scale)) or scale < 1e-30:
+        scale = 1e-30
+    got = _run_attend(lib, c, err, lse=lse, sm_scale=scale)
+    _check_attend(c, got, lse, sm_scale=float(np.float32(scale)))
+
+
+def test_attend_page8_skips_bad_pages_and_lengths(lib, err):
+    c = _attend_case(4, [(1, 100), (2, 40), (1, 50)], 4, 2, 64, 16, "int8", "bf16", False)
+    bad = int(c["table"][0, 2])
+    c["dev"]["table"][0, 2] = c["pools"][0].shape[0]
+    lse = torch.empty(c["q"].shape[:2], device="cuda")
+    got = _run_attend(lib, c, err, lse=lse)
+    assert int(err) == lib.DEV_ERR_BAD_PAGE
+    _check_attend(c, got, lse, skip_page=bad)
+    err.zero_()
+    c["dev"]["lens"][1] = 10 ** 6
+    c["dev"]["table"][0, 2] = bad
+    got = _run_attend(lib, c, err, lse=lse)
+    assert int(err) == lib.DEV_ERR_BAD_LENGTH and (got[1:3] == 0).all() and torch.isneginf(lse[1:3]).all()
+    err.zero_()
+    c["dev"]["cu"][2] = 10
+    c["dev"]["lens"][1] = 40
+    out = torch.full_like(c["dev"]["q"], 7.0)
+    _run_attend(lib, c, err, out=out)
+    assert int(err) == lib.DEV_ERR_BAD_LENGTH and (out[3:] == 7.0).all() and torch.equal(out[:1], got[:1])
+
+
+# ------------------------------------------------------------ the step as used
+
+def test_step_grows_a_batch_in_a_replayed_graph(lib, err):
+    """assign -> rotary -> write -> attend: two prompts admitted eagerly, then
+    decode steps replayed from one captured graph whose lengths grow on the
+    device, compared with the oracle step by step; a second graph over its own
+    workspace replays on another stream."""
+    B, H, Hq, D, ps, W, P, fmt = 3, 2, 8, 64, 16, 8, 20, "e4m3"
+    rng = np.random.default_rng(0)
+    cos, sin = lib.rope_table(1e4, W * ps, D)
+    axis = lib.axis_sections((12, 10, 10))
+    kp, vp = _pool(P, ps, H, D, fmt, False, 0), _pool(P, ps, H, D, fmt, False, 0)
+    ks, vs = torch.zeros(P, H, device="cuda"), torch.zeros(P, H, device="cuda")
+    o_pools, o_scales = [_nhd(kp, False), _nhd(vp, False)], [np.zeros((P, H), np.float32) for _ in range(2)]
+    table = torch.full((B, W), -1, dtype=torch.int32, device="cuda")
+    lens, count = i32([0] * B), i32([P])
+    pages = i32(rng.permutation(P))
+    o_state = (np.full((B, W), -1, np.int32), np.zeros(B, np.int32), P)
+
+    def device_step(x, new, old, ws=None):
+        T = x.shape[0]
+        old.copy_(lens)
+        _, _, _, cu, slots, pos = lib.assign_pages(new, lens, table, pages, count, ps, P, T, block_table_out=table,
+                                                   seqlens_out=lens, free_count_out=count, error_word=err)
+        q, k = lib.rope_axes(x[:, :Hq], pos.expand(3, T), axis, cos, sin, k=x[:, Hq:Hq + H], error_word=err)
+        lib.write_cache_page8(k, x[:, Hq + H:], cu, table, kp, vp, ks, vs, start_pos=old, error_word=err)
+        lse = torch.empty(T, Hq, device="cuda")
+        return lib.attend_page8(q, kp, vp, ks, vs, table, cu, lens, lse=lse, workspace=ws, error_word=err), lse, q
+
+    def oracle_step(x, new, o_state):
+        T = int(sum(new))
+        t, ln, cnt, cu, _, pos, refused = step.assign_pages(np.array(new), o_state[1], o_state[0],
+                                                            pages.cpu().numpy(), o_state[2], ps, T)
+        assert not refused
+        c, s = cos.cpu().numpy(), sin.cpu().numpy()
+        p3 = np.stack([pos] * 3)
+        r = lambda y: torch.tensor(step.rope_axes(y.float().numpy(), p3, axis, c, s)).bfloat16()  # noqa: E731
+        q, k = r(x[:, :Hq]), r(x[:, Hq:Hq + H])
+        step.write_page8(k.float().numpy(), x[:, Hq + H:].float().numpy(), cu, o_state[1], t, o_pools, o_scales, fmt)
+        return (t, ln, cnt), dict(q=q, pools=o_pools, scales=o_scales, table=t, cu=cu, lens=ln, T=T, slopes=None,
+                                  prefix=None)
+
+    def make(T):
+        return torch.tensor(rng.standard_normal((T, Hq + 2 * H, D)).astype(np.float32)).bfloat16()
+
+    new = [37, 5, 60]
+    x = make(sum(new))
+    old = i32([0] * B)
+    got, lse, _ = device_step(x.cuda(), i32(new), old)
+    o_state, c = oracle_step(x, new, o_state)
+    _check_attend(c, got, lse)
+
+    x_static, one = torch.zeros(B, Hq + 2 * H, D, dtype=torch.bfloat16, device="cuda"), i32([1] * B)
+    ws = lib.attend_page8_workspace(B, B, Hq, H, D)
+    side = torch.cuda.Stream()
+    keep = [t.clone() for t in (table, lens, count, kp, vp, ks, vs)]
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):   # warm-up on the side stream, then undone
+        device_step(x_static, one, old, ws)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        g_out = device_step(x_static, one, old, ws)
+    for t, v in zip((table, lens, count, kp, vp, ks, vs), keep):
+        t.copy_(v)
+    for i in range(20):   # crosses page borders
+        x = make(B)
+        x_static.copy_(x.cuda())
+        if i % 2:
+            graph.replay()
+        else:
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                graph.replay()
+            torch.cuda.current_stream().wait_stream(side)
+        o_state, c = oracle_step(x, [1] * B, o_state)
+        assert np.array_equal(lens.cpu().numpy(), o_state[1]) and np.array_equal(table.cpu().numpy(), o_state[0])
+        _check_attend(c, g_out[0], g_out[1])
+    assert int(count) == o_state[2] and int(err) == 0
+
+
+def test_step_entry_points_refuse_other_tensors(lib):
+    c = _attend_case(1, [(1, 20)], 4, 2, 64, 16, "int8", "bf16", False)
+    d = c["dev"]
+    with pytest.raises(TypeError):
+        lib.attend_page8(d["q"].float(), d["kp"], d["vp"], d["ks"], d["vs"], d["table"], d["cu"], d["lens"])
+    with pytest.raises(ValueError):
+        lib.attend_page8(d["q"], d["kp"], d["vp"], d["ks"][:1], d["vs"], d["table"], d["cu"], d["lens"])
+    with pytest.raises(ValueError):
+        lib.attend_page8(d["q"], d["kp"], d["vp"], d["ks"], d["vs"], d["table"].cpu(), d["cu"], d["lens"])
+    with pytest.raises(TypeError):
+        lib.attend_page8(d["q"], d["kp"], d["vp"].view(torch.uint8), d["ks"], d["vs"], d["table"], d["cu"], d["lens"])
+    with pytest.raises(lib.QpkvError):
+        lib.attend_page8(d["q"], d["kp"], d["vp"], d["ks"], d["vs"], d["table"], d["cu"], d["lens"], logit_cap=-1.0)
+    small = torch.empty(16, dtype=torch.uint8, device="cuda")
+    with pytest.raises(lib.QpkvError) as e:
+        lib.attend_page8(d["q"], d["kp"], d["vp"], d["ks"], d["vs"], d["table"], d["cu"], d["lens"], workspace=small)
+    assert e.value.status == 3
+    x = torch.zeros(3, 1, 64, device="cuda")
+    cos, sin = lib.rope_table(1e4, 8, 64)
+    with pytest.raises(ValueError):
+        lib.rope_axes(x, i32([[0, 1]]), bytes(32), cos, sin)
+    with pytest.raises(lib.QpkvError):
+        lib.rope_axes(x, i32([[0, 1, 2]]), bytes([1] * 32), cos, sin)
+    with pytest.raises(ValueError):
+        lib.rope_axes(x, i32([[0, 1, 2]]), bytes(16), cos, sin)
