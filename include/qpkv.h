@@ -755,7 +755,8 @@ qpkv_status qpkv_write_page8(const qpkv_write_page8_params* params, void* stream
  * Errors: INVALID_ARG (null or misaligned pointers, negative sizes, a cap
  * that is negative or not finite), UNSUPPORTED (D not 64 or 128, page_size
  * not a multiple of 16, Hq % Hkv, dtype, format, layout, T * Hq / Hkv or
- * bt_stride * page_size above 2^31 - 65), WORKSPACE_TOO_SMALL, CUDA. */
+ * bt_stride * page_size above 2^31 - 65, num_pages * page_size, times Hkv for
+ * HND, above 2^31 - 1), WORKSPACE_TOO_SMALL, CUDA. */
 typedef struct qpkv_attend_page8_params {
   int32_t num_seqs;      /* B */
   int32_t num_tokens;    /* T */

@@ -814,63 +814,61 @@ def mla_sparse_decode(q, kv_pool, sparse_indices, block_table, seqlens_kv, cu_se
 
 
 # ------------------------------------------- a serving step on the device
+# These calls are short on the GPU, so their host side is kept short too: one
+# look at the current device and stream per call, one combined test per
+# tensor, the parameter structs filled by position (in the order of _fields_).
 
-def _on_current(t, name):
-    """The kernels run on the current device's stream: so must the tensor."""
+def _device_and_stream():
+    """The current device's index and its current stream's raw handle."""
     torch = _torch()
-    if not t.is_cuda:
-        raise ValueError(f"{name} must live on the GPU")
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name} must live on the current device")
+    dev = torch.cuda.current_device()
+    return dev, torch._C._cuda_getCurrentRawStream(dev)
 
 
-def _arr(t, name, dtype, shape):
-    """Data pointer of a contiguous GPU tensor of the given dtype and shape."""
+def _refuse(t, name, dtype, shape, dev):
+    """Why ``t`` is not the tensor that was asked for."""
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
+    if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    _on_current(t, name)
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on the GPU")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must live on the current device")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _arr(t, name, dtype, shape, dev):
+    """Data pointer of a contiguous tensor of the given dtype and shape."""
+    if t.dtype != dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        _refuse(t, name, dtype, shape, dev)
     return t.data_ptr()
 
 
-def _heads(t, name, dtype, T, D=None, H=None):
-    """Data pointer and (token, head) strides of a [T, H, D] GPU tensor whose
-    last dimension is contiguous."""
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[0] != T or (D is not None and t.shape[2] != D) or (
-            H is not None and t.shape[1] != H):
-        raise ValueError(f"{name} must be [{T}, {H or 'H'}, {D or 'D'}], got {list(t.shape)}")
+def _heads(t, name, dtype, shape, dev):
+    """Data pointer and (token, head) strides of a [T, H, D] tensor whose last
+    dimension is contiguous."""
+    if t.dtype != dtype or t.shape != shape or t.get_device() != dev:
+        _refuse(t, name, dtype, shape, dev)
     st, sh, sd = t.stride()
-    if sd != 1 and t.shape[2] > 1:
+    if sd != 1 and shape[2] > 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
-    _on_current(t, name)
     return t.data_ptr(), st, sh
 
 
-def _error_ptr(error_word):
-    return None if error_word is None else _arr(error_word, "error_word", _torch().int32, (1,))
+def _error_ptr(error_word, dev):
+    return None if error_word is None else _arr(error_word, "error_word", _torch().int32, (1,), dev)
 
 
 def _dtype_code(dtype, f32=False):
     torch = _torch()
-    code = {torch.bfloat16: 0, torch.float16: 1}.get(dtype, 2 if f32 and dtype == torch.float32
-                                                     else None)
-    if code is None:
-        raise TypeError(f"unsupported dtype {dtype}")
-    return code
-
-
-def _format_code(pool):
-    torch = _torch()
-    if pool.dtype == torch.uint8:
-        return 0                                    # E4M3 codes
-    if pool.dtype == torch.int8:
+    if dtype == torch.bfloat16:
+        return 0
+    if dtype == torch.float16:
         return 1
-    raise TypeError(f"pools must be uint8 (E4M3) or int8, got {pool.dtype}")
+    if f32 and dtype == torch.float32:
+        return 2
+    raise TypeError(f"unsupported dtype {dtype}")
 
 
 def assign_pages(new_lens, seqlens, block_table, free_pages, free_count, page_size, num_pages,
@@ -889,30 +887,28 @@ def assign_pages(new_lens, seqlens, block_table, free_pages, free_count, page_si
     torch = _torch()
     lib = load()
     i32 = torch.int32
+    dev, stream = _device_and_stream()
     B, W = block_table.shape
-    p = AssignParams(B, num_tokens, page_size, num_pages, W, free_pages.shape[0])
-    p.new_lens = _arr(new_lens, "new_lens", i32, (B,))
-    p.seqlens = _arr(seqlens, "seqlens", i32, (B,))
-    p.block_table = _arr(block_table, "block_table", i32, (B, W))
-    p.free_pages = _arr(free_pages, "free_pages", i32, (free_pages.shape[0],))
-    p.free_count = _arr(free_count, "free_count", i32, (1,))
-    dev = block_table.device
-
-    def out(t, name, shape):
+    F = free_pages.shape[0]
+    ins = (_arr(new_lens, "new_lens", i32, (B,), dev), _arr(seqlens, "seqlens", i32, (B,), dev),
+           _arr(block_table, "block_table", i32, (B, W), dev),
+           _arr(free_pages, "free_pages", i32, (F,), dev),
+           _arr(free_count, "free_count", i32, (1,), dev))
+    outs = [block_table_out, seqlens_out, free_count_out, cu_seqlens, slot_mapping, positions]
+    shapes = ((B, W), (B,), (1,), (B,), (num_tokens,), (num_tokens,))
+    names = ("block_table_out", "seqlens_out", "free_count_out", "cu_seqlens", "slot_mapping",
+             "positions")
+    ptrs = []
+    for i, t in enumerate(outs):
         if t is None:
-            t = torch.empty(shape, dtype=i32, device=dev)
-            return t, t.data_ptr()
-        return t, _arr(t, name, i32, shape)
-
-    block_table_out, p.block_table_out = out(block_table_out, "block_table_out", (B, W))
-    seqlens_out, p.seqlens_out = out(seqlens_out, "seqlens_out", (B,))
-    free_count_out, p.free_count_out = out(free_count_out, "free_count_out", (1,))
-    cu_seqlens, p.cu_seqlens = out(cu_seqlens, "cu_seqlens", (B,))
-    slot_mapping, p.slot_mapping = out(slot_mapping, "slot_mapping", (num_tokens,))
-    positions, p.positions = out(positions, "positions", (num_tokens,))
-    p.error_word = _error_ptr(error_word)
-    _check(lib.qpkv_assign_pages(ctypes.byref(p), _stream()), "qpkv_assign_pages")
-    return block_table_out, seqlens_out, free_count_out, cu_seqlens, slot_mapping, positions
+            outs[i] = t = block_table.new_empty(shapes[i])
+            ptrs.append(t.data_ptr())
+        else:
+            ptrs.append(_arr(t, names[i], i32, shapes[i], dev))
+    p = AssignParams(B, num_tokens, page_size, num_pages, W, F, *ins, *ptrs,
+                     _error_ptr(error_word, dev))
+    _check(lib.qpkv_assign_pages(ctypes.byref(p), stream), "qpkv_assign_pages")
+    return tuple(outs)
 
 
 def axis_sections(sections, interleaved=False):
@@ -948,57 +944,60 @@ def rope_axes(q, positions, pair_axis, rope_cos, rope_sin, k=None, q_out=None, k
     and not written."""
     torch = _torch()
     lib = load()
-    T, Hq, D = q.shape
-    half = len(pair_axis)
-    p = RopeAxesParams()
-    p.num_tokens, p.num_heads_q, p.head_dim, p.rot_dim = T, Hq, D, 2 * half
-    p.dtype = _dtype_code(q.dtype, f32=True)
-    p.inverse = 1 if inverse else 0
-    p.q, p.q_stride_t, p.q_stride_h = _heads(q, "q", q.dtype, T)
+    dev, stream = _device_and_stream()
+    T, Hq, D = shape = q.shape
+    half, dtype = len(pair_axis), q.dtype
+    code = _dtype_code(dtype, f32=True)
+    qp, q_t, q_h = _heads(q, "q", dtype, shape, dev)
     if q_out is None:
-        q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
-    p.q_out, p.q_out_stride_t, p.q_out_stride_h = _heads(q_out, "q_out", q.dtype, T, D, Hq)
+        q_out = q.new_empty(shape)
+    qo, qo_t, qo_h = _heads(q_out, "q_out", dtype, shape, dev)
+    kp = ko = None
+    Hkv = k_t = k_h = ko_t = ko_h = 0
     if k is not None:
-        p.k, p.k_stride_t, p.k_stride_h = _heads(k, "k", q.dtype, T, D)
         Hkv = k.shape[1]
-        p.num_heads_kv = Hkv
+        shape = (T, Hkv, D)
+        kp, k_t, k_h = _heads(k, "k", dtype, shape, dev)
         if k_out is None:
-            k_out = torch.empty((T, Hkv, D), dtype=q.dtype, device=q.device)
-        p.k_out, p.k_out_stride_t, p.k_out_stride_h = _heads(k_out, "k_out", q.dtype, T, D, Hkv)
-    if positions.dtype != torch.int32 or positions.dim() != 2 or positions.shape[1] != T or (
-            T > 1 and positions.stride(1) != 1):
+            k_out = k.new_empty(shape)
+        ko, ko_t, ko_h = _heads(k_out, "k_out", dtype, shape, dev)
+    axes, n = positions.shape
+    axis_stride, step = positions.stride()
+    if positions.dtype != torch.int32 or n != T or (T > 1 and step != 1):
         raise ValueError("positions must be int32 [axes, T], contiguous along T")
-    _on_current(positions, "positions")
-    p.num_axes, p.axis_stride, p.positions = (positions.shape[0], positions.stride(0),
-                                              positions.data_ptr())
-    p.pair_axis = bytes(pair_axis)
-    p.rope_max_pos = rope_cos.shape[0]
-    p.rope_cos = _arr(rope_cos, "rope_cos", torch.float32, (p.rope_max_pos, half))
-    p.rope_sin = _arr(rope_sin, "rope_sin", torch.float32, (p.rope_max_pos, half))
-    p.error_word = _error_ptr(error_word)
-    _check(lib.qpkv_rope_axes(ctypes.byref(p), _stream()), "qpkv_rope_axes")
+    if positions.get_device() != dev:
+        raise ValueError("positions must live on the current device")
+    rows = rope_cos.shape[0]
+    p = RopeAxesParams(
+        T, Hq, Hkv, D, 2 * half, axes, rows, code, 1 if inverse else 0, 0, axis_stride, q_t, q_h,
+        k_t, k_h, qo_t, qo_h, ko_t, ko_h, positions.data_ptr(), bytes(pair_axis),
+        _arr(rope_cos, "rope_cos", torch.float32, (rows, half), dev),
+        _arr(rope_sin, "rope_sin", torch.float32, (rows, half), dev), qp, kp, qo, ko,
+        _error_ptr(error_word, dev))
+    _check(lib.qpkv_rope_axes(ctypes.byref(p), stream), "qpkv_rope_axes")
     return q_out if k is None else (q_out, k_out)
 
 
-def _pools(p, k_pool, v_pool, k_scale, v_scale, block_table, B, kv_layout):
-    """Fill in and check the cache's arguments; returns (Hkv, D)."""
+def _pools(k_pool, v_pool, k_scale, v_scale, block_table, B, kv_layout, dev):
+    """Check the cache's arguments: ((H, D, page size, pages, table stride,
+    format, layout), pointers of the table, pools and scales)."""
     torch = _torch()
-    if kv_layout not in KV_LAYOUTS:
+    layout = KV_LAYOUTS.get(kv_layout)
+    if layout is None:
         raise ValueError("kv_layout must be 'NHD' or 'HND'")
-    p.format = _format_code(k_pool)
-    if kv_layout == "HND":
-        P, H, ps, D = k_pool.shape
+    kind, shape = k_pool.dtype, k_pool.shape
+    if kind != torch.uint8 and kind != torch.int8:
+        raise TypeError(f"pools must be uint8 (E4M3) or int8, got {kind}")
+    if layout:
+        P, H, ps, D = shape
     else:
-        P, ps, H, D = k_pool.shape
-    p.k_pool = _arr(k_pool, "k_pool", k_pool.dtype, k_pool.shape)
-    p.v_pool = _arr(v_pool, "v_pool", k_pool.dtype, k_pool.shape)
-    p.k_scale = _arr(k_scale, "k_scale", torch.float32, (P, H))
-    p.v_scale = _arr(v_scale, "v_scale", torch.float32, (P, H))
-    p.bt_stride = block_table.shape[1]
-    p.block_table = _arr(block_table, "block_table", torch.int32, (B, p.bt_stride))
-    p.num_seqs, p.num_heads_kv, p.head_dim, p.page_size, p.num_pages = B, H, D, ps, P
-    p.kv_layout = KV_LAYOUTS[kv_layout]
-    return H, D
+        P, ps, H, D = shape
+    W = block_table.shape[1]
+    return ((H, D, ps, P, W, 0 if kind == torch.uint8 else 1, layout),
+            (_arr(block_table, "block_table", torch.int32, (B, W), dev),
+             _arr(k_pool, "k_pool", kind, shape, dev), _arr(v_pool, "v_pool", kind, shape, dev),
+             _arr(k_scale, "k_scale", torch.float32, (P, H), dev),
+             _arr(v_scale, "v_scale", torch.float32, (P, H), dev)))
 
 
 def write_cache_page8(k, v, cu_seqlens, block_table, k_pool, v_pool, k_scale, v_scale,
@@ -1010,18 +1009,18 @@ def write_cache_page8(k, v, cu_seqlens, block_table, k_pool, v_pool, k_scale, v_
     codes are rescaled when the new tokens raise its scale."""
     torch = _torch()
     lib = load()
-    T, B = k.shape[0], cu_seqlens.shape[0]
-    p = WritePage8Params()
-    H, D = _pools(p, k_pool, v_pool, k_scale, v_scale, block_table, B, kv_layout)
-    p.num_tokens = T
-    p.dtype = _dtype_code(k.dtype)
-    p.k, p.k_stride_t, p.k_stride_h = _heads(k, "k", k.dtype, T, D, H)
-    p.v, p.v_stride_t, p.v_stride_h = _heads(v, "v", k.dtype, T, D, H)
-    p.cu_seqlens_q = _arr(cu_seqlens, "cu_seqlens", torch.int32, (B,))
-    if start_pos is not None:
-        p.start_pos = _arr(start_pos, "start_pos", torch.int32, (B,))
-    p.error_word = _error_ptr(error_word)
-    _check(lib.qpkv_write_page8(ctypes.byref(p), _stream()), "qpkv_write_page8")
+    dev, stream = _device_and_stream()
+    T, B, dtype = k.shape[0], cu_seqlens.shape[0], k.dtype
+    (H, D, ps, P, W, fmt, layout), (bt, kpool, vpool, ks, vs) = _pools(
+        k_pool, v_pool, k_scale, v_scale, block_table, B, kv_layout, dev)
+    kp, k_t, k_h = _heads(k, "k", dtype, (T, H, D), dev)
+    vp, v_t, v_h = _heads(v, "v", dtype, (T, H, D), dev)
+    p = WritePage8Params(
+        B, T, H, D, ps, P, W, _dtype_code(dtype), fmt, layout, k_t, k_h, v_t, v_h,
+        _arr(cu_seqlens, "cu_seqlens", torch.int32, (B,), dev),
+        None if start_pos is None else _arr(start_pos, "start_pos", torch.int32, (B,), dev),
+        bt, kp, vp, kpool, vpool, ks, vs, _error_ptr(error_word, dev))
+    _check(lib.qpkv_write_page8(ctypes.byref(p), stream), "qpkv_write_page8")
 
 
 def attend_page8_workspace(num_seqs, num_tokens, num_heads_q, num_heads_kv, head_dim,
@@ -1048,34 +1047,36 @@ def attend_page8(q, k_pool, v_pool, k_scale, v_scale, block_table, cu_seqlens_q,
     max_seqlen_q: a bound on the queries of a sequence if known (0: T)."""
     torch = _torch()
     lib = load()
-    T, Hq, D = q.shape
-    B = cu_seqlens_q.shape[0]
-    p = AttendPage8Params()
-    H, Dp = _pools(p, k_pool, v_pool, k_scale, v_scale, block_table, B, kv_layout)
+    i32, f32 = torch.int32, torch.float32
+    dev, stream = _device_and_stream()
+    T, Hq, D = shape = q.shape
+    B, dtype = cu_seqlens_q.shape[0], q.dtype
+    (H, Dp, ps, P, W, fmt, layout), (bt, kpool, vpool, ks, vs) = _pools(
+        k_pool, v_pool, k_scale, v_scale, block_table, B, kv_layout, dev)
     if D != Dp:
         raise ValueError(f"q must be [T, Hq, {Dp}]")
-    p.num_tokens, p.max_seqlen_q, p.num_heads_q = T, max_seqlen_q, Hq
-    p.dtype = _dtype_code(q.dtype)
-    p.causal, p.window = 1 if causal else 0, window
-    p.sm_scale, p.logit_cap = (float(sm_scale) if sm_scale else 0.0), float(logit_cap)
-    p.q = _arr(q, "q", q.dtype, q.shape)
-    p.cu_seqlens_q = _arr(cu_seqlens_q, "cu_seqlens_q", torch.int32, (B,))
-    p.seqlens_kv = _arr(seqlens_kv, "seqlens_kv", torch.int32, (B,))
-    if alibi_slopes is not None:
-        p.alibi_slopes = _arr(alibi_slopes, "alibi_slopes", torch.float32, (Hq,))
-    if prefix_lens is not None:
-        p.prefix_lens = _arr(prefix_lens, "prefix_lens", torch.int32, (B,))
+    qp = _arr(q, "q", dtype, shape, dev)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    p.o = _arr(out, "out", q.dtype, q.shape)
-    if lse is not None:
-        p.lse = _arr(lse, "lse", torch.float32, (T, Hq))
+        out = q.new_empty(shape)
+        op = out.data_ptr()
+    else:
+        op = _arr(out, "out", dtype, shape, dev)
     if workspace is None:
-        n = int(lib.qpkv_attend_page8_workspace_bytes(B, T, Hq, H, D))
+        n = lib.qpkv_attend_page8_workspace_bytes(B, T, Hq, H, D)
         workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
     else:
-        _on_current(workspace, "workspace")
-    p.workspace, p.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    p.error_word = _error_ptr(error_word)
-    _check(lib.qpkv_attend_page8(ctypes.byref(p), _stream()), "qpkv_attend_page8")
+        if workspace.get_device() != dev:
+            raise ValueError("workspace must live on the current device")
+        n = workspace.numel() * workspace.element_size()
+    p = AttendPage8Params(
+        B, T, max_seqlen_q, Hq, H, D, ps, P, W, _dtype_code(dtype), fmt, layout,
+        1 if causal else 0, window, sm_scale if sm_scale else 0.0, logit_cap,
+        _arr(cu_seqlens_q, "cu_seqlens_q", i32, (B,), dev),
+        _arr(seqlens_kv, "seqlens_kv", i32, (B,), dev), bt,
+        None if prefix_lens is None else _arr(prefix_lens, "prefix_lens", i32, (B,), dev),
+        None if alibi_slopes is None else _arr(alibi_slopes, "alibi_slopes", f32, (Hq,), dev),
+        qp, kpool, vpool, ks, vs, op,
+        None if lse is None else _arr(lse, "lse", f32, (T, Hq), dev),
+        workspace.data_ptr(), n, _error_ptr(error_word, dev))
+    _check(lib.qpkv_attend_page8(ctypes.byref(p), stream), "qpkv_attend_page8")
     return out

@@ -118,6 +118,9 @@ qpkv_status qpkv_attend_page8(const qpkv_attend_page8_params* p, void* stream) {
       static_cast<int64_t>(p->num_tokens) * (p->num_heads_q / p->num_heads_kv) > INT32_MAX - 64 ||
       static_cast<int64_t>(p->num_tokens) * p->num_heads_q > 4ll * INT32_MAX)
     return QPKV_ERR_UNSUPPORTED;
+  const int64_t rows = static_cast<int64_t>(p->num_pages) * p->page_size;   // of a pool, as TMA counts them
+  if (rows > (p->kv_layout == QPKV_KV_LAYOUT_HND ? INT32_MAX / p->num_heads_kv : INT32_MAX))
+    return QPKV_ERR_UNSUPPORTED;
   if (p->num_seqs == 0 || p->num_tokens == 0) return QPKV_OK;
   if (p->cu_seqlens_q == nullptr || p->seqlens_kv == nullptr || p->block_table == nullptr ||
       p->q == nullptr || p->k_pool == nullptr || p->v_pool == nullptr || p->k_scale == nullptr ||

@@ -9,20 +9,23 @@
 // Every row's visible keys are one interval: hi_r = at_r + 1 (causal) raised
 // to the prefix length and cut at L, lo_r = at_r + 1 - window.
 //
-// Each cached byte is needed once per 16 query rows and then thrown away, so
-// the kernel is bound by HBM and built to keep loads in flight: warps work
+// Each cached byte is needed once per tile of query rows and then thrown away,
+// so the kernel is bound by HBM and built to keep loads in flight: warps work
 // alone (no block barrier after the start), each streaming groups of 16
-// tokens of one kv head through a ring of its own of cp.async stages.  Every
-// thread copies exactly the bytes it will use, in the order the matrix
-// instruction wants them, so no operand crosses threads:
-//   S = Q K^T    m16n8k16: row = query row, n = token; a thread holds 32 of a
-//                token's dims (16-byte chunks t and t + 4), taken as the k
-//                index in any order that Q follows
-//   O += P V     k = token, n = dim: thread (g, t) holds chunk g of tokens
-//                2t, 2t + 1, 2t + 8, 2t + 9, whose scores it also holds
+// tokens of one kv head through a ring of its own that TMA fills: two lanes
+// issue the K and the V box (16 rows, swizzled) in one instruction.  Measured
+// on the decode batch of 64 requests (537 MB), loads alone: 16-byte cp.async
+// 138 us (4 TB/s whatever the depth), TMA boxes from every warp 82 us (6.7
+// TB/s).  Tokens (and dims)
+// are the 16 rows of m16n8k16 and query rows its 8 columns, so the converted
+// codes serve NB tiles of 8 query rows and 8 rows (most decode) waste nothing:
+//   S^T = K Q^T      a thread holds 16-byte chunks t and t + 4 of tokens g and
+//                    g + 8, whose dims are the k index in an order Q follows
+//   O^T += V^T P^T   thread (g, t) holds chunk g of tokens 2t, 2t + 1, 2t + 8,
+//                    2t + 9; P^T is the transposed S^T (movmatrix)
 // (g = lane / 4, t = lane % 4).  E4M3 and INT8 codes are exact in f16; a bf16
 // query row enters as f16 times a power of two that puts its largest element
-// in [2^14, 2^15), exact for everything within 2^-31 of it.  P is f16 (2^-12
+// in [2^14, 2^15), exact for everything within 2^-31 of it.  P is f16 (2^-11
 // relative); statistics and O are float32.
 //
 // The value scale joins the running maximum: with y = x log2(e) + log2(vs)
@@ -32,11 +35,12 @@
 // largest keep all 11 bits (a value of 448 may meet one of 2^-9).
 //
 // Work is split without a plan, so that lengths may change on the device (and
-// in a captured graph): all (sequence, kv head, 16-row tile, 16-token group)
+// in a captured graph): all (sequence, kv head, row tile, 16-token group)
 // units in a row are cut into equal runs, one per warp.  A run that covers a
 // whole (sequence, head, tile) writes the output; pieces go to the workspace
 // (at most two per warp: the one it begins with and the one it ends with) and
 // the join kernel adds them up in the order of the runs.
+#include <climits>
 #include <type_traits>
 
 #include "common.cuh"
@@ -47,18 +51,17 @@ namespace qpkv {
 namespace {
 
 constexpr int kWarps = 4;               // per block
-constexpr int kBlocksPerSm = 3;
-constexpr int kStages = 4;
 constexpr int kGroup = 16;              // tokens of a unit
 constexpr int kMinRun = 4;              // units of a run at least (64 tokens)
-constexpr uint32_t kBadPageMark = 0x7FFFDEADu;   // in the place of a scale: skip the group
+constexpr uint32_t kBadPageMark = 0x7FFFDEADu;   // in the place of a key scale: skip the group
 
 struct SplitArgs {
   Page8Args p;
-  int workers;
-  int ws_rows;             // rows a piece holds in the workspace (at most 16)
-  float* part_o;           // [2 * workers][ws_rows][D]
-  float2* part_ml;         // [2 * workers][ws_rows] (m, l)
+  int workers;             // warps / side
+  int side;                // kv heads that neighbouring warps take over the same tokens
+  int tile;                // query rows of a tile (8 NB), and of a piece in the workspace
+  float* part_o;           // [2 * workers][tile][D]
+  float2* part_ml;         // [2 * workers][tile] (m, l)
   long long* sched;        // [B + 1] units before each sequence, [B + 1]: run length
 };
 
@@ -67,7 +70,7 @@ struct Span {
   int t0, n, len, g0, ng, nt;
 };
 
-__device__ __forceinline__ Span span_of(const Page8Args& a, int b, int* err) {
+__device__ __forceinline__ Span span_of(const Page8Args& a, int tile, int b, int* err) {
   Span s = {0, 0, 0, 0, 0, 0};
   Rows r = rows_of(a, b, err);
   s.t0 = r.t0;
@@ -78,7 +81,7 @@ __device__ __forceinline__ Span span_of(const Page8Args& a, int b, int* err) {
   if (hi > lo) {
     s.g0 = lo / kGroup;
     s.ng = (hi + kGroup - 1) / kGroup - s.g0;
-    s.nt = (r.n * a.G + 15) / 16;
+    s.nt = (r.n * a.G + tile - 1) / tile;
   }
   return s;
 }
@@ -100,7 +103,7 @@ __device__ __forceinline__ void widen(uint32_t w, uint32_t& lo, uint32_t& hi) {
 }
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -110,47 +113,80 @@ __device__ __forceinline__ float quad_max(float v) {
   v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
   return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
 }
-__device__ __forceinline__ float quad_sum(float v) {
-  v += __shfl_xor_sync(0xffffffffu, v, 1);
-  return v + __shfl_xor_sync(0xffffffffu, v, 2);
+// Over the eight lanes with the same lane % 4.
+__device__ __forceinline__ float col_max(float v) {
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+}
+__device__ __forceinline__ float col_sum(float v) {
+  v += __shfl_xor_sync(0xffffffffu, v, 4);
+  v += __shfl_xor_sync(0xffffffffu, v, 8);
+  return v + __shfl_xor_sync(0xffffffffu, v, 16);
 }
 
-__device__ __forceinline__ void cp_async_8(void* dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+// Transposes an 8 x 8 matrix of 16-bit elements: lane (g, t) gives elements
+// (g, 2t), (g, 2t + 1) and gets (2t, g), (2t + 1, g).
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
-template <int D>
-struct Ring {
-  static constexpr int kK = D / 64;                  // 16-byte chunks of a token a thread copies
-  static constexpr int kVB = D / 8;                  // bytes of a V token a thread copies
+// Blocks per SM and ring stages: more query rows take registers from warps,
+// and the ring gets what shared memory the warps leave.
+template <int D, int NB>
+struct Shape {
+  static constexpr int kBlocks = NB == 1 ? 4 : NB == 2 ? 3 : 2;
+  static constexpr int kStages = NB == 1 ? 3 : NB == 2 ? 4 : 6;
   static constexpr int kStage = 2 * kGroup * D;      // K and V of a group
   static constexpr int kWarpBytes = kStages * kStage;
 };
 
-template <typename E, int D, bool kInt8, bool kCap, bool kBias>
-__global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) attend_split_kernel(const __grid_constant__ SplitArgs sa) {
-  constexpr int KS = D / 16;      // k steps of Q K^T
-  constexpr int NT = D / 8;       // 8-dim tiles of O: thread g's dim i of its chunk
-  constexpr int KC = Ring<D>::kK;
-  constexpr int VB = Ring<D>::kVB;
+struct RowInfo {
+  int lo, hi;         // keys the row sees
+  float sc;           // logit multiplier
+  float slope, at;    // bias: slope * (j - at), log2 units
+};
+
+template <typename E, int D, bool kInt8, bool kCap, bool kBias, int NB>
+__global__ void __launch_bounds__(kWarps * 32, (Shape<D, NB>::kBlocks))
+    attend_split_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+                        const __grid_constant__ SplitArgs sa) {
+  using Sh = Shape<D, NB>;
+  constexpr int kStages = Sh::kStages;
+  constexpr int KS = D / 16;      // k steps of K Q^T
+  constexpr int NT = D / 16;      // 16-dim tiles of O: rows g, g + 8 are dims 2i, 2i + 1 of chunk g
+  constexpr int KC = D / 64;      // 16-byte chunks of a token a thread copies
+  constexpr int VB = D / 8;       // bytes of a V token a thread copies
   constexpr int VW = VB / 4;
-  extern __shared__ __align__(16) uint8_t smem[];
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  __shared__ uint64_t s_full[kWarps][kStages];
   __shared__ long long s_prefix[kWarps * 32 + 1];
-  __shared__ float2 s_scale[kWarps][kStages];
+  __shared__ long long w_sum[kWarps];
+  __shared__ RowInfo s_rows[kWarps][8 * NB];
   const Page8Args& a = sa.p;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
+  if (lane == 0) {
+    for (int s = 0; s < kStages; ++s) mbar_init(&s_full[warp][s], 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&k_map);
+    tma_prefetch_desc(&v_map);
+  }
   griddep_wait();
   griddep_launch_dependents();
 
   // ---- units before each block of `per` sequences
+  const int hgroups = a.Hkv / sa.side;
   const int per = (a.B + kWarps * 32 - 1) / (kWarps * 32);
   {
     const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
     long long mine = 0;
     for (int b = b0; b < b1; ++b) {
-      const Span s = span_of(a, b, blockIdx.x == 0 ? a.err : nullptr);
-      mine += static_cast<long long>(s.ng) * s.nt * a.Hkv;
+      const Span s = span_of(a, 8 * NB, b, blockIdx.x == 0 ? a.err : nullptr);
+      mine += static_cast<long long>(s.ng) * s.nt * hgroups;
     }
     long long inc = mine;
 #pragma unroll
@@ -158,7 +194,6 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) attend_split_kernel
       const long long u = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += u;
     }
-    __shared__ long long w_sum[kWarps];
     if (lane == 31) w_sum[warp] = inc;
     __syncthreads();
     for (int w = 0; w < warp; ++w) inc += w_sum[w];
@@ -174,125 +209,118 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) attend_split_kernel
     long long at = s_prefix[tid];
     for (int b = b0; b < b1; ++b) {
       sa.sched[b] = at;
-      const Span s = span_of(a, b, nullptr);
-      at += static_cast<long long>(s.ng) * s.nt * a.Hkv;
+      const Span s = span_of(a, 8 * NB, b, nullptr);
+      at += static_cast<long long>(s.ng) * s.nt * hgroups;
     }
     if (tid == 0) {
       sa.sched[a.B] = total;
       sa.sched[a.B + 1] = run;
     }
   }
-  const int worker = blockIdx.x * kWarps + warp;
+  const int me = blockIdx.x * kWarps + warp;
+  const int worker = me / sa.side;
   long long u = worker * run;
   const long long u_end = u + run < total ? u + run : total;
   const long long u_begin = u;
   if (u >= u_end) return;
 
-  uint8_t* ring = smem + warp * Ring<D>::kWarpBytes;
+  uint8_t* ring = smem + warp * Sh::kWarpBytes;
+  uint64_t* full = s_full[warp];
+  RowInfo* ri = s_rows[warp];
+  int in_st = 0, out_st = 0;     // ring stages of the next copy and the next use
+  uint32_t out_phase = 0;        // phase of the stage in use
+  // a thread's pieces of a stage, as TMA's swizzle places them
+  const uint32_t ka = D == 128 ? g * 128 + ((t ^ g) << 4) : g * 64 + ((t ^ (g >> 1)) << 4);
+  const uint32_t va = D == 128 ? 2 * t * 128 + (((g ^ (2 * t)) & 7) << 4) : 2 * t * 64 + (((g >> 1) ^ t) << 4) + (g & 1) * 8;
+  const uint32_t vb = D == 128 ? (2 * t + 1) * 128 + (((g ^ (2 * t + 1)) & 7) << 4) : va + 64;
   // the sequence of unit u
-  int blk = 0;
+  int b;
+  long long before;
   {
     int lo = 0, hi = kWarps * 32 - 1;
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
       if (u < s_prefix[mid + 1]) hi = mid; else lo = mid + 1;
     }
-    blk = lo;
+    b = lo * per;
+    before = s_prefix[lo];
   }
-  int b = blk * per;
-  long long before = s_prefix[blk];
-  Span sp = span_of(a, b, nullptr);
+  Span sp = span_of(a, 8 * NB, b, nullptr);
 
   while (u < u_end) {
-    long long in_b = static_cast<long long>(sp.ng) * sp.nt * a.Hkv;
+    long long in_b = static_cast<long long>(sp.ng) * sp.nt * hgroups;
     while (u >= before + in_b) {   // a run may cross into later sequences
       before += in_b;
       ++b;
-      sp = span_of(a, b, nullptr);
-      in_b = static_cast<long long>(sp.ng) * sp.nt * a.Hkv;
+      sp = span_of(a, 8 * NB, b, nullptr);
+      in_b = static_cast<long long>(sp.ng) * sp.nt * hgroups;
     }
     const long long local = u - before;
     const int task = static_cast<int>(local / sp.ng);
     const int first = static_cast<int>(local - static_cast<long long>(task) * sp.ng);
-    const int h = task / sp.nt, rt = task - h * sp.nt;
+    const int hg = task / sp.nt, rt = task - hg * sp.nt, h = hg * sa.side + me % sa.side;
     const int count = static_cast<int>(min(static_cast<long long>(sp.ng - first), u_end - u));
     const bool whole_task = count == sp.ng;
-    const size_t piece = 2 * static_cast<size_t>(worker) + (u == u_begin ? 0 : 1);
+    const size_t piece = 2 * static_cast<size_t>(me) + (u == u_begin ? 0 : 1);
     const int gbeg = sp.g0 + first;
+    const int live_rows = min(8 * NB, sp.n * a.G - rt * 8 * NB);
 
-    // ---- the ring: page ids of 32 groups at a time, one per lane
-    const long long head_off = static_cast<long long>(h) * a.head_stride;
+    // ---- the ring.  Lane l looks up group 32 k + l of the run: its row in the
+    // pools and its two scales, 32 groups at a time.
     const int32_t* bt = a.bt + static_cast<size_t>(b) * a.bt_stride;
     const int gpp = a.ps / kGroup;
-    int ids = -1, in_page = 0;
-    auto lookup = [&](int i0) {   // groups gbeg + i0 + lane
+    const int hc = a.hnd ? 0 : h;
+    int at = -1;                       // first row of the group, -1: a bad page
+    float next_ks = 0.f, next_vs = 0.f;
+    auto lookup = [&](int i0) {
       const int i = i0 + lane;
-      ids = -1;
+      at = -1;
       if (i < count) {
         const int gi = gbeg + i, pg = gi / gpp;
-        in_page = gi - pg * gpp;
-        ids = __ldg(bt + pg);
-        if (ids < 0 || ids >= a.num_pages) {
+        const int page = __ldg(bt + pg);
+        if (page >= 0 && page < a.num_pages) {
+          at = (a.hnd ? page * a.Hkv + h : page) * a.ps + (gi - pg * gpp) * kGroup;
+          const size_t sx = static_cast<size_t>(page) * a.Hkv + h;
+          next_ks = __ldg(a.ks + sx);
+          next_vs = __ldg(a.vs + sx);
+        } else {
           report_error(a.err, kDevErrBadPage);
-          ids = -1;
         }
       }
     };
     auto issue = [&](int i) {
       if (i < count) {
         if ((i & 31) == 0) lookup(i);
-        const int page = __shfl_sync(0xffffffffu, ids, i & 31);
-        const int off = __shfl_sync(0xffffffffu, in_page, i & 31);
-        const int st = i % kStages;
-        uint8_t* dst = ring + st * Ring<D>::kStage;
-        if (page >= 0) {
-          const long long base = page * a.page_stride + static_cast<long long>(off) * kGroup * a.tok_stride + head_off;
-          const uint8_t* kp = a.k + base + g * a.tok_stride + 16 * t;
-#pragma unroll
-          for (int c = 0; c < KC; ++c) {
-            cp_async_16(dst + (2 * c) * 512 + lane * 16, kp + 64 * c);
-            cp_async_16(dst + (2 * c + 1) * 512 + lane * 16, kp + 8 * a.tok_stride + 64 * c);
-          }
-          const uint8_t* vp = a.v + base + 2 * t * a.tok_stride + VB * g;
-          uint8_t* vd = dst + kGroup * D;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const uint8_t* src = vp + ((c & 1) + (c >> 1) * 8) * a.tok_stride;
-            if constexpr (VB == 16) cp_async_16(vd + c * 512 + lane * 16, src);
-            else cp_async_8(vd + c * 256 + lane * 8, src);
-          }
+        const int row = __shfl_sync(0xffffffffu, at, i & 31);
+        if (row >= 0) {
+          if (lane == 0) mbar_arrive_expect_tx(&full[in_st], Sh::kStage);
+          __syncwarp();
           if (lane < 2)
-            cp_async_4(reinterpret_cast<float*>(&s_scale[warp][st]) + lane,
-                       (lane == 0 ? a.ks : a.vs) + static_cast<size_t>(page) * a.Hkv + h);
+            tma_load_3d(ring + in_st * Sh::kStage + lane * (kGroup * D), lane == 0 ? &k_map : &v_map, &full[in_st], 0, hc, row);
+          __syncwarp();
         } else if (lane == 0) {
-          s_scale[warp][st].x = __uint_as_float(kBadPageMark);
+          mbar_arrive(&full[in_st]);   // nothing comes; the stage is skipped
         }
+        in_st = in_st + 1 == kStages ? 0 : in_st + 1;
       }
-      cp_async_commit();
     };
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) issue(i);
 
-    // ---- Q: rows rt * 16 + g and + 8; row r is query r / G, head h * G + r % G
-    Rows rows;
-    rows.t0 = sp.t0, rows.n = sp.n, rows.len = sp.len;
-    rows.prefix = a.prefix != nullptr ? __ldg(a.prefix + b) : 0;
-    uint32_t qf[KS][4];
-    float sc[2], slope[2];
-    int hi[2], lo[2], at[2];
+    // ---- Q: column g of tile nb is row rt * 8 NB + 8 nb + g, query r / G, head h * G + r % G
+    uint32_t qf[NB][KS][2];
+    int all_lo = 0, all_hi = INT_MAX;
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int r = rt * 16 + g + 8 * x;
-      const bool live = r < sp.n * a.G;
-      const int rr = live ? r : sp.n * a.G - 1;       // dead rows: zeros with the last row's limits
+    for (int nb = 0; nb < NB; ++nb) {
+      const int r = 8 * nb + g;
+      const bool live = r < live_rows;
+      const int rr = rt * 8 * NB + (live ? r : live_rows - 1);   // dead rows: zeros with the last row's limits
       const int i = rr / a.G, head = h * a.G + (rr - i * a.G);
-      at[x] = sp.len - sp.n + i;
-      hi[x] = row_hi(a, rows, i);
-      lo[x] = row_lo(a, rows, i);
-      slope[x] = kBias ? __ldg(a.slopes + head) * kLog2e : 0.f;
+      Rows rows;
+      rows.t0 = sp.t0, rows.n = sp.n, rows.len = sp.len;
+      rows.prefix = a.prefix != nullptr ? __ldg(a.prefix + b) : 0;
       const E* src = static_cast<const E*>(a.q) + (static_cast<size_t>(sp.t0 + i) * a.Hq + head) * D;
       uint2 raw[KS];
-      float amax = 0.f;
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
         const int dim = (k < 4 ? 16 * t : 16 * (t + 4)) + 4 * (k & 3);
@@ -301,186 +329,252 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) attend_split_kernel
       float inv = 1.f;
       if constexpr (std::is_same<E, __half>::value) {
 #pragma unroll
-        for (int k = 0; k < KS; ++k) qf[k][x] = raw[k].x, qf[k][2 + x] = raw[k].y;
+        for (int k = 0; k < KS; ++k) qf[nb][k][0] = raw[k].x, qf[nb][k][1] = raw[k].y;
       } else {
-        float f[KS][4];
+        float amax = 0.f;
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
-          f[k][0] = __uint_as_float(raw[k].x << 16), f[k][1] = __uint_as_float(raw[k].x & 0xFFFF0000u);
-          f[k][2] = __uint_as_float(raw[k].y << 16), f[k][3] = __uint_as_float(raw[k].y & 0xFFFF0000u);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fabsf(f[k][e]));
+          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(raw[k].x << 16)), fabsf(__uint_as_float(raw[k].x & 0xFFFF0000u))));
+          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(raw[k].y << 16)), fabsf(__uint_as_float(raw[k].y & 0xFFFF0000u))));
         }
         const float mul = q_to_f16_scale(quad_max(amax), &inv);
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
-          qf[k][x] = f32x2_to_f16x2(f[k][1] * mul, f[k][0] * mul);
-          qf[k][2 + x] = f32x2_to_f16x2(f[k][3] * mul, f[k][2] * mul);
+          qf[nb][k][0] = f32x2_to_f16x2(__uint_as_float(raw[k].x & 0xFFFF0000u) * mul, __uint_as_float(raw[k].x << 16) * mul);
+          qf[nb][k][1] = f32x2_to_f16x2(__uint_as_float(raw[k].y & 0xFFFF0000u) * mul, __uint_as_float(raw[k].y << 16) * mul);
         }
       }
-      sc[x] = inv * (kCap ? a.scale_cap : a.scale_log2);
+      const int hi = row_hi(a, rows, i), lo = row_lo(a, rows, i);
+      all_lo = max(all_lo, lo);
+      all_hi = min(all_hi, hi);
+      if (t == 0) {
+        RowInfo x;
+        x.lo = lo;
+        x.hi = hi;
+        x.sc = inv * (kCap ? a.scale_cap : a.scale_log2);
+        x.slope = kBias ? __ldg(a.slopes + head) * kLog2e : 0.f;
+        x.at = static_cast<float>(sp.len - sp.n + i);
+        ri[r] = x;
+      }
     }
     // keys that every row of the tile sees
-    int all_lo = max(lo[0], lo[1]), all_hi = min(hi[0], hi[1]);
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) {
       all_lo = max(all_lo, __shfl_xor_sync(0xffffffffu, all_lo, o));
       all_hi = min(all_hi, __shfl_xor_sync(0xffffffffu, all_hi, o));
     }
-
-    float O[NT][4];
+    __syncwarp();
+    float sc[NB][2];    // columns 2t, 2t + 1
 #pragma unroll
-    for (int i = 0; i < NT; ++i) O[i][0] = O[i][1] = O[i][2] = O[i][3] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    for (int nb = 0; nb < NB; ++nb) sc[nb][0] = ri[8 * nb + 2 * t].sc, sc[nb][1] = ri[8 * nb + 2 * t + 1].sc;
 
+    float O[NB][NT][4];
+    float m[NB][2], l[NB][2];   // m is 0 until the row has seen a key
+    uint32_t seen = 0;          // bit 2 nb + x: it has
+    bool fresh = true;          // some row has not (the same in all lanes)
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+      for (int i = 0; i < NT; ++i) O[nb][i][0] = O[nb][i][1] = O[nb][i][2] = O[nb][i][3] = 0.f;
+      m[nb][0] = m[nb][1] = 0.f;
+      l[nb][0] = l[nb][1] = 0.f;
+    }
+
+    float blk_ks = 0.f, blk_lv = 0.f, blk_rvs = 1.f;   // of the 32 groups at hand, one per lane
 #pragma unroll 1
     for (int i = 0; i < count; ++i) {
+      if ((i & 31) == 0) {     // before the copies of the next 32 groups are issued
+        const float vs = next_vs == 0.f ? 1.f : fmaxf(next_vs, kMinScale);
+        blk_ks = at >= 0 ? next_ks : __uint_as_float(kBadPageMark);
+        blk_lv = log2f(vs);
+        blk_rvs = 1.f / vs;
+      }
       issue(i + kStages - 1);
-      cp_async_wait_group<kStages - 1>();
-      __syncwarp();                                  // the scales come from lanes 0 and 1
-      const int st = i % kStages;
-      const uint8_t* src = ring + st * Ring<D>::kStage;
-      const float2 kv = s_scale[warp][st];
-      const bool skip = __float_as_uint(kv.x) == kBadPageMark;
-      if (!skip) {
-        float s[2][4] = {};
+      const float ks = __shfl_sync(0xffffffffu, blk_ks, i & 31);
+      const float lv = __shfl_sync(0xffffffffu, blk_lv, i & 31);
+      const float rvs = __shfl_sync(0xffffffffu, blk_rvs, i & 31);
+      if (!mbar_wait(&full[out_st], out_phase)) {
+        if (lane == 0) report_error(a.err, kDevErrTimeout);
+        // the copies still on their way land (or are given up) before the warp ends
+        for (int k = 1; k < kStages && i + k < count; ++k) {
+          out_phase ^= out_st + 1 == kStages;
+          out_st = out_st + 1 == kStages ? 0 : out_st + 1;
+          mbar_wait(&full[out_st], out_phase);
+        }
+        return;
+      }
+      __syncwarp();
+      const uint8_t* src = ring + out_st * Sh::kStage;
+      out_phase ^= out_st + 1 == kStages;
+      out_st = out_st + 1 == kStages ? 0 : out_st + 1;
+      if (__float_as_uint(ks) != kBadPageMark) {
+        uint4 kx[2 * KC];       // chunks t, t + 4 of tokens g, g + 8
+#pragma unroll
+        for (int c = 0; c < 2 * KC; ++c)
+          kx[c] = *reinterpret_cast<const uint4*>(src + (ka ^ ((c >> 1) * 64)) + (c & 1) * 8 * D);
+        float s[NB][4] = {};     // token g: columns 2t, 2t + 1; token g + 8: the same
 #pragma unroll
         for (int c = 0; c < KC; ++c) {
-          const uint4 x0 = *reinterpret_cast<const uint4*>(src + (2 * c) * 512 + lane * 16);
-          const uint4 x1 = *reinterpret_cast<const uint4*>(src + (2 * c + 1) * 512 + lane * 16);
-          const uint32_t w0[4] = {x0.x, x0.y, x0.z, x0.w}, w1[4] = {x1.x, x1.y, x1.z, x1.w};
+          const uint32_t w0[4] = {kx[2 * c].x, kx[2 * c].y, kx[2 * c].z, kx[2 * c].w};
+          const uint32_t w1[4] = {kx[2 * c + 1].x, kx[2 * c + 1].y, kx[2 * c + 1].z, kx[2 * c + 1].w};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            uint32_t b0, b1, d0, d1;
-            widen<kInt8>(w0[k], b0, b1);
-            widen<kInt8>(w1[k], d0, d1);
-            mma16816(s[0], qf[4 * c + k], b0, b1);
-            mma16816(s[1], qf[4 * c + k], d0, d1);
+            uint32_t f[4];
+            widen<kInt8>(w0[k], f[0], f[2]);
+            widen<kInt8>(w1[k], f[1], f[3]);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) mma16816(s[nb], f, qf[nb][4 * c + k][0], qf[nb][4 * c + k][1]);
           }
         }
-        // ---- scores in log2 units, with log2 of the value scale
-        const int j0 = (gbeg + i) * kGroup;
-        const bool whole = j0 >= all_lo && j0 + kGroup <= all_hi;
-        const float vs = fmaxf(kv.y, kMinScale);
-        const float lv = kv.y == 0.f ? 0.f : log2f(vs), rvs = kv.y == 0.f ? 1.f : 1.f / vs;
-        float y[2][4];   // [row][token 2t, 2t+1, 2t+8, 2t+9]
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const float f = sc[x] * kv.x;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float v = s[e >> 1][2 * x + (e & 1)] * f;
-            if constexpr (kCap) v = a.cap_log2 * tanh_of(v);
-            const int j = j0 + 2 * t + (e & 1) + 8 * (e >> 1);
-            if constexpr (kBias) v = fmaf(slope[x], static_cast<float>(j - at[x]), v);
-            v += lv;
-            if (!whole && (j < lo[x] || j >= hi[x])) v = -INFINITY;
-            y[x][e] = v;
-          }
-        }
-        bool up = false;
-        float top[2];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          top[x] = fmaxf(fmaxf(y[x][0], y[x][1]), fmaxf(y[x][2], y[x][3]));
-          up |= top[x] > m[x] + kMaxP;
-        }
-        if (__any_sync(0xffffffffu, up)) {
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const float now = fmaxf(m[x], quad_max(top[x]) - kSetP);
-            const float f = m[x] > -INFINITY ? fast_exp2(m[x] - now) : 0.f;
-            m[x] = now;
-            l[x] *= f;
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              O[n][2 * x] *= f;
-              O[n][2 * x + 1] *= f;
-            }
-          }
-        }
-        uint32_t pf[4];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const float mm = m[x] > -INFINITY ? m[x] : 0.f;
-          const float p0 = fast_exp2(y[x][0] - mm), p1 = fast_exp2(y[x][1] - mm);
-          const float p2 = fast_exp2(y[x][2] - mm), p3 = fast_exp2(y[x][3] - mm);
-          l[x] = fmaf((p0 + p1) + (p2 + p3), rvs, l[x]);
-          pf[x] = f32x2_to_f16x2(p1, p0);
-          pf[2 + x] = f32x2_to_f16x2(p3, p2);
-        }
-        // ---- O += P V
         const uint8_t* vsrc = src + kGroup * D;
         uint32_t vw[4][VW];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
+          const uint8_t* vp = vsrc + (c & 1 ? vb : va) + (c >> 1) * 8 * D;
           if constexpr (VB == 16) {
-            const uint4 x = *reinterpret_cast<const uint4*>(vsrc + c * 512 + lane * 16);
+            const uint4 x = *reinterpret_cast<const uint4*>(vp);
             vw[c][0] = x.x, vw[c][1] = x.y, vw[c][VW - 2] = x.z, vw[c][VW - 1] = x.w;
           } else {
-            const uint2 x = *reinterpret_cast<const uint2*>(vsrc + c * 256 + lane * 8);
+            const uint2 x = *reinterpret_cast<const uint2*>(vp);
             vw[c][0] = x.x, vw[c][1] = x.y;
           }
         }
-        if (!kInt8 && !whole) {   // P = 0 does not cancel a NaN code of a token no row sees
+        // ---- y - m in log2 units, y with log2 of the value scale
+        const int j0 = (gbeg + i) * kGroup;
+        float z[NB][4];
+        bool up = fresh;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int j = j0 + 2 * t + (c & 1) + 8 * (c >> 1);
-            if (j >= sp.len) {
+        for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
-              for (int k = 0; k < VW; ++k) vw[c][k] = 0;
+          for (int x = 0; x < 2; ++x) {
+            const float f = sc[nb][x] * ks, off = lv - m[nb][x];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float& v = z[nb][2 * e + x];
+              v = s[nb][2 * e + x];
+              float o = off;
+              if constexpr (kBias) {
+                const RowInfo& q = ri[8 * nb + 2 * t + x];
+                o = fmaf(q.slope, static_cast<float>(j0 + g + 8 * e) - q.at, o);
+              }
+              if constexpr (kCap) v = fmaf(a.cap_log2, tanh_of(v * f), o);
+              else v = fmaf(v, f, o);
             }
           }
         }
+        if (j0 < all_lo || j0 + kGroup > all_hi) {   // some row does not see some key
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const RowInfo& q = ri[8 * nb + 2 * t + (e & 1)];
+              const int j = j0 + g + 8 * (e >> 1);
+              if (j < q.lo || j >= q.hi) z[nb][e] = -INFINITY;
+            }
+          }
+          if (!kInt8) {   // P = 0 does not cancel a NaN code of a token behind the last
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              if (j0 + 2 * t + (c & 1) + 8 * (c >> 1) >= sp.len) {
+#pragma unroll
+                for (int k = 0; k < VW; ++k) vw[c][k] = 0;
+              }
+            }
+          }
+        }
+        // a row's first key, or one that exceeds the range of P
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+          up |= fmaxf(fmaxf(z[nb][0], z[nb][1]), fmaxf(z[nb][2], z[nb][3])) > kMaxP;
+        if (__any_sync(0xffffffffu, up)) {
+          uint32_t now = 0;
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const bool was = seen >> (2 * nb + x) & 1;
+              // the row's maximum so far lies between m + kSetP and m + kMaxP: m only grows
+              const float top = col_max(fmaxf(z[nb][x], z[nb][2 + x])) - kSetP;
+              const float d = was ? fmaxf(top, 0.f) : top;      // the move of m
+              if (d > -INFINITY) {
+                now |= 1u << (2 * nb + x);
+                m[nb][x] += d;
+                z[nb][x] -= d;
+                z[nb][2 + x] -= d;
+                const float f = was ? fast_exp2(-d) : 0.f;
+                l[nb][x] *= f;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                  O[nb][n][x] *= f;
+                  O[nb][n][2 + x] *= f;
+                }
+              }
+            }
+          }
+          seen |= now;
+          fresh = __any_sync(0xffffffffu, seen != (1u << 2 * NB) - 1);
+        }
+        uint32_t pf[NB][2];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          float p[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) p[e] = fast_exp2(z[nb][e]);
+          l[nb][0] = fmaf(p[0] + p[2], rvs, l[nb][0]);
+          l[nb][1] = fmaf(p[1] + p[3], rvs, l[nb][1]);
+          pf[nb][0] = transpose8(f32x2_to_f16x2(p[1], p[0]));
+          pf[nb][1] = transpose8(f32x2_to_f16x2(p[3], p[2]));
+        }
+        // ---- O^T += V^T P^T
 #pragma unroll
         for (int k = 0; k < VW; ++k) {
-          uint32_t b0[4], b1[4];
-          widen<kInt8>(__byte_perm(vw[0][k], vw[1][k], 0x5140), b0[0], b0[1]);
-          widen<kInt8>(__byte_perm(vw[0][k], vw[1][k], 0x7362), b0[2], b0[3]);
-          widen<kInt8>(__byte_perm(vw[2][k], vw[3][k], 0x5140), b1[0], b1[1]);
-          widen<kInt8>(__byte_perm(vw[2][k], vw[3][k], 0x7362), b1[2], b1[3]);
+          uint32_t f[4], d[4];
+          widen<kInt8>(__byte_perm(vw[0][k], vw[1][k], 0x5140), f[0], f[1]);
+          widen<kInt8>(__byte_perm(vw[2][k], vw[3][k], 0x5140), f[2], f[3]);
+          widen<kInt8>(__byte_perm(vw[0][k], vw[1][k], 0x7362), d[0], d[1]);
+          widen<kInt8>(__byte_perm(vw[2][k], vw[3][k], 0x7362), d[2], d[3]);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) mma16816(O[4 * k + e], pf, b0[e], b1[e]);
+          for (int nb = 0; nb < NB; ++nb) {
+            mma16816(O[nb][2 * k], f, pf[nb][0], pf[nb][1]);
+            mma16816(O[nb][2 * k + 1], d, pf[nb][0], pf[nb][1]);
+          }
         }
       }
       __syncwarp();   // the stage may be filled again
     }
-    cp_async_wait_all();
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        if (!(seen >> (2 * nb + x) & 1)) m[nb][x] = -INFINITY;
 
-    // ---- the run's part of this task: dims [VB * 2t, VB * 2t + 2 VB) of rows g, g + 8
+    // ---- the run's part of this task: dims [VB g, VB g + VB) of columns 2t, 2t + 1
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int r = rt * 16 + g + 8 * x;
-      const float lsum = quad_sum(l[x]);
-      if (r >= sp.n * a.G) continue;
-      if (whole_task) {
-        const int i = r / a.G, head = h * a.G + (r - i * a.G);
-        const size_t row = static_cast<size_t>(sp.t0 + i) * a.Hq + head;
-        const float so = lsum > 0.f ? 1.f / lsum : 0.f;
-        E* out = static_cast<E*>(a.o) + row * D + 2 * VB * t;
+    for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t w[NT / 2];
+      for (int x = 0; x < 2; ++x) {
+        const int r = 8 * nb + 2 * t + x;
+        const float lsum = col_sum(l[nb][x]);
+        if (r >= live_rows) continue;
+        if (whole_task) {
+          const int rr = rt * 8 * NB + r, i = rr / a.G, head = h * a.G + (rr - i * a.G);
+          const size_t row = static_cast<size_t>(sp.t0 + i) * a.Hq + head;
+          const float so = lsum > 0.f ? 1.f / lsum : 0.f;
+          uint32_t w[NT];
+#pragma unroll
+          for (int n = 0; n < NT; ++n) w[n] = pack_out<E>(O[nb][n][2 + x] * so, O[nb][n][x] * so);
+          uint4* out = reinterpret_cast<uint4*>(static_cast<E*>(a.o) + row * D + VB * g);
+#pragma unroll
+          for (int n = 0; n < NT / 4; ++n) out[n] = make_uint4(w[4 * n], w[4 * n + 1], w[4 * n + 2], w[4 * n + 3]);
+          if (g == 0 && a.lse != nullptr)
+            a.lse[row] = lsum > 0.f ? (m[nb][x] + log2f(lsum)) * kLn2 : -INFINITY;
+        } else {
+          float4* out = reinterpret_cast<float4*>(sa.part_o + (piece * (8 * NB) + r) * D + VB * g);
 #pragma unroll
           for (int n = 0; n < NT / 2; ++n)
-            w[n] = pack_out<E>(O[2 * n + 1][2 * x + half] * so, O[2 * n][2 * x + half] * so);
-#pragma unroll
-          for (int n = 0; n < NT / 8; ++n)
-            reinterpret_cast<uint4*>(out + VB * half)[n] = make_uint4(w[4 * n], w[4 * n + 1], w[4 * n + 2], w[4 * n + 3]);
+            out[n] = make_float4(O[nb][2 * n][x], O[nb][2 * n][2 + x], O[nb][2 * n + 1][x], O[nb][2 * n + 1][2 + x]);
+          if (g == 0) sa.part_ml[piece * (8 * NB) + r] = make_float2(m[nb][x], lsum);
         }
-        if (t == 0 && a.lse != nullptr)
-          a.lse[row] = lsum > 0.f ? (m[x] + log2f(lsum)) * kLn2 : -INFINITY;
-      } else {
-        const int pr = g + 8 * x;
-        float* out = sa.part_o + (piece * sa.ws_rows + pr) * D + 2 * VB * t;
-#pragma unroll
-        for (int half = 0; half < 2; ++half)
-#pragma unroll
-          for (int n = 0; n < NT / 4; ++n)
-            reinterpret_cast<float4*>(out + VB * half)[n] =
-                make_float4(O[4 * n][2 * x + half], O[4 * n + 1][2 * x + half], O[4 * n + 2][2 * x + half],
-                            O[4 * n + 3][2 * x + half]);
-        if (t == 0) sa.part_ml[piece * sa.ws_rows + pr] = make_float2(m[x], lsum);
       }
     }
     __syncwarp();
@@ -501,7 +595,7 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
   const int tok = static_cast<int>(w / a.Hq), head = static_cast<int>(w - static_cast<long long>(tok) * a.Hq);
   if (tok >= a.T) return;
   const int b = seq_of_token(a.cu, a.B, tok);
-  const Span sp = span_of(a, b, nullptr);
+  const Span sp = span_of(a, sa.tile, b, nullptr);
   if (sp.n <= 0 || tok < sp.t0 || tok >= sp.t0 + sp.n) return;   // a row behind the last sequence
   const size_t row = static_cast<size_t>(tok) * a.Hq + head;
   float acc[EPL];
@@ -510,13 +604,13 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
   float M = -INFINITY, l = 0.f;
   if (sp.ng > 0) {
     const int h = head / a.G, r = (tok - sp.t0) * a.G + (head - h * a.G);
-    const long long u0 = sa.sched[b] + (static_cast<long long>(h) * sp.nt + r / 16) * sp.ng, u1 = u0 + sp.ng;
+    const long long u0 = sa.sched[b] + (static_cast<long long>(h / sa.side) * sp.nt + r / sa.tile) * sp.ng, u1 = u0 + sp.ng;
     const long long run = sa.sched[a.B + 1];
     const int w0 = static_cast<int>(u0 / run), w1 = static_cast<int>((u1 - 1) / run);
     if (w0 == w1) return;   // written whole by its run
-    const int pr = r & 15;
+    const int pr = r % sa.tile;
     auto piece = [&](int k) {
-      return (2 * static_cast<size_t>(k) + (k == w0 && u0 != k * run ? 1 : 0)) * sa.ws_rows + pr;
+      return (2 * (static_cast<size_t>(k) * sa.side + h % sa.side) + (k == w0 && u0 != k * run ? 1 : 0)) * sa.tile + pr;
     };
     for (int k = w0 + lane; k <= w1; k += 32) M = fmaxf(M, sa.part_ml[piece(k)].x);
     M = warp_max(M);
@@ -547,8 +641,8 @@ int sm_count() {
   return sms;
 }
 
-template <typename K>
-cudaError_t launch(K kernel, unsigned grid, unsigned threads, size_t smem, const SplitArgs& a, cudaStream_t stream) {
+template <typename... P, typename... A>
+cudaError_t launch(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, cudaStream_t stream, const A&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(threads);
@@ -559,51 +653,73 @@ cudaError_t launch(K kernel, unsigned grid, unsigned threads, size_t smem, const
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Query tiles of 8: as many as the rows of a (sequence, kv head) need, up to 3.
+int tiles_for(int T, int max_q, int G) {
+  const long long rows = static_cast<long long>(max_q > 0 && max_q < T ? max_q : T) * G;
+  return rows <= 8 ? 1 : rows <= 16 ? 2 : 3;
+}
+
+template <typename E, int D, bool kInt8, bool kCap, bool kBias, int NB>
+cudaError_t go(SplitArgs& a, int sms, cudaStream_t s) {
+  using Sh = Shape<D, NB>;
+  constexpr size_t smem = kWarps * Sh::kWarpBytes + 1024;
+  auto kernel = attend_split_kernel<E, D, kInt8, kCap, kBias, NB>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  const unsigned blocks = static_cast<unsigned>(sms * Sh::kBlocks);
+  a.workers = static_cast<int>(blocks) * kWarps / a.side;   // side divides kWarps * 2, blocks is even
+  CUtensorMap km, vm;
+  if (!pool_map(a.p, D, a.p.k, kGroup, &km) || !pool_map(a.p, D, a.p.v, kGroup, &vm)) return cudaErrorInvalidValue;
+  if ((e = launch(kernel, blocks, kWarps * 32, smem, s, km, vm, a)) != cudaSuccess) return e;
+  const long long warps = static_cast<long long>(a.p.T) * a.p.Hq;
+  return launch(attend_join_kernel<E, D>, static_cast<unsigned>((warps + 3) / 4), 128, 0, s, a);
 }
 
 template <typename E, int D, bool kInt8, bool kCap, bool kBias>
-cudaError_t go(const SplitArgs& a, unsigned blocks, cudaStream_t s) {
-  constexpr size_t smem = kWarps * Ring<D>::kWarpBytes;
-  auto kernel = attend_split_kernel<E, D, kInt8, kCap, kBias>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  if (e != cudaSuccess) return e;
-  if ((e = launch(kernel, blocks, kWarps * 32, smem, a, s)) != cudaSuccess) return e;
-  const long long warps = static_cast<long long>(a.p.T) * a.p.Hq;
-  return launch(attend_join_kernel<E, D>, static_cast<unsigned>((warps + 3) / 4), 128, 0, a, s);
+cudaError_t pick3(SplitArgs& a, int sms, cudaStream_t s) {
+  switch (a.tile / 8) {
+    case 1: return go<E, D, kInt8, kCap, kBias, 1>(a, sms, s);
+    case 2: return go<E, D, kInt8, kCap, kBias, 2>(a, sms, s);
+    default: return go<E, D, kInt8, kCap, kBias, 3>(a, sms, s);
+  }
 }
 
 template <typename E, int D, bool kInt8>
-cudaError_t pick2(const SplitArgs& a, unsigned blocks, cudaStream_t s) {
+cudaError_t pick2(SplitArgs& a, int sms, cudaStream_t s) {
   const bool cap = a.p.cap_log2 > 0.f, bias = a.p.slopes != nullptr;
-  if (cap) return bias ? go<E, D, kInt8, true, true>(a, blocks, s) : go<E, D, kInt8, true, false>(a, blocks, s);
-  return bias ? go<E, D, kInt8, false, true>(a, blocks, s) : go<E, D, kInt8, false, false>(a, blocks, s);
+  if (cap) return bias ? pick3<E, D, kInt8, true, true>(a, sms, s) : pick3<E, D, kInt8, true, false>(a, sms, s);
+  return bias ? pick3<E, D, kInt8, false, true>(a, sms, s) : pick3<E, D, kInt8, false, false>(a, sms, s);
 }
 
 template <typename E>
-cudaError_t pick(const SplitArgs& a, int D, bool int8, unsigned blocks, cudaStream_t s) {
-  if (D == 64) return int8 ? pick2<E, 64, true>(a, blocks, s) : pick2<E, 64, false>(a, blocks, s);
-  return int8 ? pick2<E, 128, true>(a, blocks, s) : pick2<E, 128, false>(a, blocks, s);
+cudaError_t pick(SplitArgs& a, int D, bool int8, int sms, cudaStream_t s) {
+  if (D == 64) return int8 ? pick2<E, 64, true>(a, sms, s) : pick2<E, 64, false>(a, sms, s);
+  return int8 ? pick2<E, 128, true>(a, sms, s) : pick2<E, 128, false>(a, sms, s);
 }
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
-// Rows of a piece and the three arrays' sizes.
-void sizes(int B, int T, int Hq, int Hkv, int D, int workers, int* rows, size_t* o, size_t* ml, size_t* sched) {
-  const long long most = static_cast<long long>(T) * (Hq / Hkv);
-  *rows = most < 16 ? static_cast<int>(most) : 16;
-  *o = up256(static_cast<size_t>(2) * workers * *rows * D * sizeof(float));
-  *ml = up256(static_cast<size_t>(2) * workers * *rows * sizeof(float2));
+// The workspace's three arrays: pieces of O, their (m, l), the split.
+void sizes(int B, int D, int tile, int workers, size_t* o, size_t* ml, size_t* sched) {
+  *o = up256(static_cast<size_t>(2) * workers * tile * D * sizeof(float));
+  *ml = up256(static_cast<size_t>(2) * workers * tile * sizeof(float2));
   *sched = up256((static_cast<size_t>(B) + 2) * sizeof(long long));
 }
 
 }  // namespace
 
 size_t attend_page8_workspace_bytes(int B, int T, int Hq, int Hkv, int D) {
-  int rows;
-  size_t o, ml, sched;
-  sizes(B, T, Hq, Hkv, D, kAttendMaxSms * kBlocksPerSm * kWarps, &rows, &o, &ml, &sched);
-  return o + ml + sched;
+  size_t most = 0;
+  for (int nb = 1; nb <= tiles_for(T, T, Hq / Hkv); ++nb) {   // whatever max_seqlen_q will be
+    size_t o, ml, sched;
+    const int blocks = nb == 1 ? Shape<128, 1>::kBlocks : nb == 2 ? Shape<128, 2>::kBlocks : Shape<128, 3>::kBlocks;
+    sizes(B, D, 8 * nb, kAttendMaxSms * blocks * kWarps, &o, &ml, &sched);
+    most = o + ml + sched > most ? o + ml + sched : most;
+  }
+  return most;
 }
 
 cudaError_t launch_attend_page8(const qpkv_attend_page8_params& p, cudaStream_t stream) {
@@ -611,17 +727,19 @@ cudaError_t launch_attend_page8(const qpkv_attend_page8_params& p, cudaStream_t 
   a.p = page8_args(p);
   int sms = sm_count();
   if (sms > kAttendMaxSms) sms = kAttendMaxSms;
-  const unsigned blocks = static_cast<unsigned>(sms) * kBlocksPerSm;
-  a.workers = static_cast<int>(blocks) * kWarps;
+  sms -= sms & 1;   // an even number of blocks
+  a.side = a.p.Hkv % 8 == 0 ? 8 : a.p.Hkv % 4 == 0 ? 4 : a.p.Hkv % 2 == 0 ? 2 : 1;
+  a.tile = 8 * tiles_for(p.num_tokens, p.max_seqlen_q, a.p.G);
   size_t o, ml, sched;
-  sizes(p.num_seqs, p.num_tokens, p.num_heads_q, p.num_heads_kv, p.head_dim, a.workers, &a.ws_rows, &o, &ml, &sched);
+  const int blocks = a.tile == 8 ? Shape<128, 1>::kBlocks : a.tile == 16 ? Shape<128, 2>::kBlocks : Shape<128, 3>::kBlocks;
+  sizes(p.num_seqs, p.head_dim, a.tile, sms * blocks * kWarps, &o, &ml, &sched);
   uint8_t* ws = static_cast<uint8_t*>(p.workspace);
   a.part_o = reinterpret_cast<float*>(ws);
   a.part_ml = reinterpret_cast<float2*>(ws + o);
   a.sched = reinterpret_cast<long long*>(ws + o + ml);
   const bool int8 = p.format == QPKV_FORMAT_INT8;
-  return p.dtype == QPKV_DTYPE_F16 ? pick<__half>(a, p.head_dim, int8, blocks, stream)
-                                   : pick<__nv_bfloat16>(a, p.head_dim, int8, blocks, stream);
+  return p.dtype == QPKV_DTYPE_F16 ? pick<__half>(a, p.head_dim, int8, sms, stream)
+                                   : pick<__nv_bfloat16>(a, p.head_dim, int8, sms, stream);
 }
 
 }  // namespace qpkv

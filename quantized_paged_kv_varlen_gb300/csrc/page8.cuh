@@ -16,11 +16,10 @@ constexpr float kSetP = 7.0f, kMaxP = 15.0f;
 constexpr float kMinScale = 7.888609e-31f;   // 2^-100
 
 struct Page8Args {
-  int B, T, Hq, Hkv, G, ps, num_pages, bt_stride, causal, window;
+  int B, T, Hq, Hkv, G, ps, num_pages, bt_stride, causal, window, hnd;
   float scale_log2;        // softmax scale * log2(e)
   float scale_cap;         // softmax scale / cap
   float cap_log2;          // cap * log2(e), 0: no cap
-  long long page_stride, tok_stride, head_stride;   // bytes (8-bit codes)
   const int32_t *cu, *lens, *bt, *prefix;
   const float *slopes, *ks, *vs;
   const void* q;
@@ -41,17 +40,25 @@ inline Page8Args page8_args(const qpkv_attend_page8_params& p) {
   a.scale_log2 = scale * kLog2e;
   a.scale_cap = p.logit_cap > 0.f ? scale / p.logit_cap : 0.f;
   a.cap_log2 = p.logit_cap > 0.f ? p.logit_cap * kLog2e : 0.f;
-  const long long D = p.head_dim;
-  const bool hnd = p.kv_layout == QPKV_KV_LAYOUT_HND;
-  a.page_stride = static_cast<long long>(p.page_size) * p.num_heads_kv * D;
-  a.tok_stride = hnd ? D : p.num_heads_kv * D;
-  a.head_stride = hnd ? p.page_size * D : D;
+  a.hnd = p.kv_layout == QPKV_KV_LAYOUT_HND;
   a.cu = p.cu_seqlens_q, a.lens = p.seqlens_kv, a.bt = p.block_table, a.prefix = p.prefix_lens;
   a.slopes = p.alibi_slopes, a.ks = p.k_scale, a.vs = p.v_scale;
   a.q = p.q;
   a.k = static_cast<const uint8_t*>(p.k_pool), a.v = static_cast<const uint8_t*>(p.v_pool);
   a.o = p.o, a.lse = p.lse, a.err = p.error_word;
   return a;
+}
+
+// A pool for TMA: rows of D codes, boxes of `rows` tokens of one head.  NHD:
+// coordinates (0, head, page * ps + token); HND: (0, 0, (page * Hkv + head) * ps
+// + token).  Rows are 64 or 128 bytes wide and swizzled by as much.
+inline bool pool_map(const Page8Args& a, int D, const void* pool, uint32_t rows, CUtensorMap* map) {
+  const uint64_t d = static_cast<uint64_t>(D), heads = a.hnd ? 1 : a.Hkv;
+  const uint64_t dims[3] = {d, heads, static_cast<uint64_t>(a.num_pages) * a.ps * (a.hnd ? a.Hkv : 1)};
+  const uint64_t strides[2] = {d, heads * d};
+  const uint32_t box[3] = {static_cast<uint32_t>(D), 1u, rows};
+  return encode_tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(pool), dims, strides, box,
+                           D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B) == CUDA_SUCCESS;
 }
 
 // Query rows [t0, t0 + n) of a sequence and its cached tokens.
