@@ -55,6 +55,15 @@ constexpr int kGroup = 16;              // tokens of a unit
 constexpr int kMinRun = 4;              // units of a run at least (64 tokens)
 constexpr uint32_t kBadPageMark = 0x7FFFDEADu;   // in the place of a key scale: skip the group
 
+// What the join kernel needs to know of a query token: one load instead of a
+// search through the lengths, which was half of that kernel's time.
+struct alignas(16) TokenInfo {
+  long long u0;     // first unit of its sequence
+  long long run;
+  int ng, nt, r0;   // units of a task (-1: no sequence has the token), tiles, first row
+  int pad;
+};
+
 struct SplitArgs {
   Page8Args p;
   int workers;             // warps / side
@@ -62,7 +71,7 @@ struct SplitArgs {
   int tile;                // query rows of a tile (8 NB), and of a piece in the workspace
   float* part_o;           // [2 * workers][tile][D]
   float2* part_ml;         // [2 * workers][tile] (m, l)
-  long long* sched;        // [B + 1] units before each sequence, [B + 1]: run length
+  struct TokenInfo* info;  // [T]
 };
 
 // Units of sequence b: groups [g0, g0 + ng) for each of nt row tiles and Hkv heads.
@@ -138,7 +147,7 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 template <int D, int NB>
 struct Shape {
   static constexpr int kBlocks = NB == 1 ? 4 : NB == 2 ? 3 : 2;
-  static constexpr int kStages = NB == 1 ? 3 : NB == 2 ? 4 : 6;
+  static constexpr int kStages = NB == 1 ? 2 : NB == 2 ? 4 : 6;
   static constexpr int kStage = 2 * kGroup * D;      // K and V of a group
   static constexpr int kWarpBytes = kStages * kStage;
 };
@@ -175,8 +184,9 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<D, NB>::kBlocks))
     tma_prefetch_desc(&k_map);
     tma_prefetch_desc(&v_map);
   }
+  // No early launch of the dependents: join blocks that wait on an SM kept
+  // blocks of this kernel's next launch off it (107 us a call against 95).
   griddep_wait();
-  griddep_launch_dependents();
 
   // ---- units before each block of `per` sequences
   const int hgroups = a.Hkv / sa.side;
@@ -204,18 +214,21 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<D, NB>::kBlocks))
   const long long total = s_prefix[kWarps * 32];
   long long run = (total + sa.workers - 1) / sa.workers;
   run = run < kMinRun ? kMinRun : run;
-  if (blockIdx.x == 0) {   // what the join kernel needs to know of the split
-    const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
-    long long at = s_prefix[tid];
-    for (int b = b0; b < b1; ++b) {
-      sa.sched[b] = at;
-      const Span s = span_of(a, 8 * NB, b, nullptr);
-      at += static_cast<long long>(s.ng) * s.nt * hgroups;
+  for (int tok = blockIdx.x + gridDim.x * tid; tok < a.T; tok += gridDim.x * kWarps * 32) {
+    const int b = seq_of_token(a.cu, a.B, tok);
+    const Span s = span_of(a, 8 * NB, b, nullptr);
+    TokenInfo x;
+    x.u0 = s_prefix[b / per];
+    for (int c = b / per * per; c < b; ++c) {
+      const Span y = span_of(a, 8 * NB, c, nullptr);
+      x.u0 += static_cast<long long>(y.ng) * y.nt * hgroups;
     }
-    if (tid == 0) {
-      sa.sched[a.B] = total;
-      sa.sched[a.B + 1] = run;
-    }
+    x.run = run;
+    x.ng = s.n > 0 && tok >= s.t0 && tok < s.t0 + s.n ? s.ng : -1;
+    x.nt = s.nt;
+    x.r0 = (tok - s.t0) * a.G;
+    x.pad = 0;
+    sa.info[tok] = x;
   }
   const int me = blockIdx.x * kWarps + warp;
   const int worker = me / sa.side;
@@ -262,7 +275,9 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<D, NB>::kBlocks))
     const int count = static_cast<int>(min(static_cast<long long>(sp.ng - first), u_end - u));
     const bool whole_task = count == sp.ng;
     const size_t piece = 2 * static_cast<size_t>(me) + (u == u_begin ? 0 : 1);
-    const int gbeg = sp.g0 + first;
+    // from the newest group back: with a distance bias the scores then fall, and
+    // the running maximum is set once instead of moving with every group
+    const int glast = sp.g0 + first + count - 1;
     const int live_rows = min(8 * NB, sp.n * a.G - rt * 8 * NB);
 
     // ---- the ring.  Lane l looks up group 32 k + l of the run: its row in the
@@ -276,7 +291,7 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<D, NB>::kBlocks))
       const int i = i0 + lane;
       at = -1;
       if (i < count) {
-        const int gi = gbeg + i, pg = gi / gpp;
+        const int gi = glast - i, pg = gi / gpp;
         const int page = __ldg(bt + pg);
         if (page >= 0 && page < a.num_pages) {
           at = (a.hnd ? page * a.Hkv + h : page) * a.ps + (gi - pg * gpp) * kGroup;
@@ -440,7 +455,7 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<D, NB>::kBlocks))
           }
         }
         // ---- y - m in log2 units, y with log2 of the value scale
-        const int j0 = (gbeg + i) * kGroup;
+        const int j0 = (glast - i) * kGroup;
         float z[NB][4];
         bool up = fresh;
 #pragma unroll
@@ -582,51 +597,70 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<D, NB>::kBlocks))
   }
 }
 
-// One warp per (token, head): adds up the pieces of its task in the order of
-// the runs, and gives rows that see no key their zeros.
-template <typename E, int D>
-__global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant__ SplitArgs sa) {
+// Adds up the pieces of a (token, head) in the order of the runs, and gives
+// rows that see no key their zeros.  kPer warps share a row: a long context is
+// cut into hundreds of pieces when there are few rows (2 requests of 115k
+// tokens: one warp per row took 41 us).
+template <typename E, int D, int kPer>
+__global__ void __launch_bounds__(kPer > 8 ? 32 * kPer : 256) attend_join_kernel(const __grid_constant__ SplitArgs sa) {
   constexpr int EPL = D / 32;
+  constexpr int kAll = kPer > 8 ? kPer : 8;   // warps of the block
+  __shared__ float s_o[kAll][D];
+  __shared__ float s_l[kAll];
   const Page8Args& a = sa.p;
   griddep_wait();
-  griddep_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const long long w = (blockIdx.x * static_cast<long long>(blockDim.x) + threadIdx.x) >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % kPer;
+  const long long w = blockIdx.x * static_cast<long long>(kAll / kPer) + warp / kPer;
   const int tok = static_cast<int>(w / a.Hq), head = static_cast<int>(w - static_cast<long long>(tok) * a.Hq);
-  if (tok >= a.T) return;
-  const int b = seq_of_token(a.cu, a.B, tok);
-  const Span sp = span_of(a, sa.tile, b, nullptr);
-  if (sp.n <= 0 || tok < sp.t0 || tok >= sp.t0 + sp.n) return;   // a row behind the last sequence
-  const size_t row = static_cast<size_t>(tok) * a.Hq + head;
+  TokenInfo x;
+  x.ng = -1;
+  if (tok < a.T) x = sa.info[tok];
   float acc[EPL];
 #pragma unroll
   for (int e = 0; e < EPL; ++e) acc[e] = 0.f;
   float M = -INFINITY, l = 0.f;
-  if (sp.ng > 0) {
-    const int h = head / a.G, r = (tok - sp.t0) * a.G + (head - h * a.G);
-    const long long u0 = sa.sched[b] + (static_cast<long long>(h / sa.side) * sp.nt + r / sa.tile) * sp.ng, u1 = u0 + sp.ng;
-    const long long run = sa.sched[a.B + 1];
-    const int w0 = static_cast<int>(u0 / run), w1 = static_cast<int>((u1 - 1) / run);
-    if (w0 == w1) return;   // written whole by its run
-    const int pr = r % sa.tile;
-    auto piece = [&](int k) {
-      return (2 * (static_cast<size_t>(k) * sa.side + h % sa.side) + (k == w0 && u0 != k * run ? 1 : 0)) * sa.tile + pr;
-    };
-    for (int k = w0 + lane; k <= w1; k += 32) M = fmaxf(M, sa.part_ml[piece(k)].x);
-    M = warp_max(M);
-    if (M > -INFINITY) {
+  bool write = x.ng == 0;        // no key; x.ng < 0: a row behind the last sequence
+  if (x.ng > 0) {
+    const int h = head / a.G, r = x.r0 + (head - h * a.G);
+    const long long u0 = x.u0 + (static_cast<long long>(h / sa.side) * x.nt + r / sa.tile) * x.ng, u1 = u0 + x.ng;
+    const int w0 = static_cast<int>(u0 / x.run), w1 = static_cast<int>((u1 - 1) / x.run);
+    write = w0 != w1;            // else written whole by its run
+    if (write) {
+      const int pr = r % sa.tile;
+      auto piece = [&](int k) {
+        return (2 * (static_cast<size_t>(k) * sa.side + h % sa.side) + (k == w0 && u0 != k * x.run ? 1 : 0)) * sa.tile + pr;
+      };
+      for (int k = w0 + lane; k <= w1; k += 32) M = fmaxf(M, sa.part_ml[piece(k)].x);
+      M = warp_max(M);
+      if (M > -INFINITY) {
 #pragma unroll 4
-      for (int k = w0; k <= w1; ++k) {
-        const size_t at = piece(k);
-        const float2 ml = sa.part_ml[at];
-        const float f = fast_exp2(ml.x - M);   // a piece that saw nothing: m = -inf, f = 0
-        l = fmaf(ml.y, f, l);
-        const float* src = sa.part_o + at * D + lane * EPL;
+        for (int k = w0 + part; k <= w1; k += kPer) {
+          const size_t at = piece(k);
+          const float2 ml = sa.part_ml[at];
+          const float f = fast_exp2(ml.x - M);   // a piece that saw nothing: m = -inf, f = 0
+          l = fmaf(ml.y, f, l);
+          const float* src = sa.part_o + at * D + lane * EPL;
 #pragma unroll
-        for (int e = 0; e < EPL; ++e) acc[e] = fmaf(src[e], f, acc[e]);
+          for (int e = 0; e < EPL; ++e) acc[e] = fmaf(src[e], f, acc[e]);
+        }
       }
     }
   }
+  if constexpr (kPer > 1) {
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) s_o[warp][lane * EPL + e] = acc[e];
+    if (lane == 0) s_l[warp] = l;
+    __syncthreads();
+    if (part != 0) return;
+#pragma unroll
+    for (int k = 1; k < kPer; ++k) {
+      l += s_l[warp + k];
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) acc[e] += s_o[warp + k][lane * EPL + e];
+    }
+  }
+  if (!write) return;
+  const size_t row = static_cast<size_t>(tok) * a.Hq + head;
   const float so = l > 0.f ? 1.f / l : 0.f;
   E* out = static_cast<E*>(a.o) + row * D + lane * EPL;
 #pragma unroll
@@ -674,8 +708,12 @@ cudaError_t go(SplitArgs& a, int sms, cudaStream_t s) {
   CUtensorMap km, vm;
   if (!pool_map(a.p, D, a.p.k, kGroup, &km) || !pool_map(a.p, D, a.p.v, kGroup, &vm)) return cudaErrorInvalidValue;
   if ((e = launch(kernel, blocks, kWarps * 32, smem, s, km, vm, a)) != cudaSuccess) return e;
-  const long long warps = static_cast<long long>(a.p.T) * a.p.Hq;
-  return launch(attend_join_kernel<E, D>, static_cast<unsigned>((warps + 3) / 4), 128, 0, s, a);
+  // warps per row of the join: as many as leave each scheduler eight at most
+  const long long rows = static_cast<long long>(a.p.T) * a.p.Hq;
+  if (rows <= sms) return launch(attend_join_kernel<E, D, 16>, static_cast<unsigned>(rows), 512, 0, s, a);
+  if (rows <= sms * 4ll) return launch(attend_join_kernel<E, D, 8>, static_cast<unsigned>(rows), 256, 0, s, a);
+  if (rows <= sms * 64ll) return launch(attend_join_kernel<E, D, 2>, static_cast<unsigned>((rows + 3) / 4), 256, 0, s, a);
+  return launch(attend_join_kernel<E, D, 1>, static_cast<unsigned>((rows + 7) / 8), 256, 0, s, a);
 }
 
 template <typename E, int D, bool kInt8, bool kCap, bool kBias>
@@ -702,11 +740,11 @@ cudaError_t pick(SplitArgs& a, int D, bool int8, int sms, cudaStream_t s) {
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
-// The workspace's three arrays: pieces of O, their (m, l), the split.
-void sizes(int B, int D, int tile, int workers, size_t* o, size_t* ml, size_t* sched) {
+// The workspace's three arrays: pieces of O, their (m, l), the tokens' places.
+void sizes(int T, int D, int tile, int workers, size_t* o, size_t* ml, size_t* info) {
   *o = up256(static_cast<size_t>(2) * workers * tile * D * sizeof(float));
   *ml = up256(static_cast<size_t>(2) * workers * tile * sizeof(float2));
-  *sched = up256((static_cast<size_t>(B) + 2) * sizeof(long long));
+  *info = up256(static_cast<size_t>(T) * sizeof(TokenInfo));
 }
 
 }  // namespace
@@ -714,10 +752,10 @@ void sizes(int B, int D, int tile, int workers, size_t* o, size_t* ml, size_t* s
 size_t attend_page8_workspace_bytes(int B, int T, int Hq, int Hkv, int D) {
   size_t most = 0;
   for (int nb = 1; nb <= tiles_for(T, T, Hq / Hkv); ++nb) {   // whatever max_seqlen_q will be
-    size_t o, ml, sched;
+    size_t o, ml, info;
     const int blocks = nb == 1 ? Shape<128, 1>::kBlocks : nb == 2 ? Shape<128, 2>::kBlocks : Shape<128, 3>::kBlocks;
-    sizes(B, D, 8 * nb, kAttendMaxSms * blocks * kWarps, &o, &ml, &sched);
-    most = o + ml + sched > most ? o + ml + sched : most;
+    sizes(T, D, 8 * nb, kAttendMaxSms * blocks * kWarps, &o, &ml, &info);
+    most = o + ml + info > most ? o + ml + info : most;
   }
   return most;
 }
@@ -730,13 +768,13 @@ cudaError_t launch_attend_page8(const qpkv_attend_page8_params& p, cudaStream_t 
   sms -= sms & 1;   // an even number of blocks
   a.side = a.p.Hkv % 8 == 0 ? 8 : a.p.Hkv % 4 == 0 ? 4 : a.p.Hkv % 2 == 0 ? 2 : 1;
   a.tile = 8 * tiles_for(p.num_tokens, p.max_seqlen_q, a.p.G);
-  size_t o, ml, sched;
+  size_t o, ml, info;
   const int blocks = a.tile == 8 ? Shape<128, 1>::kBlocks : a.tile == 16 ? Shape<128, 2>::kBlocks : Shape<128, 3>::kBlocks;
-  sizes(p.num_seqs, p.head_dim, a.tile, sms * blocks * kWarps, &o, &ml, &sched);
+  sizes(p.num_tokens, p.head_dim, a.tile, sms * blocks * kWarps, &o, &ml, &info);
   uint8_t* ws = static_cast<uint8_t*>(p.workspace);
   a.part_o = reinterpret_cast<float*>(ws);
   a.part_ml = reinterpret_cast<float2*>(ws + o);
-  a.sched = reinterpret_cast<long long*>(ws + o + ml);
+  a.info = reinterpret_cast<TokenInfo*>(ws + o + ml);
   const bool int8 = p.format == QPKV_FORMAT_INT8;
   return p.dtype == QPKV_DTYPE_F16 ? pick<__half>(a, p.head_dim, int8, sms, stream)
                                    : pick<__nv_bfloat16>(a, p.head_dim, int8, sms, stream);
