@@ -55,15 +55,6 @@ constexpr int kGroup = 16;              // tokens of a unit
 constexpr int kMinRun = 4;              // units of a run at least (64 tokens)
 constexpr uint32_t kBadPageMark = 0x7FFFDEADu;   // in the place of a key scale: skip the group
 
-// What the join kernel needs to know of a query token: one load instead of a
-// search through the lengths, which was half of that kernel's time.
-struct alignas(16) TokenInfo {
-  long long u0;     // first unit of its sequence
-  long long run;
-  int ng, nt, r0;   // units of a task (-1: no sequence has the token), tiles, first row
-  int pad;
-};
-
 struct SplitArgs {
   Page8Args p;
   int workers;             // warps / side
@@ -71,7 +62,7 @@ struct SplitArgs {
   int tile;                // query rows of a tile (8 NB), and of a piece in the workspace
   float* part_o;           // [2 * workers][tile][D]
   float2* part_ml;         // [2 * workers][tile] (m, l)
-  struct TokenInfo* info;  // [T]
+  TokenInfo* info;         // [T]
 };
 
 // Units of sequence b: groups [g0, g0 + ng) for each of nt row tiles and Hkv heads.
@@ -85,7 +76,7 @@ __device__ __forceinline__ Span span_of(const Page8Args& a, int tile, int b, int
   s.t0 = r.t0;
   s.n = r.n;
   s.len = r.len;
-  if (r.n <= 0) return s;
+  if (r.n <= 0 || r.n * a.G > a.split_rows) return s;   // none, or in tiles of 128
   const int hi = row_hi(a, r, r.n - 1), lo = row_lo(a, r, 0);
   if (hi > lo) {
     s.g0 = lo / kGroup;
@@ -93,22 +84,6 @@ __device__ __forceinline__ Span span_of(const Page8Args& a, int tile, int b, int
     s.nt = (r.n * a.G + tile - 1) / tile;
   }
   return s;
-}
-
-template <bool kInt8>
-__device__ __forceinline__ void widen(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  if constexpr (kInt8) {
-    // 1024 + (code + 128) as f16 by its bits, minus 1152: exact
-    const uint32_t u = w ^ 0x80808080u;
-    const __half2 c = __floats2half2_rn(1152.f, 1152.f);
-    uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
-    __half2 x = __hsub2(*reinterpret_cast<__half2*>(&a), c), y = __hsub2(*reinterpret_cast<__half2*>(&b), c);
-    lo = *reinterpret_cast<uint32_t*>(&x);
-    hi = *reinterpret_cast<uint32_t*>(&y);
-  } else {
-    lo = e4m3x2_to_f16x2(static_cast<uint16_t>(w & 0xFFFFu));
-    hi = e4m3x2_to_f16x2(static_cast<uint16_t>(w >> 16));
-  }
 }
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -217,6 +192,7 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<D, NB>::kBlocks))
   for (int tok = blockIdx.x + gridDim.x * tid; tok < a.T; tok += gridDim.x * kWarps * 32) {
     const int b = seq_of_token(a.cu, a.B, tok);
     const Span s = span_of(a, 8 * NB, b, nullptr);
+    if (s.n * a.G > a.split_rows) continue;   // the tiled form's
     TokenInfo x;
     x.u0 = s_prefix[b / per];
     for (int c = b / per * per; c < b; ++c) {
@@ -225,9 +201,10 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<D, NB>::kBlocks))
     }
     x.run = run;
     x.ng = s.n > 0 && tok >= s.t0 && tok < s.t0 + s.n ? s.ng : -1;
+    x.stride = s.ng;
     x.nt = s.nt;
     x.r0 = (tok - s.t0) * a.G;
-    x.pad = 0;
+    x.kind = 0;
     sa.info[tok] = x;
   }
   const int me = blockIdx.x * kWarps + warp;
@@ -600,73 +577,105 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<D, NB>::kBlocks))
 // Adds up the pieces of a (token, head) in the order of the runs, and gives
 // rows that see no key their zeros.  kPer warps share a row: a long context is
 // cut into hundreds of pieces when there are few rows (2 requests of 115k
-// tokens: one warp per row took 41 us).
+// tokens: one warp per row took 41 us).  With kPer = 1, for many rows, a warp
+// takes 32 heads of a token, of which few have pieces.
+struct JoinArgs {
+  int T, Hq, G;
+  const TokenInfo* info;
+  struct {
+    const float* o;
+    const float2* ml;
+    int tile, side;
+  } set[2];          // by TokenInfo::kind
+  void* o;
+  float* lse;
+};
+
 template <typename E, int D, int kPer>
-__global__ void __launch_bounds__(kPer > 8 ? 32 * kPer : 256) attend_join_kernel(const __grid_constant__ SplitArgs sa) {
+__global__ void __launch_bounds__(kPer > 8 ? 32 * kPer : 256) attend_join_kernel(const __grid_constant__ JoinArgs a) {
   constexpr int EPL = D / 32;
   constexpr int kAll = kPer > 8 ? kPer : 8;   // warps of the block
   __shared__ float s_o[kAll][D];
   __shared__ float s_l[kAll];
-  const Page8Args& a = sa.p;
   griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % kPer;
   const long long w = blockIdx.x * static_cast<long long>(kAll / kPer) + warp / kPer;
-  const int tok = static_cast<int>(w / a.Hq), head = static_cast<int>(w - static_cast<long long>(tok) * a.Hq);
+  const int heads = kPer == 1 ? 32 : 1;
+  const int per_tok = (a.Hq + heads - 1) / heads;
+  const int tok = static_cast<int>(w / per_tok), head0 = static_cast<int>(w - static_cast<long long>(tok) * per_tok) * heads;
   TokenInfo x;
   x.ng = -1;
-  if (tok < a.T) x = sa.info[tok];
-  float acc[EPL];
+  if (tok < a.T) x = a.info[tok];
+  // the runs of this lane's head (all lanes the same with heads = 1)
+  int w0 = 0, w1 = 0, cut = 0;
+  const int my = head0 + (heads > 1 ? lane : 0);
+  if (x.ng > 0 && my < a.Hq) {
+    const int tile = a.set[x.kind].tile, side = a.set[x.kind].side;
+    const int h = my / a.G, r = x.r0 + (my - h * a.G);
+    const long long u0 = x.u0 + (static_cast<long long>(h / side) * x.nt + r / tile) * x.stride;
+    w0 = static_cast<int>(u0 / x.run);
+    w1 = static_cast<int>((u0 + x.ng - 1) / x.run);
+    cut = u0 != w0 * x.run;
+  }
+  // x.ng < 0: a row behind the last sequence; w0 = w1: written whole by its run
+  uint32_t todo = __ballot_sync(0xffffffffu, my < a.Hq && (x.ng == 0 || (x.ng > 0 && w0 != w1)));
+  if (heads == 1) todo &= 1u;
+  while (kPer > 1 || todo != 0) {
+    const int from = kPer > 1 ? 0 : __ffs(todo) - 1;
+    const bool write = todo != 0;
+    const int head = head0 + (heads > 1 ? from : 0);
+    const int k0 = __shfl_sync(0xffffffffu, w0, from), k1 = __shfl_sync(0xffffffffu, w1, from);
+    const int k_cut = __shfl_sync(0xffffffffu, cut, from);
+    todo &= todo - 1;
+    float acc[EPL];
 #pragma unroll
-  for (int e = 0; e < EPL; ++e) acc[e] = 0.f;
-  float M = -INFINITY, l = 0.f;
-  bool write = x.ng == 0;        // no key; x.ng < 0: a row behind the last sequence
-  if (x.ng > 0) {
-    const int h = head / a.G, r = x.r0 + (head - h * a.G);
-    const long long u0 = x.u0 + (static_cast<long long>(h / sa.side) * x.nt + r / sa.tile) * x.ng, u1 = u0 + x.ng;
-    const int w0 = static_cast<int>(u0 / x.run), w1 = static_cast<int>((u1 - 1) / x.run);
-    write = w0 != w1;            // else written whole by its run
-    if (write) {
-      const int pr = r % sa.tile;
+    for (int e = 0; e < EPL; ++e) acc[e] = 0.f;
+    float M = -INFINITY, l = 0.f;
+    if (write && x.ng > 0) {
+      const auto& set = a.set[x.kind];
+      const int h = head / a.G, r = x.r0 + (head - h * a.G), pr = r % set.tile;
       auto piece = [&](int k) {
-        return (2 * (static_cast<size_t>(k) * sa.side + h % sa.side) + (k == w0 && u0 != k * x.run ? 1 : 0)) * sa.tile + pr;
+        return (2 * (static_cast<size_t>(k) * set.side + h % set.side) + (k == k0 ? k_cut : 0)) * set.tile + pr;
       };
-      for (int k = w0 + lane; k <= w1; k += 32) M = fmaxf(M, sa.part_ml[piece(k)].x);
+      for (int k = k0 + lane; k <= k1; k += 32) M = fmaxf(M, set.ml[piece(k)].x);
       M = warp_max(M);
       if (M > -INFINITY) {
 #pragma unroll 4
-        for (int k = w0 + part; k <= w1; k += kPer) {
+        for (int k = k0 + part; k <= k1; k += kPer) {
           const size_t at = piece(k);
-          const float2 ml = sa.part_ml[at];
+          const float2 ml = set.ml[at];
           const float f = fast_exp2(ml.x - M);   // a piece that saw nothing: m = -inf, f = 0
           l = fmaf(ml.y, f, l);
-          const float* src = sa.part_o + at * D + lane * EPL;
+          const float* src = set.o + at * D + lane * EPL;
 #pragma unroll
           for (int e = 0; e < EPL; ++e) acc[e] = fmaf(src[e], f, acc[e]);
         }
       }
     }
-  }
-  if constexpr (kPer > 1) {
+    if constexpr (kPer > 1) {
 #pragma unroll
-    for (int e = 0; e < EPL; ++e) s_o[warp][lane * EPL + e] = acc[e];
-    if (lane == 0) s_l[warp] = l;
-    __syncthreads();
-    if (part != 0) return;
+      for (int e = 0; e < EPL; ++e) s_o[warp][lane * EPL + e] = acc[e];
+      if (lane == 0) s_l[warp] = l;
+      __syncthreads();
+      if (part != 0) return;
 #pragma unroll
-    for (int k = 1; k < kPer; ++k) {
-      l += s_l[warp + k];
+      for (int k = 1; k < kPer; ++k) {
+        l += s_l[warp + k];
 #pragma unroll
-      for (int e = 0; e < EPL; ++e) acc[e] += s_o[warp + k][lane * EPL + e];
+        for (int e = 0; e < EPL; ++e) acc[e] += s_o[warp + k][lane * EPL + e];
+      }
     }
-  }
-  if (!write) return;
-  const size_t row = static_cast<size_t>(tok) * a.Hq + head;
-  const float so = l > 0.f ? 1.f / l : 0.f;
-  E* out = static_cast<E*>(a.o) + row * D + lane * EPL;
+    if (write) {
+      const size_t row = static_cast<size_t>(tok) * a.Hq + head;
+      const float so = l > 0.f ? 1.f / l : 0.f;
+      E* out = static_cast<E*>(a.o) + row * D + lane * EPL;
 #pragma unroll
-  for (int e = 0; e < EPL; e += 2)
-    *reinterpret_cast<uint32_t*>(out + e) = pack_out<E>(acc[e + 1] * so, acc[e] * so);
-  if (lane == 0 && a.lse != nullptr) a.lse[row] = l > 0.f ? (M + log2f(l)) * kLn2 : -INFINITY;
+      for (int e = 0; e < EPL; e += 2)
+        *reinterpret_cast<uint32_t*>(out + e) = pack_out<E>(acc[e + 1] * so, acc[e] * so);
+      if (lane == 0 && a.lse != nullptr) a.lse[row] = l > 0.f ? (M + log2f(l)) * kLn2 : -INFINITY;
+    }
+    if (kPer > 1) return;
+  }
 }
 
 int sm_count() {
@@ -690,12 +699,6 @@ cudaError_t launch(void (*kernel)(P...), unsigned grid, unsigned threads, size_t
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// Query tiles of 8: as many as the rows of a (sequence, kv head) need, up to 3.
-int tiles_for(int T, int max_q, int G) {
-  const long long rows = static_cast<long long>(max_q > 0 && max_q < T ? max_q : T) * G;
-  return rows <= 8 ? 1 : rows <= 16 ? 2 : 3;
-}
-
 template <typename E, int D, bool kInt8, bool kCap, bool kBias, int NB>
 cudaError_t go(SplitArgs& a, int sms, cudaStream_t s) {
   using Sh = Shape<D, NB>;
@@ -707,13 +710,7 @@ cudaError_t go(SplitArgs& a, int sms, cudaStream_t s) {
   a.workers = static_cast<int>(blocks) * kWarps / a.side;   // side divides kWarps * 2, blocks is even
   CUtensorMap km, vm;
   if (!pool_map(a.p, D, a.p.k, kGroup, &km) || !pool_map(a.p, D, a.p.v, kGroup, &vm)) return cudaErrorInvalidValue;
-  if ((e = launch(kernel, blocks, kWarps * 32, smem, s, km, vm, a)) != cudaSuccess) return e;
-  // warps per row of the join: as many as leave each scheduler eight at most
-  const long long rows = static_cast<long long>(a.p.T) * a.p.Hq;
-  if (rows <= sms) return launch(attend_join_kernel<E, D, 16>, static_cast<unsigned>(rows), 512, 0, s, a);
-  if (rows <= sms * 4ll) return launch(attend_join_kernel<E, D, 8>, static_cast<unsigned>(rows), 256, 0, s, a);
-  if (rows <= sms * 64ll) return launch(attend_join_kernel<E, D, 2>, static_cast<unsigned>((rows + 3) / 4), 256, 0, s, a);
-  return launch(attend_join_kernel<E, D, 1>, static_cast<unsigned>((rows + 7) / 8), 256, 0, s, a);
+  return launch(kernel, blocks, kWarps * 32, smem, s, km, vm, a);
 }
 
 template <typename E, int D, bool kInt8, bool kCap, bool kBias>
@@ -738,26 +735,74 @@ cudaError_t pick(SplitArgs& a, int D, bool int8, int sms, cudaStream_t s) {
   return int8 ? pick2<E, 128, true>(a, sms, s) : pick2<E, 128, false>(a, sms, s);
 }
 
+template <typename E, int D>
+cudaError_t join(const JoinArgs& a, int sms, cudaStream_t s) {
+  // warps per row: as many as leave each scheduler eight at most
+  const long long rows = static_cast<long long>(a.T) * a.Hq;
+  if (rows <= sms) return launch(attend_join_kernel<E, D, 16>, static_cast<unsigned>(rows), 512, 0, s, a);
+  if (rows <= sms * 4ll) return launch(attend_join_kernel<E, D, 8>, static_cast<unsigned>(rows), 256, 0, s, a);
+  if (rows <= sms * 64ll) return launch(attend_join_kernel<E, D, 2>, static_cast<unsigned>((rows + 3) / 4), 256, 0, s, a);
+  const long long warps = static_cast<long long>(a.T) * ((a.Hq + 31) / 32);
+  return launch(attend_join_kernel<E, D, 1>, static_cast<unsigned>((warps + 7) / 8), 256, 0, s, a);
+}
+
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
-// The workspace's three arrays: pieces of O, their (m, l), the tokens' places.
-void sizes(int T, int D, int tile, int workers, size_t* o, size_t* ml, size_t* info) {
-  *o = up256(static_cast<size_t>(2) * workers * tile * D * sizeof(float));
-  *ml = up256(static_cast<size_t>(2) * workers * tile * sizeof(float2));
-  *info = up256(static_cast<size_t>(T) * sizeof(TokenInfo));
+// Which forms a call needs, by sizes the host knows: the split form takes up
+// to kSplitRows query rows of a (sequence, kv head); with a bound on a
+// sequence's queries above that the tiled form takes the larger ones, and all
+// of them when there is one sequence.
+constexpr int kSplitRows = 24;
+struct Plan {
+  bool split, tiled;
+  int tile, split_rows;
+};
+Plan plan_for(int B, int T, int max_q, int G) {
+  Plan p;
+  const long long rows = static_cast<long long>(max_q > 0 && max_q < T ? max_q : T) * G;
+  p.tiled = rows > kSplitRows && G <= 128;
+  p.split = !p.tiled || B > 1;
+  p.tile = 8 * (rows <= 8 ? 1 : rows <= 16 ? 2 : 3);
+  p.split_rows = !p.tiled ? INT_MAX : p.split ? kSplitRows : -1;
+  return p;
+}
+
+// The workspace's arrays: the tokens' places, pieces of O and (m, l) of the
+// split form, the same of the tiled one.
+struct Sizes {
+  size_t info, o, ml, to, tml;
+  size_t total() const { return info + o + ml + to + tml; }
+};
+Sizes sizes(const Plan& p, int T, int D, int sms) {
+  Sizes s = {};
+  s.info = up256(static_cast<size_t>(T) * sizeof(TokenInfo));
+  if (p.split) {
+    const int blocks = p.tile == 8 ? Shape<128, 1>::kBlocks : p.tile == 16 ? Shape<128, 2>::kBlocks : Shape<128, 3>::kBlocks;
+    const size_t rows = static_cast<size_t>(2) * sms * blocks * kWarps * p.tile;
+    s.o = up256(rows * D * sizeof(float));
+    s.ml = up256(rows * sizeof(float2));
+  }
+  if (p.tiled) {
+    const size_t rows = static_cast<size_t>(2) * sms * 256;
+    s.to = up256(rows * D * sizeof(float));
+    s.tml = up256(rows * sizeof(float2));
+  }
+  return s;
 }
 
 }  // namespace
 
 size_t attend_page8_workspace_bytes(int B, int T, int Hq, int Hkv, int D) {
+  // whatever max_seqlen_q will be
   size_t most = 0;
-  for (int nb = 1; nb <= tiles_for(T, T, Hq / Hkv); ++nb) {   // whatever max_seqlen_q will be
-    size_t o, ml, info;
-    const int blocks = nb == 1 ? Shape<128, 1>::kBlocks : nb == 2 ? Shape<128, 2>::kBlocks : Shape<128, 3>::kBlocks;
-    sizes(T, D, 8 * nb, kAttendMaxSms * blocks * kWarps, &o, &ml, &info);
-    most = o + ml + info > most ? o + ml + info : most;
+  const int G = Hq / Hkv;
+  for (int q = 1; ; q = q * 2 < T ? q * 2 : T) {
+    const size_t n = sizes(plan_for(B, T, q, G), T, D, kAttendMaxSms).total();
+    most = n > most ? n : most;
+    if (q >= T || static_cast<long long>(q) * G > 2 * kSplitRows) break;
   }
-  return most;
+  const size_t n = sizes(plan_for(B, T, T, G), T, D, kAttendMaxSms).total();
+  return n > most ? n : most;
 }
 
 cudaError_t launch_attend_page8(const qpkv_attend_page8_params& p, cudaStream_t stream) {
@@ -765,19 +810,37 @@ cudaError_t launch_attend_page8(const qpkv_attend_page8_params& p, cudaStream_t 
   a.p = page8_args(p);
   int sms = sm_count();
   if (sms > kAttendMaxSms) sms = kAttendMaxSms;
-  sms -= sms & 1;   // an even number of blocks
+  const Plan plan = plan_for(p.num_seqs, p.num_tokens, p.max_seqlen_q, a.p.G);
+  a.p.split_rows = plan.split_rows;
   a.side = a.p.Hkv % 8 == 0 ? 8 : a.p.Hkv % 4 == 0 ? 4 : a.p.Hkv % 2 == 0 ? 2 : 1;
-  a.tile = 8 * tiles_for(p.num_tokens, p.max_seqlen_q, a.p.G);
-  size_t o, ml, info;
-  const int blocks = a.tile == 8 ? Shape<128, 1>::kBlocks : a.tile == 16 ? Shape<128, 2>::kBlocks : Shape<128, 3>::kBlocks;
-  sizes(p.num_tokens, p.head_dim, a.tile, sms * blocks * kWarps, &o, &ml, &info);
+  a.tile = plan.tile;
+  const Sizes sz = sizes(plan, p.num_tokens, p.head_dim, sms);
   uint8_t* ws = static_cast<uint8_t*>(p.workspace);
-  a.part_o = reinterpret_cast<float*>(ws);
-  a.part_ml = reinterpret_cast<float2*>(ws + o);
-  a.info = reinterpret_cast<TokenInfo*>(ws + o + ml);
-  const bool int8 = p.format == QPKV_FORMAT_INT8;
-  return p.dtype == QPKV_DTYPE_F16 ? pick<__half>(a, p.head_dim, int8, sms, stream)
-                                   : pick<__nv_bfloat16>(a, p.head_dim, int8, sms, stream);
+  a.info = reinterpret_cast<TokenInfo*>(ws);
+  a.part_o = reinterpret_cast<float*>(ws + sz.info);
+  a.part_ml = reinterpret_cast<float2*>(ws + sz.info + sz.o);
+  TileArgs t;
+  t.p = a.p;
+  t.tq = a.p.G <= 128 ? 128 / a.p.G : 1;
+  t.info = a.info;
+  t.part_o = reinterpret_cast<float*>(ws + sz.info + sz.o + sz.ml);
+  t.part_ml = reinterpret_cast<float2*>(ws + sz.info + sz.o + sz.ml + sz.to);
+  const bool int8 = p.format == QPKV_FORMAT_INT8, f16 = p.dtype == QPKV_DTYPE_F16;
+  cudaError_t e = cudaSuccess;
+  if (plan.split) {
+    const int even = sms - (sms & 1);   // an even number of blocks
+    e = f16 ? pick<__half>(a, p.head_dim, int8, even, stream) : pick<__nv_bfloat16>(a, p.head_dim, int8, even, stream);
+  }
+  if (e == cudaSuccess && plan.tiled) e = launch_attend_tiles(t, p.head_dim, int8, f16, sms, stream);
+  if (e != cudaSuccess) return e;
+  JoinArgs j;
+  j.T = p.num_tokens, j.Hq = p.num_heads_q, j.G = a.p.G;
+  j.info = a.info;
+  j.set[0] = {a.part_o, a.part_ml, a.tile, a.side};
+  j.set[1] = {t.part_o, t.part_ml, 256, 1};
+  j.o = p.o, j.lse = p.lse;
+  if (f16) return p.head_dim == 64 ? join<__half, 64>(j, sms, stream) : join<__half, 128>(j, sms, stream);
+  return p.head_dim == 64 ? join<__nv_bfloat16, 64>(j, sms, stream) : join<__nv_bfloat16, 128>(j, sms, stream);
 }
 
 }  // namespace qpkv

@@ -1,0 +1,881 @@
+// Attention over the page-scaled 8-bit cache (attend_page8.cu has the
+// formulas): the tiled form for many query rows, on the 5th-generation tensor
+// cores.
+//
+// Rows of a (sequence, kv head) are its queries times the G query heads that
+// share the kv head.  A tile is 128 rows of TQ = 128 / G whole queries; an
+// item is a pair of tiles A and B, run side by side over one stream of
+// 128-key tiles: while one tile's softmax computes its exponentials the tensor
+// core works on the other, and each K/V tile is fetched and widened once for
+// both.  One persistent CTA per SM, 14 warps:
+//   warps 0-3   loads: K and V codes come straight from the pages into
+//               registers one key tile ahead (16 bytes a lane, whole rows) and
+//               go widened to f16 (exact) into the operand layouts; the
+//               item's queries as f16 (bf16 rows times a power of two)
+//   warps 4-7   softmax and epilogue of tile A, one thread per row
+//   warps 8-11  the same for tile B
+//   warp 12     one thread issues tcgen05.mma: per key tile g
+//                 PV_A(g-1) QK_A(g) PV_B(g-1) QK_B(g)
+//   warp 13     walks the work: writes for every step what the others need (the
+//               item, the pages' rows, the scales) into a ring of four
+// (With the walk in every role the registers spilled, into an L1 that shared
+// memory leaves 20 KB: 3.3 ms for a prompt of 8192, 32 heads.)
+// TMEM: S_A, S_B, O_A, O_B, 128 columns each; a tile's f16 P overwrites the
+// first half of its S.  The MMAs run in issue order, so QK_X(g+1) overwrites
+// S_X only after PV_X(g) has read P_X(g), and the commit behind QK_X(g+1) says
+// that PV_X(g) is done before O_X may be rescaled.
+//
+// The softmax reads S once: P = 2^(y - m) with the m at hand (see kSetP,
+// kMaxP), and only when some y of 32 columns exceeds the range are m, O, the
+// sums and this tile's earlier columns of P rescaled.  A row that has not seen
+// a key gets its m from a pass of its own.  Key tiles go from the newest back,
+// so that with a distance bias the first tile has the maximum.
+//
+// Work is split without a plan, as in the other form: all (item, kv head, key
+// tile) units in a row are cut into equal runs, one per CTA; a run's first and
+// last piece may be partial and go to the workspace for the join kernel.  Each
+// (item, kv head) counts kOverhead units more than its key tiles, for its
+// queries' load and its results' store (a causal prompt begins with many items
+// of one key tile).
+#include <climits>
+
+#include "common.cuh"
+#include "internal.h"
+#include "page8.cuh"
+
+namespace qpkv {
+namespace {
+
+constexpr int kT = 128;
+constexpr int kWarps = 14, kThreads = kWarps * 32;
+constexpr int kSoftA = 4, kSoftB = 8, kMma = 12, kWalk = 13;
+constexpr int kLoad = 128;                    // threads of the load warps
+constexpr int kHalf = kT * 128;               // 16 KB: 128 rows of 64 f16
+constexpr uint32_t kColS = 0, kColO = 256;
+constexpr uint32_t kBadPageMark = 0x7FFFDEADu;   // in the place of a key scale: skip the group
+constexpr int kSteps = 4;                     // ring of steps
+constexpr int kOverhead = 2;
+
+// One step of the CTA: a key tile of one (item, kv head).
+enum : int { kFirst = 1, kLast = 2, kHasB = 4, kWholeTask = 8, kEnd = 16 };
+struct Step {
+  float4 sc[8];       // per 16 keys: ks, log2 vs, 1 / vs
+  int at[8];          // per 16 keys: first pool row, -1: no keys
+  int flags;
+  int j0;             // first key
+  int seg;            // segments (runs of steps of one (item, kv head)) before this one
+  int t0, n, len, prefix;   // the sequence (Rows)
+  int h, i0;          // kv head, first query of the item
+  int piece;          // of the workspace, when the segment is not the whole task
+};
+
+template <int D>
+struct Smem {
+  static constexpr int kOp = D / 64 * kHalf;  // one operand tile
+  static constexpr int kQ = 0, kK = 2 * kOp, kV = 4 * kOp;
+  static constexpr int kBytes = 6 * kOp + 1024;
+};
+
+struct Shared {
+  uint64_t q_full, q_free;
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t s_full[2], p_ready[2], o_full[2];  // per tile A / B
+  uint64_t mma_done;
+  uint64_t step_full[kSteps], step_free[kSteps];
+  Step step[kSteps];
+  float qsc[2][2][kT];                        // [segment parity][tile][row] logit multiplier
+  long long seq_prefix[kThreads + 1];         // items before each thread's sequences
+  long long unit_prefix[kThreads + 1];        // units before each thread's items
+  long long w_sum[kWarps];
+  uint32_t tmem_base;
+  int abort;
+};
+
+__device__ __forceinline__ bool await(uint64_t* bar, uint32_t parity, Shared& sh, int* err) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (*reinterpret_cast<volatile int*>(&sh.abort)) return false;
+    if (clock64() - t0 > kWaitTimeoutCycles) {
+      sh.abort = 1;
+      report_error(err, kDevErrTimeout);
+      return false;
+    }
+  }
+}
+
+// 16 bytes that are used once: past L1, and issued where it is written.
+__device__ __forceinline__ uint4 load_stream(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+// All lanes wait, and go on converged.  (One lane polling and a shuffle of the
+// outcome is slower: a shuffle takes ~230 cycles beside the other warps' polls.)
+__device__ __forceinline__ bool warp_await(uint64_t* bar, uint32_t parity, Shared& sh, int* err) {
+  const bool ok = await(bar, parity, sh, err);
+  __syncwarp();
+  return ok;
+}
+
+// Items of a sequence: pairs of tiles, none for one that the split form takes.
+__device__ __forceinline__ int items_of(const TileArgs& a, const Rows& r) {
+  if (r.n <= 0 || r.n * a.p.G <= a.p.split_rows) return 0;
+  return (r.n + 2 * a.tq - 1) / (2 * a.tq);
+}
+
+// Key tiles [k0, k0 + n) that some row of item p sees.
+__device__ __forceinline__ int key_tiles(const TileArgs& a, const Rows& r, int p, int* k0) {
+  const int i0 = p * 2 * a.tq, i1 = min(r.n, i0 + 2 * a.tq) - 1;
+  const int lo = row_lo(a.p, r, i0), hi = row_hi(a.p, r, i1);
+  *k0 = lo / kT;
+  return hi > lo ? (hi - 1) / kT - lo / kT + 1 : 0;
+}
+__device__ __forceinline__ int units_of(int key_tiles) { return key_tiles > 0 ? key_tiles + kOverhead : 0; }
+
+// A position in the list of items.
+struct Item {
+  int b, p, np;
+  Rows r;
+  __device__ __forceinline__ void seq(const TileArgs& a, int nb, int* err = nullptr) {
+    b = nb;
+    p = 0;
+    r = rows_of(a.p, b, err);
+    np = items_of(a, r);
+  }
+  // the idx-th item of the sequences from first on
+  __device__ __forceinline__ void find(const TileArgs& a, int first, long long idx) {
+    seq(a, first);
+    while (idx >= np) {
+      idx -= np;
+      seq(a, b + 1);
+    }
+    p = static_cast<int>(idx);
+  }
+  __device__ __forceinline__ void next(const TileArgs& a) {
+    if (++p < np) return;
+    do {
+      seq(a, b + 1);
+    } while (np == 0);
+  }
+};
+
+__device__ __forceinline__ int chunk_of(const long long* prefix, long long x) {
+  int lo = 0, hi = kThreads - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (x < prefix[mid + 1]) hi = mid; else lo = mid + 1;
+  }
+  return lo;
+}
+
+// Exclusive prefix sums of one value per thread into out[0 .. kThreads].
+__device__ __forceinline__ void cta_prefix(long long v, long long* out, Shared& sh) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  if (lane == 31) sh.w_sum[warp] = v;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) v += sh.w_sum[w];
+  out[threadIdx.x + 1] = v;
+  if (threadIdx.x == 0) out[0] = 0;
+  __syncthreads();
+}
+
+// How the work lies in threads' chunks.
+struct Layout {
+  int per_seq;          // sequences per thread
+  long long per_item;   // items per thread
+  long long run;        // units of a CTA
+};
+
+// This CTA's units as segments: key tiles of one (item, kv head).
+struct Walk {
+  long long u, u_begin, u_end;
+  long long item_u0;     // first unit of the item
+  Item it;
+  int k0, nk;            // the item's key tiles
+  int h, first, count;   // kv head; steps [first, first + count) of nk, newest key tile first
+  int skip;              // units of the segment
+  int has_b, seg;
+  int j, g;              // step in the segment, step of the CTA
+  __device__ __forceinline__ void open(const TileArgs& a) {
+    // from u on, the next (item, kv head) with a key tile in this run
+    while (u < u_end) {
+      while (u >= item_u0 + static_cast<long long>(units_of(nk)) * a.p.Hkv) {
+        item_u0 += static_cast<long long>(units_of(nk)) * a.p.Hkv;
+        it.next(a);
+        nk = key_tiles(a, it.r, it.p, &k0);
+      }
+      const int per = units_of(nk);
+      const long long local = u - item_u0;
+      h = static_cast<int>(local / per);
+      first = static_cast<int>(local - static_cast<long long>(h) * per);
+      skip = static_cast<int>(min(static_cast<long long>(per - first), u_end - u));
+      count = min(skip, nk - first);
+      has_b = it.p * 2 * a.tq + a.tq < it.r.n;
+      if (count > 0) return;
+      u += skip;    // the run begins in the overhead of a task
+    }
+  }
+  __device__ __forceinline__ void start(const TileArgs& a, const Layout& lay, const Shared& sh) {
+    const long long total = sh.unit_prefix[kThreads];
+    u = u_begin = blockIdx.x * lay.run;
+    u_end = min(total, u + lay.run);
+    seg = j = g = 0;
+    if (u >= u_end) return;
+    const int c = chunk_of(sh.unit_prefix, u);
+    const long long idx = c * lay.per_item;
+    const int s = chunk_of(sh.seq_prefix, idx);
+    it.find(a, s * lay.per_seq, idx - sh.seq_prefix[s]);
+    item_u0 = sh.unit_prefix[c];
+    nk = key_tiles(a, it.r, it.p, &k0);
+    open(a);
+  }
+  __device__ __forceinline__ bool valid() const { return u < u_end; }
+  __device__ __forceinline__ int key_tile() const { return k0 + nk - 1 - first - j; }
+  __device__ __forceinline__ void next(const TileArgs& a) {
+    ++g;
+    if (++j < count) return;
+    j = 0;
+    u += skip;
+    ++seg;
+    open(a);
+  }
+};
+
+template <typename E, int D, bool kInt8, bool kCap, bool kBias>
+__global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_constant__ TileArgs ta) {
+  using L = Smem<D>;
+  const Page8Args& a = ta.p;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  __shared__ Shared sh;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    mbar_init(&sh.q_full, kLoad / 32);
+    mbar_init(&sh.q_free, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.k_full[i], kLoad / 32);
+      mbar_init(&sh.k_empty[i], 1);
+      mbar_init(&sh.v_full[i], kLoad / 32);
+      mbar_init(&sh.v_empty[i], 1);
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_ready[i], 128);
+      mbar_init(&sh.o_full[i], 1);
+    }
+    for (int i = 0; i < kSteps; ++i) {
+      mbar_init(&sh.step_full[i], 1);
+      mbar_init(&sh.step_free[i], 8);   // the softmax warps
+    }
+    mbar_init(&sh.mma_done, 1);
+    sh.abort = 0;
+    fence_mbar_init();
+  }
+  griddep_wait();
+  if (warp == kMma) tmem_alloc(&sh.tmem_base, 512);
+
+  // ---- the split: items per sequence, key tiles per item
+  Layout lay;
+  lay.per_seq = (a.B + kThreads - 1) / kThreads;
+  {
+    const int b0 = min(a.B, tid * lay.per_seq), b1 = min(a.B, b0 + lay.per_seq);
+    long long n = 0;
+    for (int b = b0; b < b1; ++b) n += items_of(ta, rows_of(a, b, blockIdx.x == 0 ? a.err : nullptr));
+    cta_prefix(n, sh.seq_prefix, sh);
+    const long long items = sh.seq_prefix[kThreads];
+    lay.per_item = (items + kThreads - 1) / kThreads;
+    lay.per_item = lay.per_item < 1 ? 1 : lay.per_item;
+    const long long x0 = min(items, tid * lay.per_item), x1 = min(items, x0 + lay.per_item);
+    long long units = 0;
+    if (x0 < x1) {
+      const int s = chunk_of(sh.seq_prefix, x0);
+      Item it;
+      it.find(ta, s * lay.per_seq, x0 - sh.seq_prefix[s]);
+      for (long long x = x0; x < x1; ++x) {
+        int k0;
+        units += static_cast<long long>(units_of(key_tiles(ta, it.r, it.p, &k0))) * a.Hkv;
+        if (x + 1 < x1) it.next(ta);
+      }
+    }
+    cta_prefix(units, sh.unit_prefix, sh);
+    lay.run = (sh.unit_prefix[kThreads] + gridDim.x - 1) / gridDim.x;
+    lay.run = lay.run < 1 ? 1 : lay.run;
+  }
+  // ---- the tokens' places, for the join kernel
+  for (int tok = blockIdx.x + gridDim.x * tid; tok < a.T; tok += gridDim.x * kThreads) {
+    const int b = seq_of_token(a.cu, a.B, tok);
+    Item it;
+    it.seq(ta, b);
+    if (it.r.n * a.G <= a.split_rows) continue;    // the split form's
+    TokenInfo x;
+    x.ng = -1;
+    x.stride = 0;
+    x.nt = 1;
+    x.kind = 1;
+    x.u0 = 0;
+    x.run = lay.run;
+    x.r0 = 0;
+    if (it.r.n > 0 && tok >= it.r.t0 && tok < it.r.t0 + it.r.n) {
+      const int i = tok - it.r.t0, p = i / (2 * ta.tq), iq = i - p * 2 * ta.tq;
+      int k0;
+      x.ng = key_tiles(ta, it.r, p, &k0);
+      x.stride = units_of(x.ng);
+      x.r0 = iq / ta.tq * kT + iq % ta.tq * a.G;
+      const int sc = b / lay.per_seq;
+      long long idx = sh.seq_prefix[sc];
+      for (int c = sc * lay.per_seq; c < b; ++c) idx += items_of(ta, rows_of(a, c, nullptr));
+      idx += p;
+      const long long ic = idx / lay.per_item, from = ic * lay.per_item;
+      x.u0 = sh.unit_prefix[ic];
+      if (from < idx) {
+        const int s = chunk_of(sh.seq_prefix, from);
+        it.find(ta, s * lay.per_seq, from - sh.seq_prefix[s]);
+        for (long long q = from; q < idx; ++q) {
+          x.u0 += static_cast<long long>(units_of(key_tiles(ta, it.r, it.p, &k0))) * a.Hkv;
+          it.next(ta);
+        }
+      }
+    }
+    ta.info[tok] = x;
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = sh.tmem_base;
+
+  if (warp < kSoftA) {
+    // --------------------------------------------------------------- loads
+    constexpr int kVecs = kT * D / 16 / kLoad;       // 16-byte vectors of a tile per thread
+    constexpr int kRowVecs = D / 16;                 // vectors of a row
+    constexpr int kRowsPer = kLoad / kRowVecs;       // rows of one round of loads
+    const int row0 = tid / kRowVecs, c = tid % kRowVecs;
+    const long long tok_bytes = a.hnd ? D : static_cast<long long>(a.Hkv) * D;
+    const int g_magic = (65536 + a.G - 1) / a.G;     // r * g_magic >> 16 = r / G for r, G <= 128
+    auto load = [&](const uint8_t* pool, const Step& s, uint4 (&v)[kVecs]) {
+      const uint8_t* base = pool + (a.hnd ? 0 : s.h * D) + c * 16;
+#pragma unroll
+      for (int k = 0; k < kVecs; ++k) {
+        const int r = row0 + k * kRowsPer, at = s.at[r >> 4];
+        v[k] = make_uint4(0, 0, 0, 0);
+        if (at >= 0) v[k] = load_stream(base + (at + (r & 15)) * tok_bytes);
+      }
+    };
+    // widen and store into the 128-byte-swizzled operand tile; rows from
+    // `valid` on become zero.  A vector's 16 codes are two 16-byte chunks; the
+    // lanes of the second 64-column half store theirs in the other order, so
+    // that the eight lanes of a row cover all banks.
+    const int swap = c >> 2 & 1, c0 = 2 * (c & 3);
+    const uint32_t off0 = (c >> 2) * kHalf + row0 * 128 + ((((c0 + swap) ^ row0) & 7) << 4);
+    const uint32_t off1 = (c >> 2) * kHalf + row0 * 128 + ((((c0 + 1 - swap) ^ row0) & 7) << 4);
+    auto store = [&](uint8_t* dst, const uint4 (&v)[kVecs], int valid) {
+#pragma unroll
+      for (int k = 0; k < kVecs; ++k) {
+        // kRowsPer is a multiple of 8: the swizzle is the same in every round
+        uint4 w = swap ? make_uint4(v[k].z, v[k].w, v[k].x, v[k].y) : v[k];
+        if (row0 + k * kRowsPer >= valid) w = make_uint4(0, 0, 0, 0);
+        uint32_t o[8];
+        widen<kInt8>(w.x, o[0], o[1]);
+        widen<kInt8>(w.y, o[2], o[3]);
+        widen<kInt8>(w.z, o[4], o[5]);
+        widen<kInt8>(w.w, o[6], o[7]);
+        *reinterpret_cast<uint4*>(dst + off0 + k * kRowsPer * 128) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(dst + off1 + k * kRowsPer * 128) = make_uint4(o[4], o[5], o[6], o[7]);
+      }
+    };
+    // the pair's queries: copied into the operand tiles as they are, then (bf16)
+    // turned into f16 in place, a thread to a row
+    auto load_q = [&](const Step& s) {
+      constexpr int kQRow = D / 8;                   // vectors of a row
+      constexpr int kQRows = kLoad / kQRow;          // rows of one round
+      const int qr = tid / kQRow, qc = tid % kQRow;
+      const int tiles = s.flags & kHasB ? 2 : 1, i0 = s.i0, n = s.n;
+      const E* q = static_cast<const E*>(a.q) + (static_cast<size_t>(s.t0) * a.Hq + s.h * a.G) * D + qc * 8;
+      uint8_t* dst = smem + L::kQ + (qc >> 3) * kHalf;
+#pragma unroll 4
+      for (int k = 0; k < tiles * (kT / kQRows); ++k) {
+        const int rr = k * kQRows + qr, tile = rr >> 7, r = rr & 127;
+        const int iq = r * g_magic >> 16, i = i0 + tile * ta.tq + iq;      // r / G
+        const bool live = iq < ta.tq && i < n;
+        const long long at = live ? (static_cast<long long>(i) * a.Hq + r - iq * a.G) * D : 0;
+        cp_async_16_zfill(dst + tile * L::kOp + r * 128 + (((qc ^ r) & 7) << 4), q + at, live ? 16u : 0u);
+      }
+      cp_async_wait_all();
+      if constexpr (!std::is_same<E, __half>::value) {
+        named_barrier(1, kLoad);
+        for (int tile = 0; tile < tiles; ++tile) {
+          uint8_t* row = smem + L::kQ + tile * L::kOp + tid * 128;
+          float amax = 0.f;
+#pragma unroll 4
+          for (int k = 0; k < D / 8; ++k) {
+            const uint4 v = *reinterpret_cast<const uint4*>(row + (k >> 3) * kHalf + (((k ^ tid) & 7) << 4));
+            const uint32_t wv[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              amax = fmax3(amax, fabsf(__uint_as_float(wv[q] << 16)), fabsf(__uint_as_float(wv[q] & 0xFFFF0000u)));
+          }
+          float inv;
+          const float mul = q_to_f16_scale(amax, &inv);
+          sh.qsc[s.seg & 1][tile][tid] = inv * (kCap ? a.scale_cap : a.scale_log2);
+#pragma unroll 4
+          for (int k = 0; k < D / 8; ++k) {
+            uint4* at = reinterpret_cast<uint4*>(row + (k >> 3) * kHalf + (((k ^ tid) & 7) << 4));
+            const uint4 v = *at;
+            uint32_t wv[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              wv[q] = f32x2_to_f16x2(__uint_as_float(wv[q] & 0xFFFF0000u) * mul, __uint_as_float(wv[q] << 16) * mul);
+            *at = make_uint4(wv[0], wv[1], wv[2], wv[3]);
+          }
+        }
+      }
+    };
+
+    uint4 kv[kVecs], vv[kVecs];
+    bool ok = warp_await(&sh.step_full[0], 0, sh, a.err);
+    bool more = ok && !(sh.step[0].flags & kEnd);
+    if (more) {
+      load(a.k, sh.step[0], kv);
+      load(a.v, sh.step[0], vv);
+    }
+    for (int g = 0; more; ++g) {
+      const Step& s = sh.step[g % kSteps];
+      const int bsel = g & 1;
+      const uint32_t ph = (g >> 1) & 1;
+      if (s.flags & kFirst) {
+        if (!warp_await(&sh.q_free, (s.seg & 1) ^ 1, sh, a.err)) break;
+        load_q(s);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.q_full);
+      }
+      const int left = s.len - s.j0;                 // keys of this tile that exist
+      if (!warp_await(&sh.k_empty[bsel], ph ^ 1, sh, a.err)) break;
+      store(smem + L::kK + bsel * L::kOp, kv, kT);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.k_full[bsel]);
+      const int n1 = g + 1;
+      if (!warp_await(&sh.step_full[n1 % kSteps], (n1 / kSteps) & 1, sh, a.err)) break;
+      const Step& s1 = sh.step[n1 % kSteps];
+      more = !(s1.flags & kEnd);
+      if (more) load(a.k, s1, kv);
+      if (!warp_await(&sh.v_empty[bsel], ph ^ 1, sh, a.err)) break;
+      store(smem + L::kV + bsel * L::kOp, vv, left);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.v_full[bsel]);
+      if (more) load(a.v, s1, vv);
+    }
+  } else if (warp == kWalk) {
+    // ---------------------------------------------------------------- walk
+    // Three steps are in hand: the oldest is written, the middle one waits for
+    // its scales, the newest for its page ids (lane l < 8: 16 keys each).
+    const int gpp = a.ps / 16;
+    Walk w;
+    w.start(ta, lay, sh);
+    struct Ahead {
+      int flags, j0, seg, t0, n, len, prefix, h, i0, piece;
+      const int32_t* bt;
+    };
+    int page[2] = {-1, -1}, at[2] = {-1, -1};      // [0] the older
+    float ks = 0.f, vs = 0.f;
+    Ahead x[3];
+    for (int i = 0; i < 3; ++i) x[i].flags = -1;   // nothing in hand
+    int g = 0;
+    bool done = false;
+    while (true) {
+      // the step behind the walk; -1 once it has ended
+      x[0] = x[1];
+      x[1] = x[2];
+      if (w.valid()) {
+        x[2].flags = (w.j == 0 ? kFirst : 0) | (w.j == w.count - 1 ? kLast : 0) | (w.has_b ? kHasB : 0) |
+                     (w.count == w.nk ? kWholeTask : 0);
+        x[2].j0 = w.key_tile() * kT;
+        x[2].seg = w.seg;
+        x[2].t0 = w.it.r.t0, x[2].n = w.it.r.n, x[2].len = w.it.r.len, x[2].prefix = w.it.r.prefix;
+        x[2].h = w.h;
+        x[2].i0 = w.it.p * 2 * ta.tq;
+        x[2].piece = 2 * blockIdx.x + (w.u == w.u_begin ? 0 : 1);
+        x[2].bt = a.bt + static_cast<size_t>(w.it.b) * a.bt_stride;
+        w.next(ta);
+      } else {
+        x[2].flags = done ? -1 : kEnd;
+        x[2].j0 = x[2].len = 0;
+        done = true;
+      }
+      const float oks = ks, ovs = vs;              // x[0]'s
+      const int oat = at[0];
+      // x[1]: its page ids are here, its scales are asked for
+      at[0] = -1;
+      if (x[1].flags >= 0 && lane < 8 && page[0] != INT_MIN) {
+        const int gi = (x[1].j0 >> 4) + lane;
+        if (page[0] >= 0 && page[0] < a.num_pages) {
+          at[0] = (a.hnd ? page[0] * a.Hkv + x[1].h : page[0]) * a.ps + (gi % gpp) * 16;
+          const size_t sx = static_cast<size_t>(page[0]) * a.Hkv + x[1].h;
+          ks = __ldg(a.ks + sx);
+          vs = __ldg(a.vs + sx);
+        } else {
+          report_error(a.err, kDevErrBadPage);
+        }
+      }
+      // x[2]: its page ids are asked for (INT_MIN: no keys there)
+      page[0] = INT_MIN;
+      if (lane < 8 && x[2].flags >= 0) {
+        const int gi = (x[2].j0 >> 4) + lane;
+        if (gi * 16 < x[2].len) page[0] = __ldg(x[2].bt + gi / gpp);
+      }
+      if (x[0].flags >= 0) {
+        if (!warp_await(&sh.step_free[g % kSteps], ((g / kSteps) & 1) ^ 1, sh, a.err)) break;
+        Step& s = sh.step[g % kSteps];
+        if (lane < 8) {
+          s.at[lane] = oat;
+          const float sv = ovs == 0.f ? 1.f : fmaxf(ovs, kMinScale);
+          s.sc[lane] = make_float4(oat >= 0 ? oks : __uint_as_float(kBadPageMark), log2f(sv), 1.f / sv, 0.f);
+        }
+        if (lane == 0) {
+          s.flags = x[0].flags, s.j0 = x[0].j0, s.seg = x[0].seg, s.t0 = x[0].t0, s.n = x[0].n, s.len = x[0].len;
+          s.prefix = x[0].prefix, s.h = x[0].h, s.i0 = x[0].i0, s.piece = x[0].piece;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.step_full[g % kSteps]);
+        ++g;
+        if (x[0].flags & kEnd) break;
+      }
+    }
+  } else if (warp == kMma) {
+    // ----------------------------------------------------------------- MMA
+    if (lane == 0) {
+      const uint32_t idesc_qk = make_idesc(kFmtF16, kFmtF16, 0, 0, kT, kT);
+      const uint32_t idesc_pv = make_idesc(kFmtF16, kFmtF16, 0, 1, kT, D);
+      const uint64_t qdesc = make_smem_desc(smem_u32(smem + L::kQ), 16, 1024, kSwizzle128B);
+      const uint64_t kdesc = make_smem_desc(smem_u32(smem + L::kK), 16, 1024, kSwizzle128B);
+      // MN-major V: 64-column atoms 16 KB apart, 16 key rows (2 KB) per K = 16 step
+      const uint64_t vdesc = make_smem_desc(smem_u32(smem + L::kV), kHalf, 1024, kSwizzle128B);
+      int cnt_p[2] = {0, 0};      // PVs issued per tile (p_ready phases)
+      int pend[2] = {-1, -1};     // flags of the step whose PV is due, by tile
+      bool ok = true;
+      // PV_x of step g - 1
+      auto pv = [&](int x, int g1) -> bool {
+        if (!await(&sh.p_ready[x], cnt_p[x] & 1, sh, a.err)) return false;
+        if (!await(&sh.v_full[g1 & 1], (g1 >> 1) & 1, sh, a.err)) return false;
+        tc_fence_after_sync();
+        const uint64_t db = vdesc + static_cast<uint64_t>(((g1 & 1) * L::kOp) >> 4);
+        const uint32_t cs = tmem + kColS + 128u * x, co = tmem + kColO + 128u * x;
+#pragma unroll
+        for (int kk = 0; kk < kT / 16; ++kk)
+          tc_mma_f16_tmem_a(co, cs + 8 * kk, db + static_cast<uint64_t>((kk * 16 * 128) >> 4), idesc_pv,
+                            (!(pend[x] & kFirst) || kk > 0) ? 1u : 0u);
+        if (x == (pend[x] & kHasB ? 1 : 0)) tc_commit(&sh.v_empty[g1 & 1]);   // the last reader of V
+        if (pend[x] & kLast) tc_commit(&sh.o_full[x]);
+        ++cnt_p[x];
+        pend[x] = -1;
+        return true;
+      };
+      auto qk = [&](int x, int g, int flags, int seg) -> bool {
+        if ((flags & kFirst) && !await(&sh.q_full, seg & 1, sh, a.err)) return false;
+        if (!await(&sh.k_full[g & 1], (g >> 1) & 1, sh, a.err)) return false;
+        tc_fence_after_sync();
+        const uint64_t da = qdesc + static_cast<uint64_t>((x * L::kOp) >> 4);
+        const uint64_t db = kdesc + static_cast<uint64_t>(((g & 1) * L::kOp) >> 4);
+        const uint32_t cs = tmem + kColS + 128u * x;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
+          tc_mma_f16(cs, da + (off >> 4), db + (off >> 4), idesc_qk, kk > 0);
+        }
+        tc_commit(&sh.s_full[x]);
+        if (x == (flags & kHasB ? 1 : 0)) {   // the last reader of K and, at the end, Q
+          tc_commit(&sh.k_empty[g & 1]);
+          if (flags & kLast) tc_commit(&sh.q_free);
+        }
+        pend[x] = flags;
+        return true;
+      };
+      // step g: PV_A(g-1) QK_A(g) PV_B(g-1) QK_B(g)
+      int g = 0;
+      for (; ok; ++g) {
+        ok = await(&sh.step_full[g % kSteps], (g / kSteps) & 1, sh, a.err);
+        if (!ok) break;
+        const int flags = sh.step[g % kSteps].flags, seg = sh.step[g % kSteps].seg;
+        const bool end = flags & kEnd;
+        if (pend[0] >= 0) ok = pv(0, g - 1);
+        if (ok && !end) ok = qk(0, g, flags, seg);
+        if (ok && pend[1] >= 0) ok = pv(1, g - 1);
+        if (ok && !end && (flags & kHasB)) ok = qk(1, g, flags, seg);
+        if (end) break;
+      }
+      // every MMA issued here completes before TMEM is released
+      tc_commit(&sh.mma_done);
+      const long long t0 = clock64();
+      while (!mbar_try_wait(&sh.mma_done, 0)) {
+        if (clock64() - t0 > kWaitTimeoutCycles) {
+          report_error(a.err, kDevErrTimeout);
+          break;
+        }
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------ softmax and epilogue
+    const int x = warp < kSoftB ? 0 : 1;          // tile A or B
+    const int r = (warp & 3) * 32 + lane;         // tile row = TMEM lane
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t srow = tmem + lane_base + kColS + 128u * x;
+    const uint32_t orow = tmem + lane_base + kColO + 128u * x;
+    int cnt = 0, units = 0;                       // steps and segments of this tile
+    float m = 0.f, l = 0.f, sc = 0.f, slope = 0.f;
+    bool seen = false;
+    int hi = 0, lo = 0, at = 0;
+    bool live = false;
+    for (int g = 0;; ++g) {
+      if (!warp_await(&sh.step_full[g % kSteps], (g / kSteps) & 1, sh, a.err)) break;
+      const Step& st = sh.step[g % kSteps];
+      const int flags = st.flags;
+      if (flags & kEnd) break;
+      if (x == 1 && !(flags & kHasB)) {     // a segment without tile B
+        if (lane == 0) mbar_arrive(&sh.step_free[g % kSteps]);
+        continue;
+      }
+      if (flags & kFirst) {
+        const int q = r / a.G, i = st.i0 + x * ta.tq + q;
+        Rows rows;
+        rows.t0 = st.t0, rows.n = st.n, rows.len = st.len, rows.prefix = st.prefix;
+        live = q < ta.tq && i < st.n;
+        hi = live ? row_hi(a, rows, i) : 0;
+        lo = live ? row_lo(a, rows, i) : 0;
+        at = st.len - st.n + i;
+        if constexpr (kBias) slope = live ? __ldg(a.slopes + st.h * a.G + r - q * a.G) * kLog2e : 0.f;
+        m = l = 0.f;
+        seen = !live;         // dead rows never wait for a key
+      }
+      if (!warp_await(&sh.s_full[x], cnt & 1, sh, a.err)) break;
+      tc_fence_after_sync();
+      if (flags & kFirst)
+        sc = std::is_same<E, __half>::value ? (kCap ? a.scale_cap : a.scale_log2) : sh.qsc[st.seg & 1][x][r];
+      const float4* gs = st.sc;
+      const int j0 = st.j0;
+      const bool whole = __all_sync(0xffffffffu, !live || (lo <= j0 && j0 + kT <= hi));
+
+      // z = y - m of 32 columns, -inf for keys the row does not see
+      auto logits = [&](int c, uint32_t (&v)[32]) {
+        tmem_ld32(srow + 32 * c, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const float4 s4 = gs[2 * c + q];
+          const bool bad = __float_as_uint(s4.x) == kBadPageMark;
+          const float f = bad ? 0.f : sc * s4.x, off = bad ? -INFINITY : s4.y - m;
+          if constexpr (!kCap && !kBias) {
+            const uint64_t f2 = f32x2_pack(f, f), o2 = f32x2_pack(off, off);
+#pragma unroll
+            for (int i = 16 * q; i < 16 * q + 16; i += 2) {
+              const float2 z = f32x2_unpack(
+                  f32x2_fma(f32x2_pack(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), f2, o2));
+              v[i] = __float_as_uint(z.x);
+              v[i + 1] = __float_as_uint(z.y);
+            }
+          } else {
+#pragma unroll
+            for (int i = 16 * q; i < 16 * q + 16; ++i) {
+              float o = off;
+              if constexpr (kBias) o = fmaf(slope, static_cast<float>(j0 + 32 * c + i - at), o);
+              const float s = __uint_as_float(v[i]);
+              v[i] = __float_as_uint(kCap ? fmaf(a.cap_log2, tanh_of(s * f), o) : fmaf(s, f, o));
+            }
+          }
+        }
+        if (!whole) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const int j = j0 + 32 * c + i;
+            if (j < lo || j >= hi) v[i] = 0xFF800000u;
+          }
+        }
+      };
+      auto top_of = [&](const uint32_t (&v)[32]) {
+        float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < 32; i += 2)
+          t4[(i >> 1) & 3] = fmax3(t4[(i >> 1) & 3], __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+        return fmax3(fmaxf(t4[0], t4[1]), t4[2], t4[3]);
+      };
+
+      if (__any_sync(0xffffffffu, !seen)) {   // rows without a key so far: their maximum first
+        float top = -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t v[32];
+          logits(c, v);
+          top = fmaxf(top, top_of(v));
+        }
+        if (!seen && top > -INFINITY) {
+          m = top - kSetP;
+          seen = true;
+        }
+      }
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        uint32_t v[32];
+        logits(c, v);
+        const float top = top_of(v);
+        if (__any_sync(0xffffffffu, top > kMaxP)) {
+          // move m; everything so far is scaled to it.  The previous PV of this
+          // tile is complete: it was issued before the QK that s_full saw.
+          const float d = seen ? fmaxf(top - kSetP, 0.f) : 0.f;
+          const float f = fast_exp2(-d);
+          m += d;
+          l *= f;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) - d);
+          if (!(flags & kFirst)) {
+#pragma unroll 1
+            for (int k = 0; k < D / 16; ++k) {
+              uint32_t o[16];
+              tmem_ld16(orow + 16 * k, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_st16(orow + 16 * k, o);
+            }
+          }
+          const __half2 f2 = __float2half2_rn(f);
+#pragma unroll 1
+          for (int k = 0; k < c; ++k) {
+            uint32_t p[16];
+            tmem_ld16(srow + 16 * k, p);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&p[i]), f2);
+              p[i] = *reinterpret_cast<const uint32_t*>(&y);
+            }
+            tmem_st16(srow + 16 * k, p);
+          }
+          tmem_st_wait();
+        }
+        uint32_t pk[16];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint64_t ls2 = f32x2_pack(0.f, 0.f);
+#pragma unroll
+          for (int i = 8 * q; i < 8 * q + 8; ++i) {
+            const float p0 = fast_exp2(__uint_as_float(v[2 * i])), p1 = fast_exp2(__uint_as_float(v[2 * i + 1]));
+            ls2 = f32x2_add(ls2, f32x2_pack(p0, p1));
+            pk[i] = f32x2_to_f16x2(p1, p0);
+          }
+          const float2 ls = f32x2_unpack(ls2);
+          l = fmaf(ls.x + ls.y, gs[2 * c + q].z, l);
+        }
+        tmem_st16(srow + 16 * c, pk);
+      }
+      tmem_st_wait();
+      tc_fence_before_sync();
+      mbar_arrive(&sh.p_ready[x]);
+      ++cnt;
+      if (flags & kLast) {
+        // ---- the segment's rows, once its last PV has landed
+        if (!warp_await(&sh.o_full[x], units & 1, sh, a.err)) break;
+        tc_fence_after_sync();
+        const float lse2 = seen && l > 0.f ? m + log2f(l) : -INFINITY;
+        if (flags & kWholeTask) {
+          const float so = l > 0.f ? 1.f / l : 0.f;
+          const size_t row = static_cast<size_t>(st.t0 + st.i0 + x * ta.tq + r / a.G) * a.Hq + st.h * a.G + r % a.G;
+          E* out = static_cast<E*>(a.o) + row * D;
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t v[32];
+            tmem_ld32(orow + 32 * c, v);
+            tmem_ld_wait();
+            if (live) {
+              uint4* o4 = reinterpret_cast<uint4*>(out + 32 * c);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                uint32_t pk[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  pk[k] = pack_out<E>(__uint_as_float(v[8 * i + 2 * k + 1]) * so, __uint_as_float(v[8 * i + 2 * k]) * so);
+                o4[i] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+              }
+            }
+          }
+          if (live && a.lse != nullptr) a.lse[row] = lse2 > -INFINITY ? lse2 * kLn2 : -INFINITY;
+        } else {
+          const size_t pr = static_cast<size_t>(st.piece) * (2 * kT) + x * kT + r;
+          float* out = ta.part_o + pr * D;
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t v[32];
+            tmem_ld32(orow + 32 * c, v);
+            tmem_ld_wait();
+            if (live) {
+              uint4* o4 = reinterpret_cast<uint4*>(out + 32 * c);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) o4[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            }
+          }
+          if (live) ta.part_ml[pr] = make_float2(seen ? m : -INFINITY, l);
+        }
+        tc_fence_before_sync();
+        ++units;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.step_free[g % kSteps]);
+    }
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == kMma) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <typename E, int D, bool kInt8, bool kCap, bool kBias>
+cudaError_t go(const TileArgs& a, int sms, cudaStream_t stream) {
+  auto kernel = attend_tile_kernel<E, D, kInt8, kCap, kBias>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(sms));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Smem<D>::kBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+template <typename E, int D, bool kInt8>
+cudaError_t pick2(const TileArgs& a, int sms, cudaStream_t s) {
+  const bool cap = a.p.cap_log2 > 0.f, bias = a.p.slopes != nullptr;
+  if (cap) return bias ? go<E, D, kInt8, true, true>(a, sms, s) : go<E, D, kInt8, true, false>(a, sms, s);
+  return bias ? go<E, D, kInt8, false, true>(a, sms, s) : go<E, D, kInt8, false, false>(a, sms, s);
+}
+
+template <typename E>
+cudaError_t pick(const TileArgs& a, int D, bool int8, int sms, cudaStream_t s) {
+  if (D == 64) return int8 ? pick2<E, 64, true>(a, sms, s) : pick2<E, 64, false>(a, sms, s);
+  return int8 ? pick2<E, 128, true>(a, sms, s) : pick2<E, 128, false>(a, sms, s);
+}
+
+}  // namespace
+
+cudaError_t launch_attend_tiles(const TileArgs& a, int head_dim, bool int8, bool f16, int sms, cudaStream_t stream) {
+  return f16 ? pick<__half>(a, head_dim, int8, sms, stream) : pick<__nv_bfloat16>(a, head_dim, int8, sms, stream);
+}
+
+}  // namespace qpkv

@@ -17,6 +17,7 @@ constexpr float kMinScale = 7.888609e-31f;   // 2^-100
 
 struct Page8Args {
   int B, T, Hq, Hkv, G, ps, num_pages, bt_stride, causal, window, hnd;
+  int split_rows;          // sequences with more query rows per kv head go in tiles of 128
   float scale_log2;        // softmax scale * log2(e)
   float scale_cap;         // softmax scale / cap
   float cap_log2;          // cap * log2(e), 0: no cap
@@ -94,6 +95,46 @@ __device__ __forceinline__ int row_hi(const Page8Args& a, const Rows& r, int i) 
 __device__ __forceinline__ int row_lo(const Page8Args& a, const Rows& r, int i) {
   if (a.window <= 0) return 0;
   return static_cast<int>(max(0ll, static_cast<long long>(r.len) - r.n + i + 1 - a.window));
+}
+
+// Where the pieces of a query token's results lie, for the join kernel: one
+// load instead of a search through the lengths.
+struct alignas(16) TokenInfo {
+  long long u0;     // first unit of its row tiles (of kv head 0)
+  long long run;    // units of a worker
+  int ng;           // units of a task that have results (-1: no sequence has the token)
+  int stride;       // units of a task
+  int nt, r0;       // tasks per kv head, first row in the task (or tasks)
+  int kind;         // 0: the split form, 1: the tiled form
+  int pad[3];
+};
+
+// The tiled form (attend_page8_tile.cu): 128 / G whole queries per tile, two
+// tiles per item, one worker per CTA.
+struct TileArgs {
+  Page8Args p;
+  int tq;
+  float* part_o;      // [2 * CTAs][256][D]
+  float2* part_ml;    // [2 * CTAs][256] (m, l)
+  TokenInfo* info;    // [T]
+};
+cudaError_t launch_attend_tiles(const TileArgs& a, int head_dim, bool int8, bool f16, int sms, cudaStream_t stream);
+
+// Four 8-bit codes as two pairs of f16 (exact).
+template <bool kInt8>
+__device__ __forceinline__ void widen(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if constexpr (kInt8) {
+    // 1024 + (code + 128) as f16 by its bits, minus 1152
+    const uint32_t u = w ^ 0x80808080u;
+    const __half2 c = __floats2half2_rn(1152.f, 1152.f);
+    uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    __half2 x = __hsub2(*reinterpret_cast<__half2*>(&a), c), y = __hsub2(*reinterpret_cast<__half2*>(&b), c);
+    lo = *reinterpret_cast<uint32_t*>(&x);
+    hi = *reinterpret_cast<uint32_t*>(&y);
+  } else {
+    lo = e4m3x2_to_f16x2(static_cast<uint16_t>(w & 0xFFFFu));
+    hi = e4m3x2_to_f16x2(static_cast<uint16_t>(w >> 16));
+  }
 }
 
 // 2^x by the hardware approximation (relative error ~2^-22; -inf -> 0).

@@ -359,6 +359,40 @@ def test_attend_page8_long_and_many(lib, err, reqs, Hq, H):
     assert torch.equal(got, again)
 
 
+TILES = [[(300, 300)], [(130, 700), (1, 50), (64, 64), (0, 9), (40, 300)], [(90, 1500)], [(200, 60), (33, 0), (30, 129)]]
+
+
+@pytest.mark.parametrize("reqs", TILES, ids=["prompt", "mixed", "piece", "short_cache"])
+@pytest.mark.parametrize("Hq,H,D,ps,fmt,dtype,hnd", [
+    (2, 2, 128, 16, "e4m3", "bf16", False), (8, 2, 128, 64, "int8", "f16", True), (7, 1, 64, 48, "e4m3", "f16", False),
+    (6, 2, 64, 128, "int8", "bf16", False)])
+@pytest.mark.parametrize("kw,slopes,prefix", [
+    (dict(), False, None), (dict(window=70), False, None), (dict(logit_cap=30.0), False, 100), (dict(causal=False), True, None),
+    (dict(), True, None)], ids=["plain", "window", "cap_prefix", "full_bias", "bias"])
+def test_attend_page8_many_rows(lib, err, reqs, Hq, H, D, ps, fmt, dtype, hnd, kw, slopes, prefix):
+    """Sequences beside one another whose rows go in tiles of 128 and whose
+    rows do not, runs that cut an item, rows before the first key."""
+    c = _attend_case(Hq + len(reqs), reqs, Hq, H, D, ps, fmt, dtype, hnd, slopes=slopes,
+                     prefix=[prefix] * len(reqs) if prefix else None, pad=3)
+    out = torch.full_like(c["dev"]["q"], 7.0)
+    lse = torch.full(out.shape[:2], 7.0, device="cuda")
+    _run_attend(lib, c, err, max_q=max(n for n, _ in reqs), out=out, lse=lse, **kw)
+    assert int(err) == 0 and (out[c["T"]:] == 7.0).all() and (lse[c["T"]:] == 7.0).all()
+    _check_attend(c, out, lse, **kw)
+
+
+def test_attend_page8_forms_agree(lib, err):
+    """The bound on a sequence's queries picks the kernels, never the result's
+    meaning: without one, and with one that is too small to be a bound."""
+    c = _attend_case(3, [(50, 400), (3, 90)], 8, 2, 128, 16, "e4m3", "bf16", False)
+    for max_q in (0, 50, 1000, 3):
+        lse = torch.empty(c["q"].shape[:2], device="cuda")
+        got = _run_attend(lib, c, err, max_q=max_q, lse=lse)
+        _check_attend(c, got, lse)
+        assert torch.equal(got, _run_attend(lib, c, err, max_q=max_q))
+    assert int(err) == 0
+
+
 @pytest.mark.parametrize("size", [1e-30, 1e-3, 300.0, 1e30])
 def test_attend_page8_query_and_value_sizes(lib, err, size):
     """Query rows of any bf16 size (the softmax scale makes up for it), value
