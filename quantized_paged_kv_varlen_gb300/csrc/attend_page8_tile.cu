@@ -77,7 +77,7 @@ struct Smem {
 };
 
 struct Shared {
-  uint64_t q_full, q_free;
+  uint64_t q_raw, q_full, q_free;             // the queries' copy, their f16, their last use
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t s_full[2], p_ready[2], o_full[2];  // per tile A / B
   uint64_t mma_done;
@@ -254,7 +254,7 @@ struct Walk {
 };
 
 template <typename E, int D, bool kInt8, bool kCap, bool kBias>
-__global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_constant__ TileArgs ta) {
+__global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ TileArgs ta) {
   using L = Smem<D>;
   const Page8Args& a = ta.p;
   extern __shared__ uint8_t smem_raw[];
@@ -263,6 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
+    mbar_init(&sh.q_raw, 1);
     mbar_init(&sh.q_full, kLoad / 32);
     mbar_init(&sh.q_free, 1);
     for (int i = 0; i < 2; ++i) {
@@ -361,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
     constexpr int kRowsPer = kLoad / kRowVecs;       // rows of one round of loads
     const int row0 = tid / kRowVecs, c = tid % kRowVecs;
     const long long tok_bytes = a.hnd ? D : static_cast<long long>(a.Hkv) * D;
-    const int g_magic = (65536 + a.G - 1) / a.G;     // r * g_magic >> 16 = r / G for r, G <= 128
+    int copies = 0;                                  // query loads that thread 0 has issued
     auto load = [&](const uint8_t* pool, const Step& s, uint4 (&v)[kVecs]) {
       const uint8_t* base = pool + (a.hnd ? 0 : s.h * D) + c * 16;
 #pragma unroll
@@ -393,26 +394,24 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
         *reinterpret_cast<uint4*>(dst + off1 + k * kRowsPer * 128) = make_uint4(o[4], o[5], o[6], o[7]);
       }
     };
-    // the pair's queries: copied into the operand tiles as they are, then (bf16)
-    // turned into f16 in place, a thread to a row
-    auto load_q = [&](const Step& s) {
-      constexpr int kQRow = D / 8;                   // vectors of a row
-      constexpr int kQRows = kLoad / kQRow;          // rows of one round
-      const int qr = tid / kQRow, qc = tid % kQRow;
-      const int tiles = s.flags & kHasB ? 2 : 1, i0 = s.i0, n = s.n;
-      const E* q = static_cast<const E*>(a.q) + (static_cast<size_t>(s.t0) * a.Hq + s.h * a.G) * D + qc * 8;
-      uint8_t* dst = smem + L::kQ + (qc >> 3) * kHalf;
-#pragma unroll 4
-      for (int k = 0; k < tiles * (kT / kQRows); ++k) {
-        const int rr = k * kQRows + qr, tile = rr >> 7, r = rr & 127;
-        const int iq = r * g_magic >> 16, i = i0 + tile * ta.tq + iq;      // r / G
-        const bool live = iq < ta.tq && i < n;
-        const long long at = live ? (static_cast<long long>(i) * a.Hq + r - iq * a.G) * D : 0;
-        cp_async_16_zfill(dst + tile * L::kOp + r * 128 + (((qc ^ r) & 7) << 4), q + at, live ? 16u : 0u);
+    // the pair's queries: TMA boxes of (64 dims, G heads, TQ queries), whose rows
+    // are a tile's rows, then (bf16) turned into f16 in place, a thread to a row.
+    // Rows behind the sequence's last are whatever the boxes bring (or were left
+    // with): nothing of them is written.
+    auto load_q = [&](const Step& s) -> bool {
+      const int tiles = s.flags & kHasB ? 2 : 1, seg = s.seg;
+      if (tid == 0) {
+        mbar_arrive_expect_tx(&sh.q_raw, tiles * D * ta.tq * a.G * 2);
+        for (int k = 0; k < tiles * (D / 64); ++k) {
+          const int tile = k / (D / 64), half = k % (D / 64);
+          tma_load_3d(smem + L::kQ + tile * L::kOp + half * kHalf, &q_map, &sh.q_raw, 64 * half, s.h * a.G,
+                      s.t0 + s.i0 + tile * ta.tq);
+        }
+        ++copies;
       }
-      cp_async_wait_all();
+      __syncwarp();
+      if (!warp_await(&sh.q_raw, seg & 1, sh, a.err)) return false;
       if constexpr (!std::is_same<E, __half>::value) {
-        named_barrier(1, kLoad);
         for (int tile = 0; tile < tiles; ++tile) {
           uint8_t* row = smem + L::kQ + tile * L::kOp + tid * 128;
           float amax = 0.f;
@@ -426,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
           }
           float inv;
           const float mul = q_to_f16_scale(amax, &inv);
-          sh.qsc[s.seg & 1][tile][tid] = inv * (kCap ? a.scale_cap : a.scale_log2);
+          sh.qsc[seg & 1][tile][tid] = inv * (kCap ? a.scale_cap : a.scale_log2);
 #pragma unroll 4
           for (int k = 0; k < D / 8; ++k) {
             uint4* at = reinterpret_cast<uint4*>(row + (k >> 3) * kHalf + (((k ^ tid) & 7) << 4));
@@ -439,6 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
           }
         }
       }
+      return true;
     };
 
     uint4 kv[kVecs], vv[kVecs];
@@ -454,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
       const uint32_t ph = (g >> 1) & 1;
       if (s.flags & kFirst) {
         if (!warp_await(&sh.q_free, (s.seg & 1) ^ 1, sh, a.err)) break;
-        load_q(s);
+        if (!load_q(s)) break;
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.q_full);
@@ -477,6 +477,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
       if (lane == 0) mbar_arrive(&sh.v_full[bsel]);
       if (more) load(a.v, s1, vv);
     }
+    // a query load still on its way (after a wait that ran out) lands before the CTA ends
+    if (tid == 0 && copies > 0) mbar_wait(&sh.q_raw, (copies - 1) & 1);
   } else if (warp == kWalk) {
     // ---------------------------------------------------------------- walk
     // Three steps are in hand: the oldest is written, the middle one waits for
@@ -846,6 +848,13 @@ cudaError_t go(const TileArgs& a, int sms, cudaStream_t stream) {
   auto kernel = attend_tile_kernel<E, D, kInt8, kCap, kBias>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
   if (e != cudaSuccess) return e;
+  CUtensorMap q_map;
+  const uint64_t dims[3] = {D, static_cast<uint64_t>(a.p.Hq), static_cast<uint64_t>(a.p.T)};
+  const uint64_t strides[2] = {D * 2, static_cast<uint64_t>(a.p.Hq) * D * 2};
+  const uint32_t box[3] = {64, static_cast<uint32_t>(a.p.G), static_cast<uint32_t>(a.tq)};
+  if (encode_tensor_map(&q_map, std::is_same<E, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                        3, const_cast<void*>(a.p.q), dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(sms));
   cfg.blockDim = dim3(kThreads);
@@ -856,7 +865,7 @@ cudaError_t go(const TileArgs& a, int sms, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a);
+  return cudaLaunchKernelEx(&cfg, kernel, q_map, a);
 }
 
 template <typename E, int D, bool kInt8>
