@@ -4,26 +4,28 @@
 //
 // Rows of a (sequence, kv head) are its queries times the G query heads that
 // share the kv head.  A tile is 128 rows of TQ = 128 / G whole queries; an
-// item is a pair of tiles A and B, run side by side over one stream of
-// 128-key tiles: while one tile's softmax computes its exponentials the tensor
-// core works on the other, and each K/V tile is fetched and widened once for
-// both.  One persistent CTA per SM, 14 warps:
+// item is a pair of tiles A and B, run side by side over one stream of 64-key
+// tiles: while one tile's softmax computes its exponentials the tensor core
+// works on the other, and each K/V tile is fetched and widened once for both.  One persistent CTA per SM, 15 warps:
 //   warps 0-3   loads: K and V codes come straight from the pages into
 //               registers one key tile ahead (16 bytes a lane, whole rows) and
 //               go widened to f16 (exact) into the operand layouts; the
 //               item's queries as f16 (bf16 rows times a power of two)
 //   warps 4-7   softmax and epilogue of tile A, one thread per row
 //   warps 8-11  the same for tile B
-//   warp 12     one thread issues tcgen05.mma: per key tile g
-//                 PV_A(g-1) QK_A(g) PV_B(g-1) QK_B(g)
+//   warps 12, 14  one thread each issues the tcgen05.mma of tile A and tile B:
+//               per key tile g QK(g+1) PV(g) (one thread for both tiles took
+//               3,600 cycles a step to issue 24 of them)
 //   warp 13     walks the work: writes for every step what the others need (the
-//               item, the pages' rows, the scales) into a ring of four
+//               item, the pages' rows, the scales) into a ring of eight
 // (With the walk in every role the registers spilled, into an L1 that shared
 // memory leaves 20 KB: 3.3 ms for a prompt of 8192, 32 heads.)
-// TMEM: S_A, S_B, O_A, O_B, 128 columns each; a tile's f16 P overwrites the
-// first half of its S.  The MMAs run in issue order, so QK_X(g+1) overwrites
-// S_X only after PV_X(g) has read P_X(g), and the commit behind QK_X(g+1) says
-// that PV_X(g) is done before O_X may be rescaled.
+// TMEM: two S of 64 columns for each tile, O_A, O_B of 128; a step's f16 P
+// overwrites the first half of its S.  S(g+1) is ready when the softmax of g
+// ends: with 128-key tiles only one S a tile fits beside O, and the chain
+// QK - softmax - PV took 5,600 cycles for 128 keys (0.76 ms for the prompt of
+// 8192).  The MMAs run in issue order, so QK_X(g+2) overwrites an S only after
+// PV_X(g) has read its P.
 //
 // The softmax reads S once: P = 2^(y - m) with the m at hand (see kSetP,
 // kMaxP), and only when some y of 32 columns exceeds the range are m, O, the
@@ -46,21 +48,25 @@
 namespace qpkv {
 namespace {
 
-constexpr int kT = 128;
-constexpr int kWarps = 14, kThreads = kWarps * 32;
-constexpr int kSoftA = 4, kSoftB = 8, kMma = 12, kWalk = 13;
+constexpr int kT = 128;                       // query rows of a tile
+constexpr int kN = 64;                        // keys of a tile
+constexpr int kGroups = kN / 16;
+constexpr int kWarps = 15, kThreads = kWarps * 32;
+constexpr int kSoftA = 4, kSoftB = 8, kMma = 12, kWalk = 13;   // tile B's MMAs: the warp behind kWalk
 constexpr int kLoad = 128;                    // threads of the load warps
-constexpr int kHalf = kT * 128;               // 16 KB: 128 rows of 64 f16
-constexpr uint32_t kColS = 0, kColO = 256;
+constexpr int kHalf = kT * 128;               // 16 KB: 128 rows of 64 f16 (Q)
+constexpr int kHalfKv = kN * 128;             // 8 KB: 64 keys of 64 f16
+constexpr int kRing = 4;                      // K and V tiles in shared memory
+constexpr uint32_t kColS = 0, kColO = 256;    // S: [tile][2] of 64 columns
 constexpr uint32_t kBadPageMark = 0x7FFFDEADu;   // in the place of a key scale: skip the group
-constexpr int kSteps = 4;                     // ring of steps
-constexpr int kOverhead = 2;
+constexpr int kSteps = 8;                     // ring of steps
+constexpr int kOverhead = 5;
 
 // One step of the CTA: a key tile of one (item, kv head).
 enum : int { kFirst = 1, kLast = 2, kHasB = 4, kWholeTask = 8, kEnd = 16 };
 struct Step {
-  float4 sc[8];       // per 16 keys: ks, log2 vs, 1 / vs
-  int at[8];          // per 16 keys: first pool row, -1: no keys
+  float4 sc[kGroups]; // per 16 keys: ks, log2 vs, 1 / vs
+  int at[kGroups];    // per 16 keys: first pool row, -1: no keys
   int flags;
   int j0;             // first key
   int seg;            // segments (runs of steps of one (item, kv head)) before this one
@@ -71,19 +77,24 @@ struct Step {
 
 template <int D>
 struct Smem {
-  static constexpr int kOp = D / 64 * kHalf;  // one operand tile
-  static constexpr int kQ = 0, kK = 2 * kOp, kV = 4 * kOp;
-  static constexpr int kBytes = 6 * kOp + 1024;
+  static constexpr int kOp = D / 64 * kHalf;      // a tile of Q
+  static constexpr int kOpKv = D / 64 * kHalfKv;  // a tile of K or V
+  static constexpr int kQ = 0, kK = 2 * kOp, kV = kK + kRing * kOpKv;
+  static constexpr int kBytes = kV + kRing * kOpKv + 1024;
 };
 
 struct Shared {
   uint64_t q_raw, q_full, q_free;             // the queries' copy, their f16, their last use
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-  uint64_t s_full[2], p_ready[2], o_full[2];  // per tile A / B
-  uint64_t mma_done;
+  uint64_t k_full[kRing], k_empty[kRing], v_full[kRing], v_empty[kRing];
+  // per tile A / B; S and P per S buffer: a softmax warp may be a step ahead of
+  // another, whose arrival for its step must not be taken by that one's
+  uint64_t s_full[2][2], p_ready[2][2], o_done[2];
+  uint64_t mma_done[2];
   uint64_t step_full[kSteps], step_free[kSteps];
   Step step[kSteps];
-  float qsc[2][2][kT];                        // [segment parity][tile][row] logit multiplier
+  // [segment % 4][tile][row] logit multiplier: QK runs a step ahead of a softmax,
+  // so with segments of one step the queries' load is up to two ahead
+  float qsc[4][2][kT];
   long long seq_prefix[kThreads + 1];         // items before each thread's sequences
   long long unit_prefix[kThreads + 1];        // units before each thread's items
   long long w_sum[kWarps];
@@ -134,8 +145,8 @@ __device__ __forceinline__ int items_of(const TileArgs& a, const Rows& r) {
 __device__ __forceinline__ int key_tiles(const TileArgs& a, const Rows& r, int p, int* k0) {
   const int i0 = p * 2 * a.tq, i1 = min(r.n, i0 + 2 * a.tq) - 1;
   const int lo = row_lo(a.p, r, i0), hi = row_hi(a.p, r, i1);
-  *k0 = lo / kT;
-  return hi > lo ? (hi - 1) / kT - lo / kT + 1 : 0;
+  *k0 = lo / kN;
+  return hi > lo ? (hi - 1) / kN - lo / kN + 1 : 0;
 }
 __device__ __forceinline__ int units_of(int key_tiles) { return key_tiles > 0 ? key_tiles + kOverhead : 0; }
 
@@ -265,21 +276,26 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
   if (tid == 0) {
     mbar_init(&sh.q_raw, 1);
     mbar_init(&sh.q_full, kLoad / 32);
-    mbar_init(&sh.q_free, 1);
-    for (int i = 0; i < 2; ++i) {
+    mbar_init(&sh.q_free, 2);             // both tiles' MMAs
+    for (int i = 0; i < kRing; ++i) {
       mbar_init(&sh.k_full[i], kLoad / 32);
-      mbar_init(&sh.k_empty[i], 1);
+      mbar_init(&sh.k_empty[i], 2);
       mbar_init(&sh.v_full[i], kLoad / 32);
-      mbar_init(&sh.v_empty[i], 1);
-      mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_ready[i], 128);
-      mbar_init(&sh.o_full[i], 1);
+      mbar_init(&sh.v_empty[i], 2);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.s_full[i][0], 1);
+      mbar_init(&sh.s_full[i][1], 1);
+      mbar_init(&sh.p_ready[i][0], 128);
+      mbar_init(&sh.p_ready[i][1], 128);
+      mbar_init(&sh.o_done[i], 1);
     }
     for (int i = 0; i < kSteps; ++i) {
       mbar_init(&sh.step_full[i], 1);
-      mbar_init(&sh.step_free[i], 8);   // the softmax warps
+      mbar_init(&sh.step_free[i], 10);  // the softmax warps and the MMA threads
     }
-    mbar_init(&sh.mma_done, 1);
+    mbar_init(&sh.mma_done[0], 1);
+    mbar_init(&sh.mma_done[1], 1);
     sh.abort = 0;
     fence_mbar_init();
   }
@@ -357,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
 
   if (warp < kSoftA) {
     // --------------------------------------------------------------- loads
-    constexpr int kVecs = kT * D / 16 / kLoad;       // 16-byte vectors of a tile per thread
+    constexpr int kVecs = kN * D / 16 / kLoad;       // 16-byte vectors of a tile per thread
     constexpr int kRowVecs = D / 16;                 // vectors of a row
     constexpr int kRowsPer = kLoad / kRowVecs;       // rows of one round of loads
     const int row0 = tid / kRowVecs, c = tid % kRowVecs;
@@ -377,8 +393,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
     // lanes of the second 64-column half store theirs in the other order, so
     // that the eight lanes of a row cover all banks.
     const int swap = c >> 2 & 1, c0 = 2 * (c & 3);
-    const uint32_t off0 = (c >> 2) * kHalf + row0 * 128 + ((((c0 + swap) ^ row0) & 7) << 4);
-    const uint32_t off1 = (c >> 2) * kHalf + row0 * 128 + ((((c0 + 1 - swap) ^ row0) & 7) << 4);
+    const uint32_t off0 = (c >> 2) * kHalfKv + row0 * 128 + ((((c0 + swap) ^ row0) & 7) << 4);
+    const uint32_t off1 = (c >> 2) * kHalfKv + row0 * 128 + ((((c0 + 1 - swap) ^ row0) & 7) << 4);
     auto store = [&](uint8_t* dst, const uint4 (&v)[kVecs], int valid) {
 #pragma unroll
       for (int k = 0; k < kVecs; ++k) {
@@ -425,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
           }
           float inv;
           const float mul = q_to_f16_scale(amax, &inv);
-          sh.qsc[seg & 1][tile][tid] = inv * (kCap ? a.scale_cap : a.scale_log2);
+          sh.qsc[seg & 3][tile][tid] = inv * (kCap ? a.scale_cap : a.scale_log2);
 #pragma unroll 4
           for (int k = 0; k < D / 8; ++k) {
             uint4* at = reinterpret_cast<uint4*>(row + (k >> 3) * kHalf + (((k ^ tid) & 7) << 4));
@@ -450,8 +466,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
     }
     for (int g = 0; more; ++g) {
       const Step& s = sh.step[g % kSteps];
-      const int bsel = g & 1;
-      const uint32_t ph = (g >> 1) & 1;
+      const int bsel = g % kRing;
+      const uint32_t ph = (g / kRing) & 1;
       if (s.flags & kFirst) {
         if (!warp_await(&sh.q_free, (s.seg & 1) ^ 1, sh, a.err)) break;
         if (!load_q(s)) break;
@@ -461,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
       }
       const int left = s.len - s.j0;                 // keys of this tile that exist
       if (!warp_await(&sh.k_empty[bsel], ph ^ 1, sh, a.err)) break;
-      store(smem + L::kK + bsel * L::kOp, kv, kT);
+      store(smem + L::kK + bsel * L::kOpKv, kv, kN);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.k_full[bsel]);
@@ -471,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
       more = !(s1.flags & kEnd);
       if (more) load(a.k, s1, kv);
       if (!warp_await(&sh.v_empty[bsel], ph ^ 1, sh, a.err)) break;
-      store(smem + L::kV + bsel * L::kOp, vv, left);
+      store(smem + L::kV + bsel * L::kOpKv, vv, left);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.v_full[bsel]);
@@ -482,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
   } else if (warp == kWalk) {
     // ---------------------------------------------------------------- walk
     // Three steps are in hand: the oldest is written, the middle one waits for
-    // its scales, the newest for its page ids (lane l < 8: 16 keys each).
+    // its scales, the newest for its page ids (lane l < 4: 16 keys each).
     const int gpp = a.ps / 16;
     Walk w;
     w.start(ta, lay, sh);
@@ -503,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
       if (w.valid()) {
         x[2].flags = (w.j == 0 ? kFirst : 0) | (w.j == w.count - 1 ? kLast : 0) | (w.has_b ? kHasB : 0) |
                      (w.count == w.nk ? kWholeTask : 0);
-        x[2].j0 = w.key_tile() * kT;
+        x[2].j0 = w.key_tile() * kN;
         x[2].seg = w.seg;
         x[2].t0 = w.it.r.t0, x[2].n = w.it.r.n, x[2].len = w.it.r.len, x[2].prefix = w.it.r.prefix;
         x[2].h = w.h;
@@ -520,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
       const int oat = at[0];
       // x[1]: its page ids are here, its scales are asked for
       at[0] = -1;
-      if (x[1].flags >= 0 && lane < 8 && page[0] != INT_MIN) {
+      if (x[1].flags >= 0 && lane < kGroups && page[0] != INT_MIN) {
         const int gi = (x[1].j0 >> 4) + lane;
         if (page[0] >= 0 && page[0] < a.num_pages) {
           at[0] = (a.hnd ? page[0] * a.Hkv + x[1].h : page[0]) * a.ps + (gi % gpp) * 16;
@@ -533,14 +549,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
       }
       // x[2]: its page ids are asked for (INT_MIN: no keys there)
       page[0] = INT_MIN;
-      if (lane < 8 && x[2].flags >= 0) {
+      if (lane < kGroups && x[2].flags >= 0) {
         const int gi = (x[2].j0 >> 4) + lane;
         if (gi * 16 < x[2].len) page[0] = __ldg(x[2].bt + gi / gpp);
       }
       if (x[0].flags >= 0) {
         if (!warp_await(&sh.step_free[g % kSteps], ((g / kSteps) & 1) ^ 1, sh, a.err)) break;
         Step& s = sh.step[g % kSteps];
-        if (lane < 8) {
+        if (lane < kGroups) {
           s.at[lane] = oat;
           const float sv = ovs == 0.f ? 1.f : fmaxf(ovs, kMinScale);
           s.sc[lane] = make_float4(oat >= 0 ? oks : __uint_as_float(kBadPageMark), log2f(sv), 1.f / sv, 0.f);
@@ -555,72 +571,83 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
         if (x[0].flags & kEnd) break;
       }
     }
-  } else if (warp == kMma) {
+  } else if (warp >= kMma) {
     // ----------------------------------------------------------------- MMA
     if (lane == 0) {
-      const uint32_t idesc_qk = make_idesc(kFmtF16, kFmtF16, 0, 0, kT, kT);
+      const int x = warp == kMma ? 0 : 1;            // tile A or B
+      const uint32_t idesc_qk = make_idesc(kFmtF16, kFmtF16, 0, 0, kT, kN);
       const uint32_t idesc_pv = make_idesc(kFmtF16, kFmtF16, 0, 1, kT, D);
-      const uint64_t qdesc = make_smem_desc(smem_u32(smem + L::kQ), 16, 1024, kSwizzle128B);
+      const uint64_t qdesc = make_smem_desc(smem_u32(smem + L::kQ + x * L::kOp), 16, 1024, kSwizzle128B);
       const uint64_t kdesc = make_smem_desc(smem_u32(smem + L::kK), 16, 1024, kSwizzle128B);
-      // MN-major V: 64-column atoms 16 KB apart, 16 key rows (2 KB) per K = 16 step
-      const uint64_t vdesc = make_smem_desc(smem_u32(smem + L::kV), kHalf, 1024, kSwizzle128B);
-      int cnt_p[2] = {0, 0};      // PVs issued per tile (p_ready phases)
-      int pend[2] = {-1, -1};     // flags of the step whose PV is due, by tile
-      bool ok = true;
-      // PV_x of step g - 1
-      auto pv = [&](int x, int g1) -> bool {
-        if (!await(&sh.p_ready[x], cnt_p[x] & 1, sh, a.err)) return false;
-        if (!await(&sh.v_full[g1 & 1], (g1 >> 1) & 1, sh, a.err)) return false;
-        tc_fence_after_sync();
-        const uint64_t db = vdesc + static_cast<uint64_t>(((g1 & 1) * L::kOp) >> 4);
-        const uint32_t cs = tmem + kColS + 128u * x, co = tmem + kColO + 128u * x;
-#pragma unroll
-        for (int kk = 0; kk < kT / 16; ++kk)
-          tc_mma_f16_tmem_a(co, cs + 8 * kk, db + static_cast<uint64_t>((kk * 16 * 128) >> 4), idesc_pv,
-                            (!(pend[x] & kFirst) || kk > 0) ? 1u : 0u);
-        if (x == (pend[x] & kHasB ? 1 : 0)) tc_commit(&sh.v_empty[g1 & 1]);   // the last reader of V
-        if (pend[x] & kLast) tc_commit(&sh.o_full[x]);
-        ++cnt_p[x];
-        pend[x] = -1;
-        return true;
+      // MN-major V: 64-column atoms 8 KB apart, 16 key rows (2 KB) per K = 16 step
+      const uint64_t vdesc = make_smem_desc(smem_u32(smem + L::kV), kHalfKv, 1024, kSwizzle128B);
+      const uint32_t scol = tmem + kColS + 128u * x, ocol = tmem + kColO + 128u * x;
+      int cnt_s = 0, cnt_p = 0;                      // QKs and PVs issued
+      // the other tile's arrival too in a segment without tile B
+      auto release = [&](uint64_t* bar, int flags) {
+        tc_commit(bar);
+        if (!(flags & kHasB)) tc_commit(bar);
       };
-      auto qk = [&](int x, int g, int flags, int seg) -> bool {
+      auto qk = [&](int g, int flags, int seg) -> bool {
         if ((flags & kFirst) && !await(&sh.q_full, seg & 1, sh, a.err)) return false;
-        if (!await(&sh.k_full[g & 1], (g >> 1) & 1, sh, a.err)) return false;
+        if (!await(&sh.k_full[g % kRing], (g / kRing) & 1, sh, a.err)) return false;
         tc_fence_after_sync();
-        const uint64_t da = qdesc + static_cast<uint64_t>((x * L::kOp) >> 4);
-        const uint64_t db = kdesc + static_cast<uint64_t>(((g & 1) * L::kOp) >> 4);
-        const uint32_t cs = tmem + kColS + 128u * x;
+        const uint64_t db = kdesc + static_cast<uint64_t>(((g % kRing) * L::kOpKv) >> 4);
+        const uint32_t cs = scol + 64u * (cnt_s & 1);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
-          tc_mma_f16(cs, da + (off >> 4), db + (off >> 4), idesc_qk, kk > 0);
-        }
-        tc_commit(&sh.s_full[x]);
-        if (x == (flags & kHasB ? 1 : 0)) {   // the last reader of K and, at the end, Q
-          tc_commit(&sh.k_empty[g & 1]);
-          if (flags & kLast) tc_commit(&sh.q_free);
-        }
-        pend[x] = flags;
+        for (int kk = 0; kk < D / 16; ++kk)
+          tc_mma_f16(cs, qdesc + (((kk >> 2) * kHalf + (kk & 3) * 32) >> 4), db + (((kk >> 2) * kHalfKv + (kk & 3) * 32) >> 4),
+                     idesc_qk, kk > 0);
+        tc_commit(&sh.s_full[x][cnt_s & 1]);
+        release(&sh.k_empty[g % kRing], flags);
+        if (flags & kLast) release(&sh.q_free, flags);
+        ++cnt_s;
         return true;
       };
-      // step g: PV_A(g-1) QK_A(g) PV_B(g-1) QK_B(g)
-      int g = 0;
-      for (; ok; ++g) {
-        ok = await(&sh.step_full[g % kSteps], (g / kSteps) & 1, sh, a.err);
-        if (!ok) break;
-        const int flags = sh.step[g % kSteps].flags, seg = sh.step[g % kSteps].seg;
-        const bool end = flags & kEnd;
-        if (pend[0] >= 0) ok = pv(0, g - 1);
-        if (ok && !end) ok = qk(0, g, flags, seg);
-        if (ok && pend[1] >= 0) ok = pv(1, g - 1);
-        if (ok && !end && (flags & kHasB)) ok = qk(1, g, flags, seg);
-        if (end) break;
+      auto pv = [&](int g, int flags) -> bool {
+        if (!await(&sh.p_ready[x][cnt_p & 1], (cnt_p >> 1) & 1, sh, a.err)) return false;
+        if (!await(&sh.v_full[g % kRing], (g / kRing) & 1, sh, a.err)) return false;
+        tc_fence_after_sync();
+        const uint64_t db = vdesc + static_cast<uint64_t>(((g % kRing) * L::kOpKv) >> 4);
+        const uint32_t cs = scol + 64u * (cnt_p & 1);
+#pragma unroll
+        for (int kk = 0; kk < kN / 16; ++kk)
+          tc_mma_f16_tmem_a(ocol, cs + 8 * kk, db + static_cast<uint64_t>((kk * 16 * 128) >> 4), idesc_pv,
+                            (!(flags & kFirst) || kk > 0) ? 1u : 0u);
+        release(&sh.v_empty[g % kRing], flags);
+        tc_commit(&sh.o_done[x]);
+        ++cnt_p;
+        return true;
+      };
+      // the next step from g on that this tile takes part in, its flags and segment
+      bool ok = true;
+      int flags = 0, seg = 0;
+      auto find = [&](int g) {
+        for (; ok; ++g) {
+          ok = await(&sh.step_full[g % kSteps], (g / kSteps) & 1, sh, a.err);
+          if (!ok) break;
+          flags = sh.step[g % kSteps].flags;
+          seg = sh.step[g % kSteps].seg;
+          mbar_arrive(&sh.step_free[g % kSteps]);
+          if ((flags & kEnd) || x == 0 || (flags & kHasB)) break;
+        }
+        return g;
+      };
+      // QK(g+1) PV(g); the first QK of a segment comes behind the last PV of the
+      // one before, as its queries take a while
+      int g = find(0);
+      if (ok && !(flags & kEnd)) ok = qk(g, flags, seg);
+      while (ok && !(flags & kEnd)) {
+        const int g0 = g, f0 = flags;
+        if (f0 & kLast) ok = pv(g0, f0);
+        if (ok) g = find(g0 + 1);
+        if (ok && !(flags & kEnd)) ok = qk(g, flags, seg);
+        if (ok && !(f0 & kLast)) ok = pv(g0, f0);
       }
       // every MMA issued here completes before TMEM is released
-      tc_commit(&sh.mma_done);
+      tc_commit(&sh.mma_done[x]);
       const long long t0 = clock64();
-      while (!mbar_try_wait(&sh.mma_done, 0)) {
+      while (!mbar_try_wait(&sh.mma_done[x], 0)) {
         if (clock64() - t0 > kWaitTimeoutCycles) {
           report_error(a.err, kDevErrTimeout);
           break;
@@ -633,13 +660,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
     const int x = warp < kSoftB ? 0 : 1;          // tile A or B
     const int r = (warp & 3) * 32 + lane;         // tile row = TMEM lane
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t srow = tmem + lane_base + kColS + 128u * x;
+    const uint32_t srow2 = tmem + lane_base + kColS + 128u * x;
     const uint32_t orow = tmem + lane_base + kColO + 128u * x;
-    int cnt = 0, units = 0;                       // steps and segments of this tile
+    int cnt = 0;                                  // steps of this tile
     float m = 0.f, l = 0.f, sc = 0.f, slope = 0.f;
     bool seen = false;
     int hi = 0, lo = 0, at = 0;
-    bool live = false;
+    bool live = false, dead = false;
     for (int g = 0;; ++g) {
       if (!warp_await(&sh.step_full[g % kSteps], (g / kSteps) & 1, sh, a.err)) break;
       const Step& st = sh.step[g % kSteps];
@@ -661,13 +688,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
         m = l = 0.f;
         seen = !live;         // dead rows never wait for a key
       }
-      if (!warp_await(&sh.s_full[x], cnt & 1, sh, a.err)) break;
+      if (!warp_await(&sh.s_full[x][cnt & 1], (cnt >> 1) & 1, sh, a.err)) break;
       tc_fence_after_sync();
+      const uint32_t srow = srow2 + 64u * (cnt & 1);
       if (flags & kFirst)
-        sc = std::is_same<E, __half>::value ? (kCap ? a.scale_cap : a.scale_log2) : sh.qsc[st.seg & 1][x][r];
+        sc = std::is_same<E, __half>::value ? (kCap ? a.scale_cap : a.scale_log2) : sh.qsc[st.seg & 3][x][r];
       const float4* gs = st.sc;
       const int j0 = st.j0;
-      const bool whole = __all_sync(0xffffffffu, !live || (lo <= j0 && j0 + kT <= hi));
+      const bool whole = __all_sync(0xffffffffu, !live || (lo <= j0 && j0 + kN <= hi));
 
       // z = y - m of 32 columns, -inf for keys the row does not see
       auto logits = [&](int c, uint32_t (&v)[32]) {
@@ -716,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
       if (__any_sync(0xffffffffu, !seen)) {   // rows without a key so far: their maximum first
         float top = -INFINITY;
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < kN / 32; ++c) {
           uint32_t v[32];
           logits(c, v);
           top = fmaxf(top, top_of(v));
@@ -727,13 +755,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
         }
       }
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < kN / 32; ++c) {
         uint32_t v[32];
         logits(c, v);
         const float top = top_of(v);
         if (__any_sync(0xffffffffu, top > kMaxP)) {
-          // move m; everything so far is scaled to it.  The previous PV of this
-          // tile is complete: it was issued before the QK that s_full saw.
+          // move m; everything so far is scaled to it, O once its last PV has landed
+          if (!(flags & kFirst) && !warp_await(&sh.o_done[x], (cnt - 1) & 1, sh, a.err)) {
+            dead = true;
+            break;
+          }
+          tc_fence_after_sync();
           const float d = seen ? fmaxf(top - kSetP, 0.f) : 0.f;
           const float f = fast_exp2(-d);
           m += d;
@@ -781,13 +813,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
         }
         tmem_st16(srow + 16 * c, pk);
       }
+      if (dead) break;
       tmem_st_wait();
       tc_fence_before_sync();
-      mbar_arrive(&sh.p_ready[x]);
+      mbar_arrive(&sh.p_ready[x][cnt & 1]);
       ++cnt;
       if (flags & kLast) {
         // ---- the segment's rows, once its last PV has landed
-        if (!warp_await(&sh.o_full[x], units & 1, sh, a.err)) break;
+        if (!warp_await(&sh.o_done[x], (cnt - 1) & 1, sh, a.err)) break;
         tc_fence_after_sync();
         const float lse2 = seen && l > 0.f ? m + log2f(l) : -INFINITY;
         if (flags & kWholeTask) {
@@ -829,7 +862,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
           if (live) ta.part_ml[pr] = make_float2(seen ? m : -INFINITY, l);
         }
         tc_fence_before_sync();
-        ++units;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.step_free[g % kSteps]);
