@@ -135,6 +135,35 @@ __device__ __forceinline__ bool warp_await(uint64_t* bar, uint32_t parity, Share
   return ok;
 }
 
+// MMAs and commits issued by one elected lane of a converged warp.  The warp
+// computes the operands, which so stay in uniform registers; in code of a
+// single lane each MMA first moved them there.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
+      : "memory");
+}
+
 // Items of a sequence: pairs of tiles, none for one that the split form takes.
 __device__ __forceinline__ int items_of(const TileArgs& a, const Rows& r) {
   if (r.n <= 0 || r.n * a.p.G <= a.p.split_rows) return 0;
@@ -573,49 +602,50 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
     }
   } else if (warp >= kMma) {
     // ----------------------------------------------------------------- MMA
-    if (lane == 0) {
-      const int x = warp == kMma ? 0 : 1;            // tile A or B
+    {
+      const int x = __shfl_sync(0xffffffffu, warp == kMma ? 0 : 1, 0);   // tile A or B, the same in all lanes
+      const uint32_t tmem_u = __shfl_sync(0xffffffffu, tmem, 0);
       const uint32_t idesc_qk = make_idesc(kFmtF16, kFmtF16, 0, 0, kT, kN);
       const uint32_t idesc_pv = make_idesc(kFmtF16, kFmtF16, 0, 1, kT, D);
       const uint64_t qdesc = make_smem_desc(smem_u32(smem + L::kQ + x * L::kOp), 16, 1024, kSwizzle128B);
       const uint64_t kdesc = make_smem_desc(smem_u32(smem + L::kK), 16, 1024, kSwizzle128B);
       // MN-major V: 64-column atoms 8 KB apart, 16 key rows (2 KB) per K = 16 step
       const uint64_t vdesc = make_smem_desc(smem_u32(smem + L::kV), kHalfKv, 1024, kSwizzle128B);
-      const uint32_t scol = tmem + kColS + 128u * x, ocol = tmem + kColO + 128u * x;
+      const uint32_t scol = tmem_u + kColS + 128u * x, ocol = tmem_u + kColO + 128u * x;
       int cnt_s = 0, cnt_p = 0;                      // QKs and PVs issued
       // the other tile's arrival too in a segment without tile B
       auto release = [&](uint64_t* bar, int flags) {
-        tc_commit(bar);
-        if (!(flags & kHasB)) tc_commit(bar);
+        commit(bar);
+        if (!(flags & kHasB)) commit(bar);
       };
       auto qk = [&](int g, int flags, int seg) -> bool {
-        if ((flags & kFirst) && !await(&sh.q_full, seg & 1, sh, a.err)) return false;
-        if (!await(&sh.k_full[g % kRing], (g / kRing) & 1, sh, a.err)) return false;
+        if ((flags & kFirst) && !warp_await(&sh.q_full, seg & 1, sh, a.err)) return false;
+        if (!warp_await(&sh.k_full[g % kRing], (g / kRing) & 1, sh, a.err)) return false;
         tc_fence_after_sync();
         const uint64_t db = kdesc + static_cast<uint64_t>(((g % kRing) * L::kOpKv) >> 4);
         const uint32_t cs = scol + 64u * (cnt_s & 1);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          tc_mma_f16(cs, qdesc + (((kk >> 2) * kHalf + (kk & 3) * 32) >> 4), db + (((kk >> 2) * kHalfKv + (kk & 3) * 32) >> 4),
+          mma_ss(cs, qdesc + (((kk >> 2) * kHalf + (kk & 3) * 32) >> 4), db + (((kk >> 2) * kHalfKv + (kk & 3) * 32) >> 4),
                      idesc_qk, kk > 0);
-        tc_commit(&sh.s_full[x][cnt_s & 1]);
+        commit(&sh.s_full[x][cnt_s & 1]);
         release(&sh.k_empty[g % kRing], flags);
         if (flags & kLast) release(&sh.q_free, flags);
         ++cnt_s;
         return true;
       };
       auto pv = [&](int g, int flags) -> bool {
-        if (!await(&sh.p_ready[x][cnt_p & 1], (cnt_p >> 1) & 1, sh, a.err)) return false;
-        if (!await(&sh.v_full[g % kRing], (g / kRing) & 1, sh, a.err)) return false;
+        if (!warp_await(&sh.p_ready[x][cnt_p & 1], (cnt_p >> 1) & 1, sh, a.err)) return false;
+        if (!warp_await(&sh.v_full[g % kRing], (g / kRing) & 1, sh, a.err)) return false;
         tc_fence_after_sync();
         const uint64_t db = vdesc + static_cast<uint64_t>(((g % kRing) * L::kOpKv) >> 4);
         const uint32_t cs = scol + 64u * (cnt_p & 1);
 #pragma unroll
         for (int kk = 0; kk < kN / 16; ++kk)
-          tc_mma_f16_tmem_a(ocol, cs + 8 * kk, db + static_cast<uint64_t>((kk * 16 * 128) >> 4), idesc_pv,
+          mma_ts(ocol, cs + 8 * kk, db + static_cast<uint64_t>((kk * 16 * 128) >> 4), idesc_pv,
                             (!(flags & kFirst) || kk > 0) ? 1u : 0u);
         release(&sh.v_empty[g % kRing], flags);
-        tc_commit(&sh.o_done[x]);
+        commit(&sh.o_done[x]);
         ++cnt_p;
         return true;
       };
@@ -624,11 +654,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
       int flags = 0, seg = 0;
       auto find = [&](int g) {
         for (; ok; ++g) {
-          ok = await(&sh.step_full[g % kSteps], (g / kSteps) & 1, sh, a.err);
+          ok = warp_await(&sh.step_full[g % kSteps], (g / kSteps) & 1, sh, a.err);
           if (!ok) break;
-          flags = sh.step[g % kSteps].flags;
-          seg = sh.step[g % kSteps].seg;
-          mbar_arrive(&sh.step_free[g % kSteps]);
+          const int both = __shfl_sync(0xffffffffu, sh.step[g % kSteps].flags | sh.step[g % kSteps].seg << 8, 0);
+          flags = both & 0xFF;
+          seg = both >> 8;
+          if (lane == 0) mbar_arrive(&sh.step_free[g % kSteps]);
+          __syncwarp();
           if ((flags & kEnd) || x == 0 || (flags & kHasB)) break;
         }
         return g;
@@ -645,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
         if (ok && !(f0 & kLast)) ok = pv(g0, f0);
       }
       // every MMA issued here completes before TMEM is released
-      tc_commit(&sh.mma_done[x]);
+      commit(&sh.mma_done[x]);
       const long long t0 = clock64();
       while (!mbar_try_wait(&sh.mma_done[x], 0)) {
         if (clock64() - t0 > kWaitTimeoutCycles) {
