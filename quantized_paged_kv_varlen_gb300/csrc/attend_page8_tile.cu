@@ -7,17 +7,18 @@
 // item is a pair of tiles A and B, run side by side over one stream of 64-key
 // tiles: while one tile's softmax computes its exponentials the tensor core
 // works on the other, and each K/V tile is fetched and widened once for both.  One persistent CTA per SM, 15 warps:
-//   warps 0-3   loads: K and V codes come straight from the pages into
-//               registers one key tile ahead (16 bytes a lane, whole rows) and
-//               go widened to f16 (exact) into the operand layouts; the
-//               item's queries as f16 (bf16 rows times a power of two)
+//   warps 0-3   widen K and V codes to f16 (exact), from the raw ring into the
+//               operand layouts; the item's queries as f16 (bf16 rows times a
+//               power of two)
 //   warps 4-7   softmax and epilogue of tile A, one thread per row
 //   warps 8-11  the same for tile B
 //   warps 12, 14  one thread each issues the tcgen05.mma of tile A and tile B:
 //               per key tile g QK(g+1) PV(g) (one thread for both tiles took
 //               3,600 cycles a step to issue 24 of them)
 //   warp 13     walks the work: writes for every step what the others need (the
-//               item, the pages' rows, the scales) into a ring of eight
+//               item, the scales) into a ring of eight, and issues the copies of
+//               its keys, a TMA box for 16 of them, into the raw ring (loads into
+//               registers by warps 0-3 took them 1,100 cycles a step to issue)
 // (With the walk in every role the registers spilled, into an L1 that shared
 // memory leaves 20 KB: 3.3 ms for a prompt of 8192, 32 heads.)
 // TMEM: two S of 64 columns for each tile, O_A, O_B of 128; a step's f16 P
@@ -56,14 +57,15 @@ constexpr int kSoftA = 4, kSoftB = 8, kMma = 12, kWalk = 13;   // tile B's MMAs:
 constexpr int kLoad = 128;                    // threads of the load warps
 constexpr int kHalf = kT * 128;               // 16 KB: 128 rows of 64 f16 (Q)
 constexpr int kHalfKv = kN * 128;             // 8 KB: 64 keys of 64 f16
-constexpr int kRing = 4;                      // K and V tiles in shared memory
+constexpr int kRing = 3;                      // K and V tiles as f16
+constexpr int kRaw = 3;                       // K and V tiles as codes
 constexpr uint32_t kColS = 0, kColO = 256;    // S: [tile][2] of 64 columns
 constexpr uint32_t kBadPageMark = 0x7FFFDEADu;   // in the place of a key scale: skip the group
 constexpr int kSteps = 8;                     // ring of steps
 constexpr int kOverhead = 5;
 
 // One step of the CTA: a key tile of one (item, kv head).
-enum : int { kFirst = 1, kLast = 2, kHasB = 4, kWholeTask = 8, kEnd = 16 };
+enum : int { kFirst = 1, kLast = 2, kHasB = 4, kWholeTask = 8, kEnd = 16, kAllKeys = 32 };
 struct Step {
   float4 sc[kGroups]; // per 16 keys: ks, log2 vs, 1 / vs
   int at[kGroups];    // per 16 keys: first pool row, -1: no keys
@@ -79,8 +81,10 @@ template <int D>
 struct Smem {
   static constexpr int kOp = D / 64 * kHalf;      // a tile of Q
   static constexpr int kOpKv = D / 64 * kHalfKv;  // a tile of K or V
+  static constexpr int kRawTile = kN * D;         // codes of K or V
   static constexpr int kQ = 0, kK = 2 * kOp, kV = kK + kRing * kOpKv;
-  static constexpr int kBytes = kV + kRing * kOpKv + 1024;
+  static constexpr int kCodes = kV + kRing * kOpKv;
+  static constexpr int kBytes = kCodes + 2 * kRaw * kRawTile + 1024;
 };
 
 struct Shared {
@@ -91,6 +95,7 @@ struct Shared {
   uint64_t s_full[2][2], p_ready[2][2], o_done[2];
   uint64_t mma_done[2];
   uint64_t step_full[kSteps], step_free[kSteps];
+  uint64_t raw_full[kRaw], raw_empty[kRaw];
   Step step[kSteps];
   // [segment % 4][tile][row] logit multiplier: QK runs a step ahead of a softmax,
   // so with segments of one step the queries' load is up to two ahead
@@ -116,15 +121,6 @@ __device__ __forceinline__ bool await(uint64_t* bar, uint32_t parity, Shared& sh
       return false;
     }
   }
-}
-
-// 16 bytes that are used once: past L1, and issued where it is written.
-__device__ __forceinline__ uint4 load_stream(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
 }
 
 // All lanes wait, and go on converged.  (One lane polling and a shuffle of the
@@ -247,7 +243,7 @@ struct Walk {
   int h, first, count;   // kv head; steps [first, first + count) of nk, newest key tile first
   int skip;              // units of the segment
   int has_b, seg;
-  int j, g;              // step in the segment, step of the CTA
+  int j;                 // step in the segment
   __device__ __forceinline__ void open(const TileArgs& a) {
     // from u on, the next (item, kv head) with a key tile in this run
     while (u < u_end) {
@@ -271,7 +267,7 @@ struct Walk {
     const long long total = sh.unit_prefix[kThreads];
     u = u_begin = blockIdx.x * lay.run;
     u_end = min(total, u + lay.run);
-    seg = j = g = 0;
+    seg = j = 0;
     if (u >= u_end) return;
     const int c = chunk_of(sh.unit_prefix, u);
     const long long idx = c * lay.per_item;
@@ -283,9 +279,10 @@ struct Walk {
   }
   __device__ __forceinline__ bool valid() const { return u < u_end; }
   __device__ __forceinline__ int key_tile() const { return k0 + nk - 1 - first - j; }
-  __device__ __forceinline__ void next(const TileArgs& a) {
-    ++g;
-    if (++j < count) return;
+  // n steps on, at most to the segment's end
+  __device__ __forceinline__ void advance(const TileArgs& a, int n) {
+    j += n;
+    if (j < count) return;
     j = 0;
     u += skip;
     ++seg;
@@ -294,7 +291,8 @@ struct Walk {
 };
 
 template <typename E, int D, bool kInt8, bool kCap, bool kBias>
-__global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ TileArgs ta) {
+__global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
+                       const __grid_constant__ CUtensorMap v_map, const __grid_constant__ TileArgs ta) {
   using L = Smem<D>;
   const Page8Args& a = ta.p;
   extern __shared__ uint8_t smem_raw[];
@@ -318,6 +316,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
       mbar_init(&sh.p_ready[i][0], 128);
       mbar_init(&sh.p_ready[i][1], 128);
       mbar_init(&sh.o_done[i], 1);
+    }
+    for (int i = 0; i < kRaw; ++i) {
+      mbar_init(&sh.raw_full[i], 1);
+      mbar_init(&sh.raw_empty[i], kLoad / 32);
     }
     for (int i = 0; i < kSteps; ++i) {
       mbar_init(&sh.step_full[i], 1);
@@ -401,35 +403,28 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
   const uint32_t tmem = sh.tmem_base;
 
   if (warp < kSoftA) {
-    // --------------------------------------------------------------- loads
+    // --------------------------------------------------------------- widen
     constexpr int kVecs = kN * D / 16 / kLoad;       // 16-byte vectors of a tile per thread
     constexpr int kRowVecs = D / 16;                 // vectors of a row
-    constexpr int kRowsPer = kLoad / kRowVecs;       // rows of one round of loads
+    constexpr int kRowsPer = kLoad / kRowVecs;       // rows of one round, a multiple of 8:
+                                                     // the swizzles are the same in every round
     const int row0 = tid / kRowVecs, c = tid % kRowVecs;
-    const long long tok_bytes = a.hnd ? D : static_cast<long long>(a.Hkv) * D;
     int copies = 0;                                  // query loads that thread 0 has issued
-    auto load = [&](const uint8_t* pool, const Step& s, uint4 (&v)[kVecs]) {
-      const uint8_t* base = pool + (a.hnd ? 0 : s.h * D) + c * 16;
-#pragma unroll
-      for (int k = 0; k < kVecs; ++k) {
-        const int r = row0 + k * kRowsPer, at = s.at[r >> 4];
-        v[k] = make_uint4(0, 0, 0, 0);
-        if (at >= 0) v[k] = load_stream(base + (at + (r & 15)) * tok_bytes);
-      }
-    };
-    // widen and store into the 128-byte-swizzled operand tile; rows from
-    // `valid` on become zero.  A vector's 16 codes are two 16-byte chunks; the
-    // lanes of the second 64-column half store theirs in the other order, so
-    // that the eight lanes of a row cover all banks.
+    const uint32_t in0 = D == 128 ? row0 * 128 + (((c ^ row0) & 7) << 4) : row0 * 64 + (((c ^ (row0 >> 1)) & 3) << 4);
+    // A vector's 16 codes are two 16-byte chunks of f16; the lanes of the second
+    // 64-column half store theirs in the other order, so that the eight lanes of
+    // a row cover all banks.
     const int swap = c >> 2 & 1, c0 = 2 * (c & 3);
     const uint32_t off0 = (c >> 2) * kHalfKv + row0 * 128 + ((((c0 + swap) ^ row0) & 7) << 4);
     const uint32_t off1 = (c >> 2) * kHalfKv + row0 * 128 + ((((c0 + 1 - swap) ^ row0) & 7) << 4);
-    auto store = [&](uint8_t* dst, const uint4 (&v)[kVecs], int valid) {
+    // keys without codes (`all` false: behind the last, in a bad page) become zero
+    auto store = [&](uint8_t* dst, const uint8_t* src, const Step& s, bool all) {
 #pragma unroll
       for (int k = 0; k < kVecs; ++k) {
-        // kRowsPer is a multiple of 8: the swizzle is the same in every round
-        uint4 w = swap ? make_uint4(v[k].z, v[k].w, v[k].x, v[k].y) : v[k];
-        if (row0 + k * kRowsPer >= valid) w = make_uint4(0, 0, 0, 0);
+        const int r = row0 + k * kRowsPer;
+        const uint4 v = *reinterpret_cast<const uint4*>(src + in0 + k * kRowsPer * D);
+        uint4 w = swap ? make_uint4(v.z, v.w, v.x, v.y) : v;
+        if (!all && (s.j0 + r >= s.len || s.at[r >> 4] < 0)) w = make_uint4(0, 0, 0, 0);
         uint32_t o[8];
         widen<kInt8>(w.x, o[0], o[1]);
         widen<kInt8>(w.y, o[2], o[3]);
@@ -486,16 +481,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
       return true;
     };
 
-    uint4 kv[kVecs], vv[kVecs];
-    bool ok = warp_await(&sh.step_full[0], 0, sh, a.err);
-    bool more = ok && !(sh.step[0].flags & kEnd);
-    if (more) {
-      load(a.k, sh.step[0], kv);
-      load(a.v, sh.step[0], vv);
-    }
-    for (int g = 0; more; ++g) {
+    for (int g = 0;; ++g) {
+      if (!warp_await(&sh.step_full[g % kSteps], (g / kSteps) & 1, sh, a.err)) break;
       const Step& s = sh.step[g % kSteps];
-      const int bsel = g % kRing;
+      if (s.flags & kEnd) break;
       const uint32_t ph = (g / kRing) & 1;
       if (s.flags & kFirst) {
         if (!warp_await(&sh.q_free, (s.seg & 1) ^ 1, sh, a.err)) break;
@@ -504,102 +493,122 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.q_full);
       }
-      const int left = s.len - s.j0;                 // keys of this tile that exist
-      if (!warp_await(&sh.k_empty[bsel], ph ^ 1, sh, a.err)) break;
-      store(smem + L::kK + bsel * L::kOpKv, kv, kN);
+      const bool all = s.flags & kAllKeys;
+      const uint8_t* raw = smem + L::kCodes + (g % kRaw) * 2 * L::kRawTile;
+      if (!warp_await(&sh.raw_full[g % kRaw], (g / kRaw) & 1, sh, a.err)) break;
+      if (!warp_await(&sh.k_empty[g % kRing], ph ^ 1, sh, a.err)) break;
+      store(smem + L::kK + (g % kRing) * L::kOpKv, raw, s, all);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.k_full[bsel]);
-      const int n1 = g + 1;
-      if (!warp_await(&sh.step_full[n1 % kSteps], (n1 / kSteps) & 1, sh, a.err)) break;
-      const Step& s1 = sh.step[n1 % kSteps];
-      more = !(s1.flags & kEnd);
-      if (more) load(a.k, s1, kv);
-      if (!warp_await(&sh.v_empty[bsel], ph ^ 1, sh, a.err)) break;
-      store(smem + L::kV + bsel * L::kOpKv, vv, left);
+      if (lane == 0) mbar_arrive(&sh.k_full[g % kRing]);
+      if (!warp_await(&sh.v_empty[g % kRing], ph ^ 1, sh, a.err)) break;
+      store(smem + L::kV + (g % kRing) * L::kOpKv, raw + L::kRawTile, s, all);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.v_full[bsel]);
-      if (more) load(a.v, s1, vv);
+      if (lane == 0) {
+        mbar_arrive(&sh.v_full[g % kRing]);
+        mbar_arrive(&sh.raw_empty[g % kRaw]);
+      }
     }
     // a query load still on its way (after a wait that ran out) lands before the CTA ends
     if (tid == 0 && copies > 0) mbar_wait(&sh.q_raw, (copies - 1) & 1);
   } else if (warp == kWalk) {
     // ---------------------------------------------------------------- walk
-    // Three steps are in hand: the oldest is written, the middle one waits for
-    // its scales, the newest for its page ids (lane l < 4: 16 keys each).
-    const int gpp = a.ps / 16;
+    // Eight steps at a time, a lane for each 16 keys: the next eight are looked
+    // up before the ones in hand are written as the ring's places come free.
+    // (One step at a time took 2,600 cycles a step for its dependent loads, more
+    // than anything else in the kernel.)
+    constexpr int kBatch = 32 / kGroups;
+    const int gpp = a.ps / 16, mine = lane / kGroups, grp = lane % kGroups;
     Walk w;
     w.start(ta, lay, sh);
-    struct Ahead {
-      int flags, j0, seg, t0, n, len, prefix, h, i0, piece;
-      const int32_t* bt;
+    struct Batch {
+      int n;            // steps, 0: the end
+      int flags, j0;    // of the segment; first key of its first step
+      int seg, t0, rows, len, prefix, h, i0, piece;
+      int at;           // this lane's 16 keys
+      float ks, vs;
     };
-    int page[2] = {-1, -1}, at[2] = {-1, -1};      // [0] the older
-    float ks = 0.f, vs = 0.f;
-    Ahead x[3];
-    for (int i = 0; i < 3; ++i) x[i].flags = -1;   // nothing in hand
-    int g = 0;
-    bool done = false;
-    while (true) {
-      // the step behind the walk; -1 once it has ended
-      x[0] = x[1];
-      x[1] = x[2];
-      if (w.valid()) {
-        x[2].flags = (w.j == 0 ? kFirst : 0) | (w.j == w.count - 1 ? kLast : 0) | (w.has_b ? kHasB : 0) |
-                     (w.count == w.nk ? kWholeTask : 0);
-        x[2].j0 = w.key_tile() * kN;
-        x[2].seg = w.seg;
-        x[2].t0 = w.it.r.t0, x[2].n = w.it.r.n, x[2].len = w.it.r.len, x[2].prefix = w.it.r.prefix;
-        x[2].h = w.h;
-        x[2].i0 = w.it.p * 2 * ta.tq;
-        x[2].piece = 2 * blockIdx.x + (w.u == w.u_begin ? 0 : 1);
-        x[2].bt = a.bt + static_cast<size_t>(w.it.b) * a.bt_stride;
-        w.next(ta);
-      } else {
-        x[2].flags = done ? -1 : kEnd;
-        x[2].j0 = x[2].len = 0;
-        done = true;
-      }
-      const float oks = ks, ovs = vs;              // x[0]'s
-      const int oat = at[0];
-      // x[1]: its page ids are here, its scales are asked for
-      at[0] = -1;
-      if (x[1].flags >= 0 && lane < kGroups && page[0] != INT_MIN) {
-        const int gi = (x[1].j0 >> 4) + lane;
-        if (page[0] >= 0 && page[0] < a.num_pages) {
-          at[0] = (a.hnd ? page[0] * a.Hkv + x[1].h : page[0]) * a.ps + (gi % gpp) * 16;
-          const size_t sx = static_cast<size_t>(page[0]) * a.Hkv + x[1].h;
-          ks = __ldg(a.ks + sx);
-          vs = __ldg(a.vs + sx);
+    auto fetch = [&]() {
+      Batch x;
+      x.n = 0;
+      x.flags = kEnd;
+      x.j0 = x.seg = x.t0 = x.rows = x.len = x.prefix = x.h = x.i0 = x.piece = 0;
+      x.at = -1;
+      x.ks = x.vs = 0.f;
+      if (!w.valid()) return x;
+      x.n = min(kBatch, w.count - w.j);
+      x.flags = (w.has_b ? kHasB : 0) | (w.count == w.nk ? kWholeTask : 0) | (w.j == 0 ? kFirst : 0) |
+                (w.j + x.n == w.count ? kLast : 0);
+      x.j0 = w.key_tile() * kN;
+      x.seg = w.seg;
+      x.t0 = w.it.r.t0, x.rows = w.it.r.n, x.len = w.it.r.len, x.prefix = w.it.r.prefix;
+      x.h = w.h;
+      x.i0 = w.it.p * 2 * ta.tq;
+      x.piece = 2 * blockIdx.x + (w.u == w.u_begin ? 0 : 1);
+      const int gi = (x.j0 >> 4) - mine * kGroups + grp;
+      if (mine < x.n && gi * 16 < x.len) {
+        const int pg = gi / gpp;
+        const int page = __ldg(a.bt + static_cast<size_t>(w.it.b) * a.bt_stride + pg);
+        if (page >= 0 && page < a.num_pages) {
+          x.at = (a.hnd ? page * a.Hkv + x.h : page) * a.ps + (gi - pg * gpp) * 16;
+          const size_t sx = static_cast<size_t>(page) * a.Hkv + x.h;
+          x.ks = __ldg(a.ks + sx);
+          x.vs = __ldg(a.vs + sx);
         } else {
           report_error(a.err, kDevErrBadPage);
         }
       }
-      // x[2]: its page ids are asked for (INT_MIN: no keys there)
-      page[0] = INT_MIN;
-      if (lane < kGroups && x[2].flags >= 0) {
-        const int gi = (x[2].j0 >> 4) + lane;
-        if (gi * 16 < x[2].len) page[0] = __ldg(x[2].bt + gi / gpp);
-      }
-      if (x[0].flags >= 0) {
-        if (!warp_await(&sh.step_free[g % kSteps], ((g / kSteps) & 1) ^ 1, sh, a.err)) break;
+      w.advance(ta, x.n);
+      return x;
+    };
+    Batch x = fetch();
+    bool ok = true;
+    int issued = 0;
+    for (int g = 0; ok;) {
+      const Batch next = x.n > 0 ? fetch() : x;
+      const float sv = x.vs == 0.f ? 1.f : fmaxf(x.vs, kMinScale);
+      const float4 sc = make_float4(x.at >= 0 ? x.ks : __uint_as_float(kBadPageMark), log2f(sv), 1.f / sv, 0.f);
+      const int n = x.n > 0 ? x.n : 1;     // the end is a step too
+      for (int i = 0; i < n; ++i, ++g) {
+        ok = warp_await(&sh.step_free[g % kSteps], ((g / kSteps) & 1) ^ 1, sh, a.err);
+        if (!ok) break;
+        const bool here = mine == i && x.at >= 0;
+        const int keys = __popc(__ballot_sync(0xffffffffu, here && x.j0 - i * kN + grp * 16 + 16 <= x.len));
+        if (!(x.flags & kEnd)) {
+          // the codes: lane (i, grp) copies 16 keys of K and of V
+          ok = warp_await(&sh.raw_empty[g % kRaw], ((g / kRaw) & 1) ^ 1, sh, a.err);
+          if (!ok) break;
+          const int boxes = __popc(__ballot_sync(0xffffffffu, here));
+          uint8_t* raw = smem + L::kCodes + (g % kRaw) * 2 * L::kRawTile + grp * 16 * D;
+          if (lane == 0) mbar_arrive_expect_tx(&sh.raw_full[g % kRaw], boxes * 2 * 16 * D);
+          __syncwarp();
+          if (here) {
+            tma_load_3d(raw, &k_map, &sh.raw_full[g % kRaw], 0, a.hnd ? 0 : x.h, x.at);
+            tma_load_3d(raw + L::kRawTile, &v_map, &sh.raw_full[g % kRaw], 0, a.hnd ? 0 : x.h, x.at);
+          }
+          issued = g + 1;
+          __syncwarp();
+        }
         Step& s = sh.step[g % kSteps];
-        if (lane < kGroups) {
-          s.at[lane] = oat;
-          const float sv = ovs == 0.f ? 1.f : fmaxf(ovs, kMinScale);
-          s.sc[lane] = make_float4(oat >= 0 ? oks : __uint_as_float(kBadPageMark), log2f(sv), 1.f / sv, 0.f);
+        if (mine == i) {
+          s.at[grp] = x.at;
+          s.sc[grp] = sc;
         }
         if (lane == 0) {
-          s.flags = x[0].flags, s.j0 = x[0].j0, s.seg = x[0].seg, s.t0 = x[0].t0, s.n = x[0].n, s.len = x[0].len;
-          s.prefix = x[0].prefix, s.h = x[0].h, s.i0 = x[0].i0, s.piece = x[0].piece;
+          s.flags = (x.flags & ((i == 0 ? ~0 : ~kFirst) & (i == n - 1 ? ~0 : ~kLast))) | (keys == kGroups ? kAllKeys : 0);
+          s.j0 = x.j0 - i * kN, s.seg = x.seg, s.t0 = x.t0, s.n = x.rows, s.len = x.len;
+          s.prefix = x.prefix, s.h = x.h, s.i0 = x.i0, s.piece = x.piece;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.step_full[g % kSteps]);
-        ++g;
-        if (x[0].flags & kEnd) break;
       }
+      if (x.n == 0) break;
+      x = next;
     }
+    // copies still on their way (after a wait that ran out) land before the CTA ends
+    if (lane == 0)
+      for (int k = issued > kRaw ? issued - kRaw : 0; k < issued; ++k) mbar_wait(&sh.raw_full[k % kRaw], (k / kRaw) & 1);
   } else if (warp >= kMma) {
     // ----------------------------------------------------------------- MMA
     {
@@ -912,7 +921,8 @@ cudaError_t go(const TileArgs& a, int sms, cudaStream_t stream) {
   auto kernel = attend_tile_kernel<E, D, kInt8, kCap, kBias>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
   if (e != cudaSuccess) return e;
-  CUtensorMap q_map;
+  CUtensorMap q_map, k_map, v_map;
+  if (!pool_map(a.p, D, a.p.k, 16, &k_map) || !pool_map(a.p, D, a.p.v, 16, &v_map)) return cudaErrorInvalidValue;
   const uint64_t dims[3] = {D, static_cast<uint64_t>(a.p.Hq), static_cast<uint64_t>(a.p.T)};
   const uint64_t strides[2] = {D * 2, static_cast<uint64_t>(a.p.Hq) * D * 2};
   const uint32_t box[3] = {64, static_cast<uint32_t>(a.p.G), static_cast<uint32_t>(a.tq)};
@@ -929,7 +939,7 @@ cudaError_t go(const TileArgs& a, int sms, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, q_map, a);
+  return cudaLaunchKernelEx(&cfg, kernel, q_map, k_map, v_map, a);
 }
 
 template <typename E, int D, bool kInt8>
