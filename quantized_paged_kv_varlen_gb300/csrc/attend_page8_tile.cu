@@ -28,11 +28,10 @@
 // 8192).  The MMAs run in issue order, so QK_X(g+2) overwrites an S only after
 // PV_X(g) has read its P.
 //
-// The softmax reads S once: P = 2^(y - m) with the m at hand (see kSetP,
-// kMaxP), and only when some y of 32 columns exceeds the range are m, O, the
-// sums and this tile's earlier columns of P rescaled.  A row that has not seen
-// a key gets its m from a pass of its own.  Key tiles go from the newest back,
-// so that with a distance bias the first tile has the maximum.
+// The softmax reads S once, a row's 64 columns in registers: P = 2^(y - m)
+// with the m at hand (see kSetP, kMaxP), and only when some y exceeds the range
+// are m, O and the sums rescaled.  Key tiles go from the newest back, so that
+// with a distance bias the first tile has the maximum.
 //
 // Work is split without a plan, as in the other form: all (item, kv head, key
 // tile) units in a row are cut into equal runs, one per CTA; a run's first and
@@ -100,6 +99,7 @@ struct Shared {
   // [segment % 4][tile][row] logit multiplier: QK runs a step ahead of a softmax,
   // so with segments of one step the queries' load is up to two ahead
   float qsc[4][2][kT];
+  int s_step[2][2];                           // per tile and S buffer: its step, -1: the end
   long long seq_prefix[kThreads + 1];         // items before each thread's sequences
   long long unit_prefix[kThreads + 1];        // units before each thread's items
   long long w_sum[kWarps];
@@ -107,16 +107,17 @@ struct Shared {
   int abort;
 };
 
-__device__ __forceinline__ bool await(uint64_t* bar, uint32_t parity, Shared& sh, int* err) {
-  if (mbar_try_wait(bar, parity)) return true;
+// The polls behind a wait that is not over at once, out of line: fifteen roles'
+// worth of them inline did not fit the instruction cache.
+__device__ __noinline__ bool await_slow(uint64_t* bar, uint32_t parity, Shared* sh, int* err) {
   const long long t0 = clock64();
   while (true) {
 #pragma unroll 1
     for (int i = 0; i < 64; ++i)
       if (mbar_try_wait(bar, parity)) return true;
-    if (*reinterpret_cast<volatile int*>(&sh.abort)) return false;
+    if (*reinterpret_cast<volatile int*>(&sh->abort)) return false;
     if (clock64() - t0 > kWaitTimeoutCycles) {
-      sh.abort = 1;
+      sh->abort = 1;
       report_error(err, kDevErrTimeout);
       return false;
     }
@@ -126,7 +127,8 @@ __device__ __forceinline__ bool await(uint64_t* bar, uint32_t parity, Shared& sh
 // All lanes wait, and go on converged.  (One lane polling and a shuffle of the
 // outcome is slower: a shuffle takes ~230 cycles beside the other warps' polls.)
 __device__ __forceinline__ bool warp_await(uint64_t* bar, uint32_t parity, Shared& sh, int* err) {
-  const bool ok = await(bar, parity, sh, err);
+  bool ok = mbar_try_wait(bar, parity);
+  if (!ok) ok = await_slow(bar, parity, &sh, err);
   __syncwarp();
   return ok;
 }
@@ -323,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
     }
     for (int i = 0; i < kSteps; ++i) {
       mbar_init(&sh.step_full[i], 1);
-      mbar_init(&sh.step_free[i], 10);  // the softmax warps and the MMA threads
+      mbar_init(&sh.step_free[i], 2);   // each tile's PV, or tile B's absence
     }
     mbar_init(&sh.mma_done[0], 1);
     mbar_init(&sh.mma_done[1], 1);
@@ -637,6 +639,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
         for (int kk = 0; kk < D / 16; ++kk)
           mma_ss(cs, qdesc + (((kk >> 2) * kHalf + (kk & 3) * 32) >> 4), db + (((kk >> 2) * kHalfKv + (kk & 3) * 32) >> 4),
                      idesc_qk, kk > 0);
+        if (lane == 0) sh.s_step[x][cnt_s & 1] = g;   // read behind the commit
+        __syncwarp();
         commit(&sh.s_full[x][cnt_s & 1]);
         release(&sh.k_empty[g % kRing], flags);
         if (flags & kLast) release(&sh.q_free, flags);
@@ -654,6 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
           mma_ts(ocol, cs + 8 * kk, db + static_cast<uint64_t>((kk * 16 * 128) >> 4), idesc_pv,
                             (!(flags & kFirst) || kk > 0) ? 1u : 0u);
         release(&sh.v_empty[g % kRing], flags);
+        commit(&sh.step_free[g % kSteps]);
         commit(&sh.o_done[x]);
         ++cnt_p;
         return true;
@@ -668,9 +673,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
           const int both = __shfl_sync(0xffffffffu, sh.step[g % kSteps].flags | sh.step[g % kSteps].seg << 8, 0);
           flags = both & 0xFF;
           seg = both >> 8;
-          if (lane == 0) mbar_arrive(&sh.step_free[g % kSteps]);
-          __syncwarp();
           if ((flags & kEnd) || x == 0 || (flags & kHasB)) break;
+          if (lane == 0) mbar_arrive(&sh.step_free[g % kSteps]);   // not tile B's
+          __syncwarp();
         }
         return g;
       };
@@ -685,6 +690,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
         if (ok && !(flags & kEnd)) ok = qk(g, flags, seg);
         if (ok && !(f0 & kLast)) ok = pv(g0, f0);
       }
+      if (lane == 0) {
+        sh.s_step[x][cnt_s & 1] = -1;
+        mbar_arrive(&sh.s_full[x][cnt_s & 1]);
+      }
+      __syncwarp();
       // every MMA issued here completes before TMEM is released
       commit(&sh.mma_done[x]);
       const long long t0 = clock64();
@@ -707,17 +717,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
     float m = 0.f, l = 0.f, sc = 0.f, slope = 0.f;
     bool seen = false;
     int hi = 0, lo = 0, at = 0;
-    bool live = false, dead = false;
-    for (int g = 0;; ++g) {
-      if (!warp_await(&sh.step_full[g % kSteps], (g / kSteps) & 1, sh, a.err)) break;
-      const Step& st = sh.step[g % kSteps];
+    bool live = false;
+    size_t row = 0;                               // its row of o or of the workspace
+    while (true) {
+      if (!warp_await(&sh.s_full[x][cnt & 1], (cnt >> 1) & 1, sh, a.err)) break;
+      tc_fence_after_sync();
+      const int g = sh.s_step[x][cnt & 1];
+      if (g < 0) break;
+      const Step& st = sh.step[g % kSteps];       // until the last PV of this step: none of it is read behind p_ready
       const int flags = st.flags;
-      if (flags & kEnd) break;
-      if (x == 1 && !(flags & kHasB)) {     // a segment without tile B
-        if (lane == 0) mbar_arrive(&sh.step_free[g % kSteps]);
-        continue;
-      }
-      if (flags & kFirst) {
+      const uint32_t srow = srow2 + 64u * (cnt & 1);
+      if (__builtin_expect(flags & kFirst, 0)) {
         const int q = r / a.G, i = st.i0 + x * ta.tq + q;
         Rows rows;
         rows.t0 = st.t0, rows.n = st.n, rows.len = st.len, rows.prefix = st.prefix;
@@ -725,148 +735,117 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
         hi = live ? row_hi(a, rows, i) : 0;
         lo = live ? row_lo(a, rows, i) : 0;
         at = st.len - st.n + i;
+        row = flags & kWholeTask ? static_cast<size_t>(st.t0 + i) * a.Hq + st.h * a.G + r - q * a.G
+                                 : static_cast<size_t>(st.piece) * (2 * kT) + x * kT + r;
         if constexpr (kBias) slope = live ? __ldg(a.slopes + st.h * a.G + r - q * a.G) * kLog2e : 0.f;
+        sc = std::is_same<E, __half>::value ? (kCap ? a.scale_cap : a.scale_log2) : sh.qsc[st.seg & 3][x][r];
         m = l = 0.f;
         seen = !live;         // dead rows never wait for a key
       }
-      if (!warp_await(&sh.s_full[x][cnt & 1], (cnt >> 1) & 1, sh, a.err)) break;
-      tc_fence_after_sync();
-      const uint32_t srow = srow2 + 64u * (cnt & 1);
-      if (flags & kFirst)
-        sc = std::is_same<E, __half>::value ? (kCap ? a.scale_cap : a.scale_log2) : sh.qsc[st.seg & 3][x][r];
       const float4* gs = st.sc;
       const int j0 = st.j0;
       const bool whole = __all_sync(0xffffffffu, !live || (lo <= j0 && j0 + kN <= hi));
 
-      // z = y - m of 32 columns, -inf for keys the row does not see
-      auto logits = [&](int c, uint32_t (&v)[32]) {
-        tmem_ld32(srow + 32 * c, v);
-        tmem_ld_wait();
+      // z = y - m, -inf for keys the row does not see; m is 0 until it has seen one
+      uint32_t v[2][32];
+      tmem_ld32(srow, v[0]);
+      tmem_ld32(srow + 32, v[1]);
+      float rvs[kGroups], top = -INFINITY;
+      tmem_ld_wait();
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const float4 s4 = gs[2 * c + q];
-          const bool bad = __float_as_uint(s4.x) == kBadPageMark;
-          const float f = bad ? 0.f : sc * s4.x, off = bad ? -INFINITY : s4.y - m;
-          if constexpr (!kCap && !kBias) {
-            const uint64_t f2 = f32x2_pack(f, f), o2 = f32x2_pack(off, off);
+      for (int q = 0; q < kGroups; ++q) {
+        uint32_t(&w)[32] = v[q >> 1];
+        const float4 s4 = gs[q];
+        rvs[q] = s4.z;
+        const bool bad = __float_as_uint(s4.x) == kBadPageMark;
+        const float f = bad ? 0.f : sc * s4.x, off = bad ? -INFINITY : s4.y - m;
+        const int w0 = 16 * (q & 1);
+        if constexpr (!kCap && !kBias) {
+          const uint64_t f2 = f32x2_pack(f, f), o2 = f32x2_pack(off, off);
 #pragma unroll
-            for (int i = 16 * q; i < 16 * q + 16; i += 2) {
-              const float2 z = f32x2_unpack(
-                  f32x2_fma(f32x2_pack(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), f2, o2));
-              v[i] = __float_as_uint(z.x);
-              v[i + 1] = __float_as_uint(z.y);
-            }
-          } else {
+          for (int i = w0; i < w0 + 16; i += 2) {
+            const float2 z = f32x2_unpack(
+                f32x2_fma(f32x2_pack(__uint_as_float(w[i]), __uint_as_float(w[i + 1])), f2, o2));
+            w[i] = __float_as_uint(z.x);
+            w[i + 1] = __float_as_uint(z.y);
+          }
+        } else {
 #pragma unroll
-            for (int i = 16 * q; i < 16 * q + 16; ++i) {
-              float o = off;
-              if constexpr (kBias) o = fmaf(slope, static_cast<float>(j0 + 32 * c + i - at), o);
-              const float s = __uint_as_float(v[i]);
-              v[i] = __float_as_uint(kCap ? fmaf(a.cap_log2, tanh_of(s * f), o) : fmaf(s, f, o));
-            }
+          for (int i = w0; i < w0 + 16; ++i) {
+            float o = off;
+            if constexpr (kBias) o = fmaf(slope, static_cast<float>(j0 + 32 * (q >> 1) + i - at), o);
+            const float s = __uint_as_float(w[i]);
+            w[i] = __float_as_uint(kCap ? fmaf(a.cap_log2, tanh_of(s * f), o) : fmaf(s, f, o));
           }
         }
-        if (!whole) {
+      }
+      if (__builtin_expect(!whole, 0)) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int j = j0 + 32 * c + i;
-            if (j < lo || j >= hi) v[i] = 0xFF800000u;
-          }
-        }
-      };
-      auto top_of = [&](const uint32_t (&v)[32]) {
+        for (int i = 0; i < kN; ++i)
+          if (j0 + i < lo || j0 + i >= hi) v[i >> 5][i & 31] = 0xFF800000u;
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
         float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int i = 0; i < 32; i += 2)
-          t4[(i >> 1) & 3] = fmax3(t4[(i >> 1) & 3], __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
-        return fmax3(fmaxf(t4[0], t4[1]), t4[2], t4[3]);
-      };
-
-      if (__any_sync(0xffffffffu, !seen)) {   // rows without a key so far: their maximum first
-        float top = -INFINITY;
-#pragma unroll 1
-        for (int c = 0; c < kN / 32; ++c) {
-          uint32_t v[32];
-          logits(c, v);
-          top = fmaxf(top, top_of(v));
-        }
-        if (!seen && top > -INFINITY) {
-          m = top - kSetP;
-          seen = true;
-        }
+          t4[(i >> 1) & 3] = fmax3(t4[(i >> 1) & 3], __uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1]));
+        top = fmax3(top, fmax3(t4[0], t4[1], t4[2]), t4[3]);
       }
-#pragma unroll 1
-      for (int c = 0; c < kN / 32; ++c) {
-        uint32_t v[32];
-        logits(c, v);
-        const float top = top_of(v);
-        if (__any_sync(0xffffffffu, top > kMaxP)) {
-          // move m; everything so far is scaled to it, O once its last PV has landed
-          if (!(flags & kFirst) && !warp_await(&sh.o_done[x], (cnt - 1) & 1, sh, a.err)) {
-            dead = true;
-            break;
-          }
+      if (__builtin_expect(__any_sync(0xffffffffu, top > (seen ? kMaxP : -INFINITY)), 0)) {
+        // m is set, or moves with everything so far: O once its last PV has landed
+        float d = 0.f;
+        if (seen) d = fmaxf(top - kSetP, 0.f);
+        else if (top > -INFINITY) d = top - kSetP;
+        const float f = seen ? fast_exp2(-d) : 1.f;
+        m += d;
+        l *= f;
+        if (__any_sync(0xffffffffu, f != 1.f)) {   // never in a segment's first step
+          if (!warp_await(&sh.o_done[x], (cnt - 1) & 1, sh, a.err)) break;
           tc_fence_after_sync();
-          const float d = seen ? fmaxf(top - kSetP, 0.f) : 0.f;
-          const float f = fast_exp2(-d);
-          m += d;
-          l *= f;
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) - d);
-          if (!(flags & kFirst)) {
 #pragma unroll 1
-            for (int k = 0; k < D / 16; ++k) {
-              uint32_t o[16];
-              tmem_ld16(orow + 16 * k, o);
-              tmem_ld_wait();
-#pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-              tmem_st16(orow + 16 * k, o);
-            }
-          }
-          const __half2 f2 = __float2half2_rn(f);
-#pragma unroll 1
-          for (int k = 0; k < c; ++k) {
-            uint32_t p[16];
-            tmem_ld16(srow + 16 * k, p);
+          for (int k = 0; k < D / 16; ++k) {
+            uint32_t o[16];
+            tmem_ld16(orow + 16 * k, o);
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&p[i]), f2);
-              p[i] = *reinterpret_cast<const uint32_t*>(&y);
-            }
-            tmem_st16(srow + 16 * k, p);
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tmem_st16(orow + 16 * k, o);
           }
-          tmem_st_wait();
         }
+        seen |= top > -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) v[i >> 5][i & 31] = __float_as_uint(__uint_as_float(v[i >> 5][i & 31]) - d);
+      }
+      // P over the first half of S, which has been read
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
         uint32_t pk[16];
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           uint64_t ls2 = f32x2_pack(0.f, 0.f);
 #pragma unroll
           for (int i = 8 * q; i < 8 * q + 8; ++i) {
-            const float p0 = fast_exp2(__uint_as_float(v[2 * i])), p1 = fast_exp2(__uint_as_float(v[2 * i + 1]));
+            const float p0 = fast_exp2(__uint_as_float(v[c][2 * i])), p1 = fast_exp2(__uint_as_float(v[c][2 * i + 1]));
             ls2 = f32x2_add(ls2, f32x2_pack(p0, p1));
             pk[i] = f32x2_to_f16x2(p1, p0);
           }
           const float2 ls = f32x2_unpack(ls2);
-          l = fmaf(ls.x + ls.y, gs[2 * c + q].z, l);
+          l = fmaf(ls.x + ls.y, rvs[2 * c + q], l);
         }
         tmem_st16(srow + 16 * c, pk);
       }
-      if (dead) break;
       tmem_st_wait();
       tc_fence_before_sync();
       mbar_arrive(&sh.p_ready[x][cnt & 1]);
       ++cnt;
-      if (flags & kLast) {
+      if (__builtin_expect(flags & kLast, 0)) {
         // ---- the segment's rows, once its last PV has landed
         if (!warp_await(&sh.o_done[x], (cnt - 1) & 1, sh, a.err)) break;
         tc_fence_after_sync();
         const float lse2 = seen && l > 0.f ? m + log2f(l) : -INFINITY;
         if (flags & kWholeTask) {
           const float so = l > 0.f ? 1.f / l : 0.f;
-          const size_t row = static_cast<size_t>(st.t0 + st.i0 + x * ta.tq + r / a.G) * a.Hq + st.h * a.G + r % a.G;
           E* out = static_cast<E*>(a.o) + row * D;
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
@@ -887,8 +866,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
           }
           if (live && a.lse != nullptr) a.lse[row] = lse2 > -INFINITY ? lse2 * kLn2 : -INFINITY;
         } else {
-          const size_t pr = static_cast<size_t>(st.piece) * (2 * kT) + x * kT + r;
-          float* out = ta.part_o + pr * D;
+          float* out = ta.part_o + row * D;
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t v[32];
@@ -900,12 +878,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
               for (int i = 0; i < 8; ++i) o4[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
             }
           }
-          if (live) ta.part_ml[pr] = make_float2(seen ? m : -INFINITY, l);
+          if (live) ta.part_ml[row] = make_float2(seen ? m : -INFINITY, l);
         }
         tc_fence_before_sync();
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.step_free[g % kSteps]);
     }
   }
   tc_fence_before_sync();
