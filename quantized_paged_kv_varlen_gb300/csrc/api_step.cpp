@@ -84,7 +84,8 @@ qpkv_status qpkv_write_page8(const qpkv_write_page8_params* p, void* stream) {
   if (st != QPKV_OK) return st;
   if (p->num_heads_kv > 65535) return QPKV_ERR_UNSUPPORTED;
   if (p->num_seqs == 0 || p->num_tokens == 0) return QPKV_OK;
-  if (static_cast<int64_t>(p->num_tokens) / p->page_size + 2ll * p->num_seqs > INT32_MAX)
+  // two blocks at most for a (piece, head)
+  if ((static_cast<int64_t>(p->num_tokens) / p->page_size + 2ll * p->num_seqs) * 2 * p->num_heads_kv > INT32_MAX)
     return QPKV_ERR_UNSUPPORTED;
   if (p->cu_seqlens_q == nullptr || p->block_table == nullptr || p->k == nullptr || p->v == nullptr ||
       p->k_pool == nullptr || p->v_pool == nullptr || p->k_scale == nullptr || p->v_scale == nullptr)

@@ -12,7 +12,13 @@
 // QMAX = 448 (E4M3) or 127 (INT8); divisions are IEEE float32, products are
 // rounded to float32, s = 0 gives zero codes.
 //
-// HBM-bound: 2 bytes in and 1 out per element and tensor.  Pieces are found
+// HBM-bound: 2 bytes in and 1 out per element and tensor, if the quantiser is
+// kept short: the IEEE division is what fixes the codes, but x (1 / s) times
+// 1 - 2^-21 and 1 + 2^-21 lies on both sides of it, so where both give one code
+// that is the division's (rounding is monotonic).  A thread's words of four
+// codes where they differ (~2 %, many of them exact ties) are noted and done by
+// division afterwards.  Neighbouring blocks take neighbouring heads of a page,
+// so that rows are read whole.  Pieces are found
 // without a plan: sequence b owns work items [floor(cu[b-1] / ps) + 2 b, ...),
 // since n tokens touch at most floor(n / ps) + 2 pages, so a block finds its
 // sequence by a binary search and items past a sequence's last piece return.
@@ -36,6 +42,7 @@ struct WriteArgs {
   float *k_scale, *v_scale;            // [P, H]
   int* err;
   int tg;                              // threads of one (piece, head)
+  int hblocks, rounds;                 // blocks of a piece's heads, heads one after another in each
 };
 
 template <typename E>
@@ -58,6 +65,31 @@ __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) 
   }
 }
 
+// Codes of four values under a scale s with lo / hi = (1 -+ 2^-21) / s; *same:
+// they are those of the IEEE quotients.
+template <bool kInt8>
+__device__ __forceinline__ uint32_t encode4_fast(float2 a, float2 b, float lo, float hi, bool* same) {
+  const uint64_t x0 = f32x2_pack(a.x, a.y), x1 = f32x2_pack(b.x, b.y);
+  const uint64_t lo2 = f32x2_pack(lo, lo), hi2 = f32x2_pack(hi, hi);
+  if constexpr (kInt8) {
+    // + 1.5 * 2^23 rounds to the nearest integer (ties to even) into the low bits
+    const uint64_t magic = f32x2_pack(12582912.f, 12582912.f);
+    const uint64_t l0 = f32x2_fma(x0, lo2, magic), l1 = f32x2_fma(x1, lo2, magic);
+    const uint64_t h0 = f32x2_fma(x0, hi2, magic), h1 = f32x2_fma(x1, hi2, magic);
+    *same = l0 == h0 && l1 == h1;
+    const uint32_t c0 = __byte_perm(static_cast<uint32_t>(l0), static_cast<uint32_t>(l0 >> 32), 0x0040);
+    const uint32_t c1 = __byte_perm(static_cast<uint32_t>(l1), static_cast<uint32_t>(l1 >> 32), 0x0040);
+    return __byte_perm(c0, c1, 0x5410);
+  } else {
+    const uint64_t zero = f32x2_pack(-0.f, -0.f);   // x + -0 is x, signs of zero too
+    const float2 l0 = f32x2_unpack(f32x2_fma(x0, lo2, zero)), l1 = f32x2_unpack(f32x2_fma(x1, lo2, zero));
+    const float2 h0 = f32x2_unpack(f32x2_fma(x0, hi2, zero)), h1 = f32x2_unpack(f32x2_fma(x1, hi2, zero));
+    const uint32_t l = encode4<false>(l0.x, l0.y, l1.x, l1.y);
+    *same = l == encode4<false>(h0.x, h0.y, h1.x, h1.y);
+    return l;
+  }
+}
+
 template <bool kInt8>
 __device__ __forceinline__ float4 decode4(uint32_t w) {
   if constexpr (kInt8) {
@@ -69,15 +101,18 @@ __device__ __forceinline__ float4 decode4(uint32_t w) {
   }
 }
 
-template <typename E, int D, bool kInt8>
-__global__ void __launch_bounds__(1024) write_page8_kernel(const WriteArgs a) {
+template <typename E, int D, bool kInt8, int kThreads>
+__global__ void __launch_bounds__(kThreads, 512 / kThreads) write_page8_kernel(const __grid_constant__ WriteArgs a) {
   constexpr int VR = D / 8;             // 16-byte vectors of a row
   constexpr float kMax = kInt8 ? 127.f : 448.f;
-  __shared__ float s_max[32];
+  __shared__ float s_max[2][32];        // by round: one barrier a round is enough
   griddep_wait();
   griddep_launch_dependents();
+  // blocks of a page's heads lie side by side, K before V
+  const int hblocks = a.hblocks, which = blockIdx.x / hblocks, hblock = blockIdx.x - which * hblocks;
+  const bool is_v = which & 1;
   // the sequence of this work item: the last b with floor(cu[b-1] / ps) + 2 b <= item
-  const int item = blockIdx.x, ps = a.ps;
+  const int item = which >> 1, ps = a.ps;
   int lo = 0, hi = a.B - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -108,87 +143,130 @@ __global__ void __launch_bounds__(1024) write_page8_kernel(const WriteArgs a) {
   }
   const int groups = blockDim.x / a.tg;                 // heads side by side in this block
   const int grp = threadIdx.x / a.tg, th = threadIdx.x - grp * a.tg;
-  const int h = blockIdx.y * groups + grp;
-  const bool live = h < a.H;
-  const bool is_v = blockIdx.z != 0;
-  const long long st = is_v ? a.vs_t : a.ks_t;
-  const E* src = static_cast<const E*>(is_v ? a.v : a.k) + (t0 + (p0 - start)) * st +
-                 static_cast<long long>(h) * (is_v ? a.vs_h : a.ks_h);
-  uint8_t* dst = (is_v ? a.v_pool : a.k_pool) + page * a.page_stride + static_cast<long long>(h) * a.head_stride;
-  float* scale_at = (is_v ? a.v_scale : a.k_scale) + static_cast<size_t>(page) * a.H + h;
-  const int vecs = live ? n * VR : 0;
-
-  uint4 x[kVecs];
-  float amax = 0.f;
-  auto top = [&](const uint4& r) {
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+  const int h0 = hblock * groups * a.rounds + grp;
+  const long long st = is_v ? a.vs_t : a.ks_t, sh = is_v ? a.vs_h : a.ks_h;
+  const E* src0 = static_cast<const E*>(is_v ? a.v : a.k) + (t0 + (p0 - start)) * st;
+  uint8_t* pool = (is_v ? a.v_pool : a.k_pool) + page * a.page_stride + o0 * a.tok_stride;
+  float* scales = (is_v ? a.v_scale : a.k_scale) + static_cast<size_t>(page) * a.H;
+  // tg is a multiple of VR: a thread's vectors lie rows_per rows apart in one column
+  const int row0 = th / VR, rows_per = a.tg / VR;
+  src0 += row0 * st + (th % VR) * 8;
+  pool += row0 * a.tok_stride + (th % VR) * 8;
+  const long long src_step = rows_per * st, dst_step = rows_per * a.tok_stride;
+  auto load = [&](int h, int j) {
+    return __ldg(reinterpret_cast<const uint4*>(src0 + h * sh + j * src_step));
+  };
+  auto fill = [&](int h, uint4 (&x)[kVecs]) {
+    const E* p = src0 + h * sh;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = pair_f32<E>(w[i]);
-      amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+    for (int j = 0; j < kVecs; ++j) {
+      x[j] = make_uint4(0, 0, 0, 0);
+      if (h < a.H && row0 + j * rows_per < n) x[j] = __ldg(reinterpret_cast<const uint4*>(p));
+      p += src_step;
     }
   };
-  auto load = [&](int i) { return __ldg(reinterpret_cast<const uint4*>(src + (i / VR) * st + (i % VR) * 8)); };
+  uint4 x[kVecs], next[kVecs];
+  fill(h0, x);
+#pragma unroll 1
+  for (int round = 0; round < a.rounds; ++round) {
+    const int h = h0 + round * groups;
+    const bool live = h < a.H;
+    if (round + 1 < a.rounds) fill(h + groups, next);
+    const int rows = live ? n : 0;
+    // magnitudes of 16-bit floats are ordered like their bits
+    uint32_t top = 0;
+    auto take = [&](const uint4& r) {
+      top = __vmaxu2(top, __vmaxu2(__vmaxu2(r.x & 0x7FFF7FFFu, r.y & 0x7FFF7FFFu),
+                                   __vmaxu2(r.z & 0x7FFF7FFFu, r.w & 0x7FFF7FFFu)));
+    };
 #pragma unroll
-  for (int j = 0; j < kVecs; ++j) {
-    const int i = th + j * a.tg;
-    x[j] = i < vecs ? load(i) : make_uint4(0, 0, 0, 0);
-  }
-#pragma unroll
-  for (int j = 0; j < kVecs; ++j) top(x[j]);
-  for (int i = th + kVecs * a.tg; i < vecs; i += a.tg) top(load(i));   // pages beyond the registers
-  amax = warp_max(amax);
-  if (a.tg > 32) {   // the same for all threads of the block
-    if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = amax;
-    __syncthreads();
-    for (int w = grp * (a.tg >> 5); w < (grp + 1) * (a.tg >> 5); ++w) amax = fmaxf(amax, s_max[w]);
-  }
-  if (!live) return;
-  float s = __fdiv_rn(amax, kMax);
-  if (o0 > 0) {
-    const float was = *scale_at;
-    if (s > was) {
-      // the tokens that are there, in units of the new scale
-      for (int i = th; i < o0 * (D / 4); i += a.tg) {
-        uint32_t* at = reinterpret_cast<uint32_t*>(dst + (i / (D / 4)) * a.tok_stride + (i % (D / 4)) * 4);
-        const float4 v = decode4<kInt8>(*at);
-        *at = encode4<kInt8>(__fdiv_rn(__fmul_rn(v.x, was), s), __fdiv_rn(__fmul_rn(v.y, was), s),
-                             __fdiv_rn(__fmul_rn(v.z, was), s), __fdiv_rn(__fmul_rn(v.w, was), s));
+    for (int j = 0; j < kVecs; ++j) take(x[j]);
+    for (int j = kVecs; row0 + j * rows_per < rows; ++j) take(load(h, j));   // pages beyond the registers
+    const float2 two = pair_f32<E>(top);
+    float amax = warp_max(fmaxf(two.x, two.y));
+    if (a.tg > 32) {   // the same for all threads of the block
+      float* mx = s_max[round & 1];
+      if ((threadIdx.x & 31) == 0) mx[threadIdx.x >> 5] = amax;
+      __syncthreads();
+      for (int w = grp * (a.tg >> 5); w < (grp + 1) * (a.tg >> 5); ++w) amax = fmaxf(amax, mx[w]);
+    }
+    if (live) {
+      uint8_t* dst = pool + h * a.head_stride;
+      float s = __fdiv_rn(amax, kMax);
+      if (o0 > 0) {
+        const float was = scales[h];
+        if (s > was) {
+          // the tokens that are there, in units of the new scale
+          uint8_t* first = dst - (o0 + row0) * a.tok_stride - (th % VR) * 8;
+          for (int i = th; i < o0 * (D / 4); i += a.tg) {
+            uint32_t* at = reinterpret_cast<uint32_t*>(first + (i / (D / 4)) * a.tok_stride + (i % (D / 4)) * 4);
+            const float4 v = decode4<kInt8>(*at);
+            *at = encode4<kInt8>(__fdiv_rn(__fmul_rn(v.x, was), s), __fdiv_rn(__fmul_rn(v.y, was), s),
+                                 __fdiv_rn(__fmul_rn(v.z, was), s), __fdiv_rn(__fmul_rn(v.w, was), s));
+          }
+        } else {
+          s = was;
+        }
+        // every thread of the group has read the old scale before it is replaced
+        if (a.tg > 32) {
+          named_barrier(1 + grp, a.tg);
+        } else {
+          __syncwarp();
+        }
       }
-    } else {
-      s = was;
-    }
-    // every thread of the group has read the old scale before it is replaced
-    if (a.tg > 32) {
-      named_barrier(1 + grp, a.tg);
-    } else {
-      __syncwarp();
-    }
-  }
-  if (th == 0) *scale_at = s;
-  auto put = [&](int i, const uint4& r) {
-    uint2 code = make_uint2(0, 0);
-    if (s > 0.f) {
-      const float2 f0 = pair_f32<E>(r.x), f1 = pair_f32<E>(r.y), f2 = pair_f32<E>(r.z), f3 = pair_f32<E>(r.w);
-      code.x = encode4<kInt8>(__fdiv_rn(f0.x, s), __fdiv_rn(f0.y, s), __fdiv_rn(f1.x, s), __fdiv_rn(f1.y, s));
-      code.y = encode4<kInt8>(__fdiv_rn(f2.x, s), __fdiv_rn(f2.y, s), __fdiv_rn(f3.x, s), __fdiv_rn(f3.y, s));
-    }
-    *reinterpret_cast<uint2*>(dst + (o0 + i / VR) * a.tok_stride + (i % VR) * 8) = code;
-  };
+      if (th == 0) scales[h] = s;
+      auto at = [&](int j) { return reinterpret_cast<uint2*>(dst + j * dst_step); };
+      auto divide = [&](uint32_t r0, uint32_t r1) {
+        const float2 f0 = pair_f32<E>(r0), f1 = pair_f32<E>(r1);
+        return encode4<kInt8>(__fdiv_rn(f0.x, s), __fdiv_rn(f0.y, s), __fdiv_rn(f1.x, s), __fdiv_rn(f1.y, s));
+      };
+      const float inv = 1.f / s, lo_inv = inv * (1.f - 0x1p-21f), hi_inv = inv * (1.f + 0x1p-21f);
+      const bool fast = s > 0x1p-100f && s < 0x1p100f;    // neither 1 / s nor x / s leaves float32's range
+      uint32_t again = 0;                                 // words of codes to be done by division
 #pragma unroll
-  for (int j = 0; j < kVecs; ++j) {
-    const int i = th + j * a.tg;
-    if (i < vecs) put(i, x[j]);
+      for (int j = 0; j < kVecs; ++j) {
+        if (row0 + j * rows_per < rows) {
+          bool same0, same1;
+          uint2 code;
+          code.x = encode4_fast<kInt8>(pair_f32<E>(x[j].x), pair_f32<E>(x[j].y), lo_inv, hi_inv, &same0);
+          code.y = encode4_fast<kInt8>(pair_f32<E>(x[j].z), pair_f32<E>(x[j].w), lo_inv, hi_inv, &same1);
+          *at(j) = s > 0.f ? code : make_uint2(0, 0);
+          if (!(same0 && fast)) again |= 1u << 2 * j;
+          if (!(same1 && fast)) again |= 2u << 2 * j;
+        }
+      }
+      if (!(s > 0.f)) again = 0;
+      while (again) {
+        const int k = __ffs(again) - 1, j = k >> 1;
+        again &= again - 1;
+        // its two words of values, from L1 or L2
+        const uint2 r = __ldg(reinterpret_cast<const uint2*>(src0 + h * sh + j * src_step) + (k & 1));
+        reinterpret_cast<uint32_t*>(at(j))[k & 1] = divide(r.x, r.y);
+      }
+      for (int j = kVecs; row0 + j * rows_per < rows; ++j) {
+        const uint4 r = load(h, j);
+        *at(j) = s > 0.f ? make_uint2(divide(r.x, r.y), divide(r.z, r.w)) : make_uint2(0, 0);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) x[j] = next[j];
   }
-  for (int i = th + kVecs * a.tg; i < vecs; i += a.tg) put(i, load(i));
 }
 
 template <typename E, int D, bool kInt8>
 cudaError_t go(const WriteArgs& a, cudaStream_t stream) {
   const int threads = a.tg < 128 ? 128 : a.tg;
   const int groups = threads / a.tg;
+  WriteArgs w = a;
+  // up to eight heads one after another, the next one's loads ahead of the work
+  // on this one's, while that leaves every SM eight blocks (8 prompts of 32
+  // heads: 177 us with one, 112 with two, 97 with eight)
+  const long long pieces = (a.T / a.ps + 2ll * a.B) * 2;
+  w.rounds = 8;
+  while (w.rounds > 1 && (a.H < groups * w.rounds || pieces * (a.H / (groups * w.rounds)) < 152 * 8)) w.rounds /= 2;
+  w.hblocks = (a.H + groups * w.rounds - 1) / (groups * w.rounds);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.T / a.ps + 2 * a.B), static_cast<unsigned>((a.H + groups - 1) / groups), 2);
+  cfg.gridDim = dim3(static_cast<unsigned>(pieces * w.hblocks));
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -196,7 +274,8 @@ cudaError_t go(const WriteArgs& a, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, write_page8_kernel<E, D, kInt8>, a);
+  if (threads == 128) return cudaLaunchKernelEx(&cfg, write_page8_kernel<E, D, kInt8, 128>, w);
+  return cudaLaunchKernelEx(&cfg, write_page8_kernel<E, D, kInt8, 512>, w);
 }
 
 template <typename E>
@@ -231,9 +310,9 @@ cudaError_t launch_write_page8(const qpkv_write_page8_params& p, cudaStream_t st
   a.v_scale = p.v_scale;
   a.err = p.error_word;
   // threads of a (piece, head): the power of two that holds a full page in
-  // kVecs vectors a thread, between a warp and a block of 1024
+  // kVecs vectors a thread, between a warp and a block of 512
   int tg = 32;
-  while (tg < 1024 && tg * kVecs < p.page_size * p.head_dim / 8) tg *= 2;
+  while (tg < 512 && tg * kVecs < p.page_size * p.head_dim / 8) tg *= 2;
   a.tg = tg;
   const bool int8 = p.format == QPKV_FORMAT_INT8;
   return p.dtype == QPKV_DTYPE_F16 ? pick<__half>(a, p.head_dim, int8, stream)
