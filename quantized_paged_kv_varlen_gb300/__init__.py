@@ -894,21 +894,29 @@ def assign_pages(new_lens, seqlens, block_table, free_pages, free_count, page_si
            _arr(block_table, "block_table", i32, (B, W), dev),
            _arr(free_pages, "free_pages", i32, (F,), dev),
            _arr(free_count, "free_count", i32, (1,), dev))
-    outs = [block_table_out, seqlens_out, free_count_out, cu_seqlens, slot_mapping, positions]
-    shapes = ((B, W), (B,), (1,), (B,), (num_tokens,), (num_tokens,))
-    names = ("block_table_out", "seqlens_out", "free_count_out", "cu_seqlens", "slot_mapping",
-             "positions")
-    ptrs = []
-    for i, t in enumerate(outs):
-        if t is None:
-            outs[i] = t = block_table.new_empty(shapes[i])
-            ptrs.append(t.data_ptr())
-        else:
-            ptrs.append(_arr(t, names[i], i32, shapes[i], dev))
+    like = torch.empty_like
+    if block_table_out is None:
+        block_table_out = like(block_table)
+    if seqlens_out is None:
+        seqlens_out = like(seqlens)
+    if free_count_out is None:
+        free_count_out = like(free_count)
+    if cu_seqlens is None:
+        cu_seqlens = like(seqlens)
+    if slot_mapping is None:
+        slot_mapping = torch.empty(num_tokens, dtype=i32, device=block_table.device)
+    if positions is None:
+        positions = like(slot_mapping)
+    ptrs = (_arr(block_table_out, "block_table_out", i32, (B, W), dev),
+            _arr(seqlens_out, "seqlens_out", i32, (B,), dev),
+            _arr(free_count_out, "free_count_out", i32, (1,), dev),
+            _arr(cu_seqlens, "cu_seqlens", i32, (B,), dev),
+            _arr(slot_mapping, "slot_mapping", i32, (num_tokens,), dev),
+            _arr(positions, "positions", i32, (num_tokens,), dev))
     p = AssignParams(B, num_tokens, page_size, num_pages, W, F, *ins, *ptrs,
                      _error_ptr(error_word, dev))
     _check(lib.qpkv_assign_pages(ctypes.byref(p), stream), "qpkv_assign_pages")
-    return tuple(outs)
+    return block_table_out, seqlens_out, free_count_out, cu_seqlens, slot_mapping, positions
 
 
 def axis_sections(sections, interleaved=False):
@@ -950,7 +958,7 @@ def rope_axes(q, positions, pair_axis, rope_cos, rope_sin, k=None, q_out=None, k
     code = _dtype_code(dtype, f32=True)
     qp, q_t, q_h = _heads(q, "q", dtype, shape, dev)
     if q_out is None:
-        q_out = q.new_empty(shape)
+        q_out = torch.empty(shape, dtype=dtype, device=q.device)
     qo, qo_t, qo_h = _heads(q_out, "q_out", dtype, shape, dev)
     kp = ko = None
     Hkv = k_t = k_h = ko_t = ko_h = 0
@@ -959,7 +967,7 @@ def rope_axes(q, positions, pair_axis, rope_cos, rope_sin, k=None, q_out=None, k
         shape = (T, Hkv, D)
         kp, k_t, k_h = _heads(k, "k", dtype, shape, dev)
         if k_out is None:
-            k_out = k.new_empty(shape)
+            k_out = torch.empty(shape, dtype=dtype, device=q.device)
         ko, ko_t, ko_h = _heads(k_out, "k_out", dtype, shape, dev)
     axes, n = positions.shape
     axis_stride, step = positions.stride()
@@ -1057,7 +1065,7 @@ def attend_page8(q, k_pool, v_pool, k_scale, v_scale, block_table, cu_seqlens_q,
         raise ValueError(f"q must be [T, Hq, {Dp}]")
     qp = _arr(q, "q", dtype, shape, dev)
     if out is None:
-        out = q.new_empty(shape)
+        out = torch.empty_like(q)
         op = out.data_ptr()
     else:
         op = _arr(out, "out", dtype, shape, dev)
