@@ -792,6 +792,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
           t4[(i >> 1) & 3] = fmax3(t4[(i >> 1) & 3], __uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1]));
         top = fmax3(top, fmax3(t4[0], t4[1], t4[2]), t4[3]);
       }
+      if (!live) top = -INFINITY;   // what lies in a dead row moves nobody's m
       if (__builtin_expect(__any_sync(0xffffffffu, top > (seen ? kMaxP : -INFINITY)), 0)) {
         // m is set, or moves with everything so far: O once its last PV has landed
         float d = 0.f;
@@ -801,6 +802,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
         m += d;
         l *= f;
         if (__any_sync(0xffffffffu, f != 1.f)) {   // never in a segment's first step
+          // PV(g-2) is behind the QK(g) that s_full saw: the phase waited for is the next
           if (!warp_await(&sh.o_done[x], (cnt - 1) & 1, sh, a.err)) break;
           tc_fence_after_sync();
 #pragma unroll 1
@@ -841,6 +843,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
       ++cnt;
       if (__builtin_expect(flags & kLast, 0)) {
         // ---- the segment's rows, once its last PV has landed
+        // (PV of the step before first: a parity tells a phase from its neighbours
+        // only, and S(g) is ready without PV(g-1))
+        if (cnt > 1 && !warp_await(&sh.o_done[x], (cnt - 2) & 1, sh, a.err)) break;
         if (!warp_await(&sh.o_done[x], (cnt - 1) & 1, sh, a.err)) break;
         tc_fence_after_sync();
         const float lse2 = seen && l > 0.f ? m + log2f(l) : -INFINITY;

@@ -381,6 +381,55 @@ def test_attend_page8_many_rows(lib, err, reqs, Hq, H, D, ps, fmt, dtype, hnd, k
     _check_attend(c, out, lse, **kw)
 
 
+def _attend_64bit(c, causal=True):
+    """The attention of a case's sequences in float64 on the GPU, for sizes the
+    oracle's loops are too slow for: (o, lse, sum_j p_j |v_j|)."""
+    d, outs, t0 = c["dev"], [[], [], []], 0
+    for b, (end, L) in enumerate(zip(c["cu"].tolist(), c["lens"].tolist())):
+        n, pg = end - t0, torch.tensor(c["table"][b][:-(-L // c["pools"][0].shape[1])].astype(np.int64))
+        kv = [torch.tensor(step.decode(p[pg]) * s[pg].astype(np.float64)[:, None, :, None]).cuda().flatten(0, 1)[:L]
+              for p, s in zip(c["pools"], c["scales"])]
+        q = d["q"][t0:end].double()
+        at = torch.arange(n, device="cuda")[:, None] + L - n
+        see = torch.arange(L, device="cuda")[None] <= at if causal else torch.ones(n, L, dtype=bool, device="cuda")
+        for h in range(q.shape[1]):
+            g = h * kv[0].shape[1] // q.shape[1]
+            x = (q[:, h] @ kv[0][:, g].T / q.shape[2] ** 0.5).masked_fill(~see, -np.inf)
+            lse = torch.logsumexp(x, -1)
+            p = torch.exp(x - lse[:, None])
+            for o, y in zip(outs, (p @ kv[1][:, g], lse, p @ kv[1][:, g].abs())):
+                o.append(y)
+        t0 = end
+    H = d["q"].shape[1]
+    return [torch.cat([torch.stack(o[i:i + H], 1) for i in range(0, len(o), H)]) for o in outs]
+
+
+@pytest.mark.parametrize("reqs,Hq,H,D,fmt,dtype", [
+    ([(1500, 5000)], 8, 8, 128, "e4m3", "bf16"), ([(700, 4100), (900, 2300), (1, 9000), (130, 130)], 28, 4, 128, "int8", "f16"),
+    ([(2600, 2600)], 16, 4, 64, "int8", "bf16")])
+@pytest.mark.parametrize("causal", [True, False])
+def test_attend_page8_long_runs(lib, err, reqs, Hq, H, D, fmt, dtype, causal):
+    """Every CTA gets dozens of key tiles: the rings wrap, running maxima move,
+    and results do not depend on which warp is ahead (five times the same)."""
+    c = _attend_case(11, reqs, Hq, H, D, 16, fmt, dtype, False)
+    want, want_lse, size = _attend_64bit(c, causal)
+    first = None
+    for _ in range(5):
+        lse = torch.empty(c["q"].shape[:2], device="cuda")
+        got = _run_attend(lib, c, err, max_q=max(n for n, _ in reqs), lse=lse, causal=causal)
+        eps = torch.finfo(c["q"].dtype).eps / 2
+        # the tolerance of this file; all keys' codes and the largest weight bound its last term
+        flush = 2.0 ** -32 * float(c["scales"][1].max()) * 448 * max(L for _, L in reqs)
+        tol = eps * want.abs() + 2.0 ** -10 * size * (1 + eps) + flush + (2.0 ** -25 if dtype == "f16" else 0)
+        worst = float(((got.double() - want).abs() / tol).max())
+        assert worst <= 1, worst
+        off = float((lse - want_lse).abs().max())
+        assert off <= 2.0 ** -17 * (4 + 2 * float(want_lse.abs().max())), off
+        first = got if first is None else first
+        assert torch.equal(got, first)
+    assert int(err) == 0
+
+
 def test_attend_page8_forms_agree(lib, err):
     """The bound on a sequence's queries picks the kernels, never the result's
     meaning: without one, and with one that is too small to be a bound."""
