@@ -753,7 +753,7 @@ qpkv_status qpkv_write_page8(const qpkv_write_page8_params* params, void* stream
  * max_seqlen_q (a host bound on any n, <= 0: unknown) only picks the kernels.
  * sm_scale <= 0 selects 1/sqrt(D).
  * Errors: INVALID_ARG (null or misaligned pointers, negative sizes, a cap
- * that is negative or not finite), UNSUPPORTED (D not 64 or 128, page_size
+ * that is negative, below 1e-20 but not 0, or not finite), UNSUPPORTED (D not 64 or 128, page_size
  * not a multiple of 16, Hq % Hkv, dtype, format, layout, T * Hq / Hkv or
  * bt_stride * page_size above 2^31 - 65, num_pages * page_size, times Hkv for
  * HND, above 2^31 - 1), WORKSPACE_TOO_SMALL, CUDA. */

@@ -110,7 +110,8 @@ size_t qpkv_attend_page8_workspace_bytes(int32_t num_seqs, int32_t num_tokens, i
 
 qpkv_status qpkv_attend_page8(const qpkv_attend_page8_params* p, void* stream) {
   if (p == nullptr || p->num_seqs < 0 || p->num_tokens < 0 || p->num_heads_q < 1 || p->window < 0 ||
-      !(p->logit_cap >= 0.f) || !std::isfinite(p->logit_cap) || !std::isfinite(p->sm_scale))
+      !(p->logit_cap >= 0.f) || !std::isfinite(p->logit_cap) || !std::isfinite(p->sm_scale) ||
+      (p->logit_cap > 0.f && p->logit_cap < 1e-20f))   // its reciprocal times a score must stay finite
     return QPKV_ERR_INVALID_ARG;
   const qpkv_status st = check_pools(p->head_dim, p->page_size, p->num_pages, p->bt_stride,
                                      p->num_heads_kv, p->dtype, p->format, p->kv_layout);

@@ -224,6 +224,7 @@ cudaError_t launch_rope_axes(const qpkv_rope_axes_params& p, cudaStream_t stream
   int blocks = static_cast<int>((want + a.T - 1) / a.T);
   const int most = (heads + side - 1) / side;
   blocks = blocks < 1 ? 1 : blocks > most ? most : blocks;
+  blocks = blocks > 65535 ? 65535 : blocks;   // gridDim.y
   a.heads_per_block = ((heads + blocks - 1) / blocks + side - 1) / side * side;
   blocks = (heads + a.heads_per_block - 1) / a.heads_per_block;
   switch (p.dtype) {

@@ -486,6 +486,63 @@ def test_attend_page8_skips_bad_pages_and_lengths(lib, err):
     assert int(err) == lib.DEV_ERR_BAD_LENGTH and (out[3:] == 7.0).all() and torch.equal(out[:1], got[:1])
 
 
+def test_attend_page8_tiles_skip_bad_pages(lib, err):
+    """A page outside the pool in the middle of a prompt in tiles: its keys are
+    no keys, whatever the copies of other pages left in its place."""
+    c = _attend_case(6, [(60, 500), (2, 300)], 8, 2, 128, 32, "e4m3", "bf16", False)
+    bad = int(c["table"][0, 3])
+    c["dev"]["table"][0, 3] = -5
+    lse = torch.empty(c["q"].shape[:2], device="cuda")
+    got = _run_attend(lib, c, err, max_q=60, lse=lse)
+    assert int(err) == lib.DEV_ERR_BAD_PAGE
+    _check_attend(c, got, lse, skip_page=bad)
+
+
+@pytest.mark.parametrize("reqs,Hq,H", [([(1, 700), (1, 90), (2, 40)], 64, 1), ([(1, 300), (3, 50)], 150, 1), ([(140, 140)], 128, 1)])
+def test_attend_page8_many_heads_per_kv_head(lib, err, reqs, Hq, H):
+    """One kv head for up to 150 query heads: whole queries per tile, or (more
+    than 128) the split form's tiles."""
+    c = _attend_case(7, reqs, Hq, H, 64, 16, "int8", "f16", False)
+    lse = torch.empty(c["q"].shape[:2], device="cuda")
+    got = _run_attend(lib, c, err, max_q=max(n for n, _ in reqs), lse=lse)
+    _check_attend(c, got, lse)
+    assert int(err) == 0
+
+
+def test_attend_page8_on_two_streams_at_once(lib, err):
+    """Two calls that overlap, each with a workspace of its own, on streams that
+    are not the tensors' own."""
+    a = _attend_case(8, [(1, 3000)] * 16, 8, 2, 128, 16, "e4m3", "bf16", False)
+    b = _attend_case(9, [(200, 900), (1, 5000)], 8, 2, 128, 16, "int8", "f16", False)
+    want = [_run_attend(lib, x, err, max_q=200) for x in (a, b)]
+    ws = [lib.attend_page8_workspace(len(x["lens"]), x["q"].shape[0], 8, 2, 128) for x in (a, b)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [torch.empty_like(w) for w in want]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for x, w, s, o in zip((a, b), ws, streams, outs):
+            with torch.cuda.stream(s):
+                _run_attend(lib, x, err, max_q=200, out=o, ws=w)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1]) and int(err) == 0
+
+
+def test_step_with_nothing_to_do(lib, err):
+    """No tokens, no sequences: no launch, nothing written."""
+    c = _attend_case(1, [(2, 20)], 4, 2, 64, 16, "int8", "bf16", False)
+    d = c["dev"]
+    none = torch.empty(0, 4, 64, dtype=torch.bfloat16, device="cuda")
+    assert lib.attend_page8(none, d["kp"], d["vp"], d["ks"], d["vs"], d["table"], i32([0]), d["lens"]).shape == (0, 4, 64)
+    lib.attend_page8(d["q"], d["kp"], d["vp"], d["ks"], d["vs"], d["table"][:0], i32([]), i32([]))
+    before = d["kp"].clone()
+    lib.write_cache_page8(none[:, :2], none[:, :2], i32([0]), d["table"], d["kp"], d["vp"], d["ks"], d["vs"], error_word=err)
+    assert torch.equal(before, d["kp"])
+    cos, sin = lib.rope_table(1e4, 8, 64)
+    assert lib.rope_axes(none, i32(np.zeros((2, 0))), bytes(32), cos, sin).shape == (0, 4, 64)
+    got = lib.assign_pages(i32([0]), d["lens"], d["table"], i32([]), i32([0]), 16, 8, 0, error_word=err)
+    assert got[1].tolist() == [20] and got[3].tolist() == [0] and int(err) == 0
+
+
 # ------------------------------------------------------------ the step as used
 
 def test_step_grows_a_batch_in_a_replayed_graph(lib, err):

@@ -93,7 +93,7 @@ def _attend(q):
 
 @pytest.mark.parametrize("change,want", [
     (dict(num_seqs=-1), INVALID), (dict(num_tokens=-1), INVALID), (dict(num_heads_q=0), INVALID), (dict(window=-1), INVALID),
-    (dict(logit_cap=-1.0), INVALID), (dict(logit_cap=float("nan")), INVALID), (dict(logit_cap=float("inf")), INVALID),
+    (dict(logit_cap=-1.0), INVALID), (dict(logit_cap=float("nan")), INVALID), (dict(logit_cap=float("inf")), INVALID), (dict(logit_cap=1e-30), INVALID),
     (dict(sm_scale=float("nan")), INVALID), (dict(num_heads_q=7), UNSUPPORTED), (dict(head_dim=80), UNSUPPORTED),
     (dict(page_size=8), UNSUPPORTED), (dict(dtype=2), UNSUPPORTED), (dict(format=-1), UNSUPPORTED), (dict(kv_layout=5), UNSUPPORTED),
     (dict(bt_stride=1 << 27), UNSUPPORTED), (dict(num_tokens=1 << 30), UNSUPPORTED), (dict(q=None), INVALID), (dict(o=FAKE + 4), INVALID),
