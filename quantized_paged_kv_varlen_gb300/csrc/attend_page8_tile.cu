@@ -89,9 +89,12 @@ struct Smem {
 struct Shared {
   uint64_t q_raw, q_full, q_free;             // the queries' copy, their f16, their last use
   uint64_t k_full[kRing], k_empty[kRing], v_full[kRing], v_empty[kRing];
-  // per tile A / B; S and P per S buffer: a softmax warp may be a step ahead of
-  // another, whose arrival for its step must not be taken by that one's
-  uint64_t s_full[2][2], p_ready[2][2], o_done[2];
+  // per tile A / B and S buffer: a softmax warp may be a step ahead of another,
+  // whose arrival for its step must not be taken by that one's; and two PVs of a
+  // tile may be in flight, with one barrier whose parity tells them apart for
+  // nobody: a wait for the second could return behind the one before the first,
+  // a wait for the first could miss its phase
+  uint64_t s_full[2][2], p_ready[2][2], o_done[2][2];
   uint64_t mma_done[2];
   uint64_t step_full[kSteps], step_free[kSteps];
   uint64_t raw_full[kRaw], raw_empty[kRaw];
@@ -317,7 +320,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
       mbar_init(&sh.s_full[i][1], 1);
       mbar_init(&sh.p_ready[i][0], 128);
       mbar_init(&sh.p_ready[i][1], 128);
-      mbar_init(&sh.o_done[i], 1);
+      mbar_init(&sh.o_done[i][0], 1);
+      mbar_init(&sh.o_done[i][1], 1);
     }
     for (int i = 0; i < kRaw; ++i) {
       mbar_init(&sh.raw_full[i], 1);
@@ -659,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
                             (!(flags & kFirst) || kk > 0) ? 1u : 0u);
         release(&sh.v_empty[g % kRing], flags);
         commit(&sh.step_free[g % kSteps]);
-        commit(&sh.o_done[x]);
+        commit(&sh.o_done[x][cnt_p & 1]);
         ++cnt_p;
         return true;
       };
@@ -802,8 +806,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
         m += d;
         l *= f;
         if (__any_sync(0xffffffffu, f != 1.f)) {   // never in a segment's first step
-          // PV(g-2) is behind the QK(g) that s_full saw: the phase waited for is the next
-          if (!warp_await(&sh.o_done[x], (cnt - 1) & 1, sh, a.err)) break;
+          // (of this barrier, PV(g-3) is behind the QK(g) that s_full saw, and PV(g+1)
+          // in front of this warp's P(g): its current phase is PV(g-1)'s or just over)
+          if (!warp_await(&sh.o_done[x][(cnt - 1) & 1], ((cnt - 1) >> 1) & 1, sh, a.err)) break;
           tc_fence_after_sync();
 #pragma unroll 1
           for (int k = 0; k < D / 16; ++k) {
@@ -842,11 +847,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
       mbar_arrive(&sh.p_ready[x][cnt & 1]);
       ++cnt;
       if (__builtin_expect(flags & kLast, 0)) {
-        // ---- the segment's rows, once its last PV has landed
-        // (PV of the step before first: a parity tells a phase from its neighbours
-        // only, and S(g) is ready without PV(g-1))
-        if (cnt > 1 && !warp_await(&sh.o_done[x], (cnt - 2) & 1, sh, a.err)) break;
-        if (!warp_await(&sh.o_done[x], (cnt - 1) & 1, sh, a.err)) break;
+        // ---- the segment's rows, once its last PV has landed (and with it the one before)
+        if (!warp_await(&sh.o_done[x][(cnt - 1) & 1], ((cnt - 1) >> 1) & 1, sh, a.err)) break;
         tc_fence_after_sync();
         const float lse2 = seen && l > 0.f ? m + log2f(l) : -INFINITY;
         if (flags & kWholeTask) {
