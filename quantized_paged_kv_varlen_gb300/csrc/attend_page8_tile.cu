@@ -38,7 +38,9 @@
 // last piece may be partial and go to the workspace for the join kernel.  Each
 // (item, kv head) counts kOverhead units more than its key tiles, for its
 // queries' load and its results' store (a causal prompt begins with many items
-// of one key tile).
+// of one key tile).  9: the prompt of 8192 534 us, against 680 (4), 631 (5), 575
+// (6), 544 (7), 541 (12); over thirteen batches of prompts and pieces 7 to 12 are
+// within 1 %.
 #include <climits>
 
 #include "common.cuh"
@@ -58,10 +60,15 @@ constexpr int kHalf = kT * 128;               // 16 KB: 128 rows of 64 f16 (Q)
 constexpr int kHalfKv = kN * 128;             // 8 KB: 64 keys of 64 f16
 constexpr int kRing = 3;                      // K and V tiles as f16
 constexpr int kRaw = 3;                       // K and V tiles as codes
+// Tile B passes over the steps of an item without it and may come to step g
+// while tile A is steps behind.  That g is written tells that raw slot g - kRaw
+// was free, so kv_full's phase before g's is over and a wait for g cannot return
+// early; and g's keys come behind g's queries.
+static_assert(kRaw <= kRing, "a step may be written only once the ring place before it is full");
 constexpr uint32_t kColS = 0, kColO = 256;    // S: [tile][2] of 64 columns
 constexpr uint32_t kBadPageMark = 0x7FFFDEADu;   // in the place of a key scale: skip the group
 constexpr int kSteps = 8;                     // ring of steps
-constexpr int kOverhead = 5;
+constexpr int kOverhead = 9;
 
 // One step of the CTA: a key tile of one (item, kv head).
 enum : int { kFirst = 1, kLast = 2, kHasB = 4, kWholeTask = 8, kEnd = 16, kAllKeys = 32 };
@@ -88,7 +95,7 @@ struct Smem {
 
 struct Shared {
   uint64_t q_raw, q_full, q_free;             // the queries' copy, their f16, their last use
-  uint64_t k_full[kRing], k_empty[kRing], v_full[kRing], v_empty[kRing];
+  uint64_t kv_full[kRing], kv_empty[kRing];
   // per tile A / B and S buffer: a softmax warp may be a step ahead of another,
   // whose arrival for its step must not be taken by that one's; and two PVs of a
   // tile may be in flight, with one barrier whose parity tells them apart for
@@ -310,10 +317,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
     mbar_init(&sh.q_full, kLoad / 32);
     mbar_init(&sh.q_free, 2);             // both tiles' MMAs
     for (int i = 0; i < kRing; ++i) {
-      mbar_init(&sh.k_full[i], kLoad / 32);
-      mbar_init(&sh.k_empty[i], 2);
-      mbar_init(&sh.v_full[i], kLoad / 32);
-      mbar_init(&sh.v_empty[i], 2);
+      mbar_init(&sh.kv_full[i], kLoad / 32);
+      mbar_init(&sh.kv_empty[i], 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i][0], 1);
@@ -461,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
         for (int tile = 0; tile < tiles; ++tile) {
           uint8_t* row = smem + L::kQ + tile * L::kOp + tid * 128;
           float amax = 0.f;
-#pragma unroll 4
+#pragma unroll
           for (int k = 0; k < D / 8; ++k) {
             const uint4 v = *reinterpret_cast<const uint4*>(row + (k >> 3) * kHalf + (((k ^ tid) & 7) << 4));
             const uint32_t wv[4] = {v.x, v.y, v.z, v.w};
@@ -472,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
           float inv;
           const float mul = q_to_f16_scale(amax, &inv);
           sh.qsc[seg & 3][tile][tid] = inv * (kCap ? a.scale_cap : a.scale_log2);
-#pragma unroll 4
+#pragma unroll
           for (int k = 0; k < D / 8; ++k) {
             uint4* at = reinterpret_cast<uint4*>(row + (k >> 3) * kHalf + (((k ^ tid) & 7) << 4));
             const uint4 v = *at;
@@ -502,17 +507,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
       const bool all = s.flags & kAllKeys;
       const uint8_t* raw = smem + L::kCodes + (g % kRaw) * 2 * L::kRawTile;
       if (!warp_await(&sh.raw_full[g % kRaw], (g / kRaw) & 1, sh, a.err)) break;
-      if (!warp_await(&sh.k_empty[g % kRing], ph ^ 1, sh, a.err)) break;
+      if (!warp_await(&sh.kv_empty[g % kRing], ph ^ 1, sh, a.err)) break;
       store(smem + L::kK + (g % kRing) * L::kOpKv, raw, s, all);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.k_full[g % kRing]);
-      if (!warp_await(&sh.v_empty[g % kRing], ph ^ 1, sh, a.err)) break;
       store(smem + L::kV + (g % kRing) * L::kOpKv, raw + L::kRawTile, s, all);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&sh.v_full[g % kRing]);
+        mbar_arrive(&sh.kv_full[g % kRing]);
         mbar_arrive(&sh.raw_empty[g % kRaw]);
       }
     }
@@ -635,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
       };
       auto qk = [&](int g, int flags, int seg) -> bool {
         if ((flags & kFirst) && !warp_await(&sh.q_full, seg & 1, sh, a.err)) return false;
-        if (!warp_await(&sh.k_full[g % kRing], (g / kRing) & 1, sh, a.err)) return false;
+        if (!warp_await(&sh.kv_full[g % kRing], (g / kRing) & 1, sh, a.err)) return false;
         tc_fence_after_sync();
         const uint64_t db = kdesc + static_cast<uint64_t>(((g % kRing) * L::kOpKv) >> 4);
         const uint32_t cs = scol + 64u * (cnt_s & 1);
@@ -646,14 +647,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
         if (lane == 0) sh.s_step[x][cnt_s & 1] = g;   // read behind the commit
         __syncwarp();
         commit(&sh.s_full[x][cnt_s & 1]);
-        release(&sh.k_empty[g % kRing], flags);
         if (flags & kLast) release(&sh.q_free, flags);
         ++cnt_s;
         return true;
       };
       auto pv = [&](int g, int flags) -> bool {
         if (!warp_await(&sh.p_ready[x][cnt_p & 1], (cnt_p >> 1) & 1, sh, a.err)) return false;
-        if (!warp_await(&sh.v_full[g % kRing], (g / kRing) & 1, sh, a.err)) return false;
         tc_fence_after_sync();
         const uint64_t db = vdesc + static_cast<uint64_t>(((g % kRing) * L::kOpKv) >> 4);
         const uint32_t cs = scol + 64u * (cnt_p & 1);
@@ -661,7 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
         for (int kk = 0; kk < kN / 16; ++kk)
           mma_ts(ocol, cs + 8 * kk, db + static_cast<uint64_t>((kk * 16 * 128) >> 4), idesc_pv,
                             (!(flags & kFirst) || kk > 0) ? 1u : 0u);
-        release(&sh.v_empty[g % kRing], flags);
+        release(&sh.kv_empty[g % kRing], flags);
         commit(&sh.step_free[g % kSteps]);
         commit(&sh.o_done[x][cnt_p & 1]);
         ++cnt_p;
