@@ -60,14 +60,13 @@ constexpr int kHalf = kT * 128;               // 16 KB: 128 rows of 64 f16 (Q)
 constexpr int kHalfKv = kN * 128;             // 8 KB: 64 keys of 64 f16
 constexpr int kRing = 3;                      // K and V tiles as f16
 constexpr int kRaw = 3;                       // K and V tiles as codes
-// Tile B passes over the steps of an item without it and may come to step g
-// while tile A is steps behind.  That g is written tells that raw slot g - kRaw
-// was free, so kv_full's phase before g's is over and a wait for g cannot return
-// early; and g's keys come behind g's queries.
-static_assert(kRaw <= kRing, "a step may be written only once the ring place before it is full");
 constexpr uint32_t kColS = 0, kColO = 256;    // S: [tile][2] of 64 columns
 constexpr uint32_t kBadPageMark = 0x7FFFDEADu;   // in the place of a key scale: skip the group
-constexpr int kSteps = 8;                     // ring of steps
+// Ring of steps.  Step g is written once raw slot g - kRaw is free: those keys
+// were widened, into the place of step g - kRaw - kRing, whose PVs (tile B's, or
+// its passing) were through, and with them all reading of step g - kSteps.
+constexpr int kSteps = 8;
+static_assert(kSteps >= kRaw + kRing, "a step may be written only once nobody reads the one before it");
 constexpr int kOverhead = 9;
 
 // One step of the CTA: a key tile of one (item, kv head).
@@ -75,7 +74,7 @@ enum : int { kFirst = 1, kLast = 2, kHasB = 4, kWholeTask = 8, kEnd = 16, kAllKe
 struct Step {
   float4 sc[kGroups]; // per 16 keys: ks, log2 vs, 1 / vs
   int at[kGroups];    // per 16 keys: first pool row, -1: no keys
-  int flags;
+  int flags;          // and the segment's number % 4 << 8
   int j0;             // first key
   int seg;            // segments (runs of steps of one (item, kv head)) before this one
   int t0, n, len, prefix;   // the sequence (Rows)
@@ -103,7 +102,7 @@ struct Shared {
   // a wait for the first could miss its phase
   uint64_t s_full[2][2], p_ready[2][2], o_done[2][2];
   uint64_t mma_done[2];
-  uint64_t step_full[kSteps], step_free[kSteps];
+  uint64_t step_full[kSteps];
   uint64_t raw_full[kRaw], raw_empty[kRaw];
   Step step[kSteps];
   // [segment % 4][tile][row] logit multiplier: QK runs a step ahead of a softmax,
@@ -332,10 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
       mbar_init(&sh.raw_full[i], 1);
       mbar_init(&sh.raw_empty[i], kLoad / 32);
     }
-    for (int i = 0; i < kSteps; ++i) {
-      mbar_init(&sh.step_full[i], 1);
-      mbar_init(&sh.step_free[i], 2);   // each tile's PV, or tile B's absence
-    }
+    for (int i = 0; i < kSteps; ++i) mbar_init(&sh.step_full[i], 1);
     mbar_init(&sh.mma_done[0], 1);
     mbar_init(&sh.mma_done[1], 1);
     sh.abort = 0;
@@ -578,14 +574,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
       const float4 sc = make_float4(x.at >= 0 ? x.ks : __uint_as_float(kBadPageMark), log2f(sv), 1.f / sv, 0.f);
       const int n = x.n > 0 ? x.n : 1;     // the end is a step too
       for (int i = 0; i < n; ++i, ++g) {
-        ok = warp_await(&sh.step_free[g % kSteps], ((g / kSteps) & 1) ^ 1, sh, a.err);
+        ok = warp_await(&sh.raw_empty[g % kRaw], ((g / kRaw) & 1) ^ 1, sh, a.err);
         if (!ok) break;
         const bool here = mine == i && x.at >= 0;
         const int keys = __popc(__ballot_sync(0xffffffffu, here && x.j0 - i * kN + grp * 16 + 16 <= x.len));
         if (!(x.flags & kEnd)) {
           // the codes: lane (i, grp) copies 16 keys of K and of V
-          ok = warp_await(&sh.raw_empty[g % kRaw], ((g / kRaw) & 1) ^ 1, sh, a.err);
-          if (!ok) break;
           const int boxes = __popc(__ballot_sync(0xffffffffu, here));
           uint8_t* raw = smem + L::kCodes + (g % kRaw) * 2 * L::kRawTile + grp * 16 * D;
           if (lane == 0) mbar_arrive_expect_tx(&sh.raw_full[g % kRaw], boxes * 2 * 16 * D);
@@ -603,7 +597,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
           s.sc[grp] = sc;
         }
         if (lane == 0) {
-          s.flags = (x.flags & ((i == 0 ? ~0 : ~kFirst) & (i == n - 1 ? ~0 : ~kLast))) | (keys == kGroups ? kAllKeys : 0);
+          s.flags = (x.flags & ((i == 0 ? ~0 : ~kFirst) & (i == n - 1 ? ~0 : ~kLast))) | (keys == kGroups ? kAllKeys : 0) |
+                    (x.seg & 3) << 8;
           s.j0 = x.j0 - i * kN, s.seg = x.seg, s.t0 = x.t0, s.n = x.rows, s.len = x.len;
           s.prefix = x.prefix, s.h = x.h, s.i0 = x.i0, s.piece = x.piece;
         }
@@ -629,69 +624,79 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
       const uint64_t vdesc = make_smem_desc(smem_u32(smem + L::kV), kHalfKv, 1024, kSwizzle128B);
       const uint32_t scol = tmem_u + kColS + 128u * x, ocol = tmem_u + kColO + 128u * x;
       int cnt_s = 0, cnt_p = 0;                      // QKs and PVs issued
-      // the other tile's arrival too in a segment without tile B
-      auto release = [&](uint64_t* bar, int flags) {
-        commit(bar);
-        if (!(flags & kHasB)) commit(bar);
+      // A step's number, its place in the K/V ring and that place's parity, counted
+      // along: a division by three per use is a chain of its own in this warp.
+      struct At {
+        int g, place, parity, flags;
+        __device__ __forceinline__ void next() {
+          ++g;
+          if (++place == kRing) place = 0, parity ^= 1;
+        }
       };
-      auto qk = [&](int g, int flags, int seg) -> bool {
-        if ((flags & kFirst) && !warp_await(&sh.q_full, seg & 1, sh, a.err)) return false;
-        if (!warp_await(&sh.kv_full[g % kRing], (g / kRing) & 1, sh, a.err)) return false;
+      auto qk = [&](const At& s) -> bool {
+        if ((s.flags & kFirst) && !warp_await(&sh.q_full, (s.flags >> 8) & 1, sh, a.err)) return false;
+        if (!warp_await(&sh.kv_full[s.place], s.parity, sh, a.err)) return false;
         tc_fence_after_sync();
-        const uint64_t db = kdesc + static_cast<uint64_t>(((g % kRing) * L::kOpKv) >> 4);
+        const uint64_t db = kdesc + static_cast<uint64_t>((s.place * L::kOpKv) >> 4);
         const uint32_t cs = scol + 64u * (cnt_s & 1);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
           mma_ss(cs, qdesc + (((kk >> 2) * kHalf + (kk & 3) * 32) >> 4), db + (((kk >> 2) * kHalfKv + (kk & 3) * 32) >> 4),
                      idesc_qk, kk > 0);
-        if (lane == 0) sh.s_step[x][cnt_s & 1] = g;   // read behind the commit
+        if (lane == 0) sh.s_step[x][cnt_s & 1] = s.g;   // read behind the commit
         __syncwarp();
         commit(&sh.s_full[x][cnt_s & 1]);
-        if (flags & kLast) release(&sh.q_free, flags);
+        if (s.flags & kLast) {
+          commit(&sh.q_free);
+          if (!(s.flags & kHasB)) commit(&sh.q_free);   // tile B's arrival too
+        }
         ++cnt_s;
         return true;
       };
-      auto pv = [&](int g, int flags) -> bool {
+      auto pv = [&](const At& s) -> bool {
         if (!warp_await(&sh.p_ready[x][cnt_p & 1], (cnt_p >> 1) & 1, sh, a.err)) return false;
         tc_fence_after_sync();
-        const uint64_t db = vdesc + static_cast<uint64_t>(((g % kRing) * L::kOpKv) >> 4);
+        const uint64_t db = vdesc + static_cast<uint64_t>((s.place * L::kOpKv) >> 4);
         const uint32_t cs = scol + 64u * (cnt_p & 1);
 #pragma unroll
         for (int kk = 0; kk < kN / 16; ++kk)
           mma_ts(ocol, cs + 8 * kk, db + static_cast<uint64_t>((kk * 16 * 128) >> 4), idesc_pv,
-                            (!(flags & kFirst) || kk > 0) ? 1u : 0u);
-        release(&sh.kv_empty[g % kRing], flags);
-        commit(&sh.step_free[g % kSteps]);
+                            (!(s.flags & kFirst) || kk > 0) ? 1u : 0u);
+        commit(&sh.kv_empty[s.place]);
         commit(&sh.o_done[x][cnt_p & 1]);
         ++cnt_p;
         return true;
       };
-      // the next step from g on that this tile takes part in, its flags and segment
+      // from s on, the next step that this tile takes part in
       bool ok = true;
-      int flags = 0, seg = 0;
-      auto find = [&](int g) {
-        for (; ok; ++g) {
-          ok = warp_await(&sh.step_full[g % kSteps], (g / kSteps) & 1, sh, a.err);
+      auto find = [&](At s) {
+        while (true) {
+          ok = warp_await(&sh.step_full[s.g % kSteps], (s.g / kSteps) & 1, sh, a.err);
           if (!ok) break;
-          const int both = __shfl_sync(0xffffffffu, sh.step[g % kSteps].flags | sh.step[g % kSteps].seg << 8, 0);
-          flags = both & 0xFF;
-          seg = both >> 8;
-          if ((flags & kEnd) || x == 0 || (flags & kHasB)) break;
-          if (lane == 0) mbar_arrive(&sh.step_free[g % kSteps]);   // not tile B's
+          s.flags = sh.step[s.g % kSteps].flags;
+          if ((s.flags & kEnd) || x == 0 || (s.flags & kHasB)) break;
+          // not tile B's: its place is free for this tile, once it is this step's
+          // (so every phase of every place is waited for, and none mistaken)
+          ok = warp_await(&sh.kv_full[s.place], s.parity, sh, a.err);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive(&sh.kv_empty[s.place]);
           __syncwarp();
+          s.next();
         }
-        return g;
+        return s;
       };
       // QK(g+1) PV(g); the first QK of a segment comes behind the last PV of the
       // one before, as its queries take a while
-      int g = find(0);
-      if (ok && !(flags & kEnd)) ok = qk(g, flags, seg);
-      while (ok && !(flags & kEnd)) {
-        const int g0 = g, f0 = flags;
-        if (f0 & kLast) ok = pv(g0, f0);
-        if (ok) g = find(g0 + 1);
-        if (ok && !(flags & kEnd)) ok = qk(g, flags, seg);
-        if (ok && !(f0 & kLast)) ok = pv(g0, f0);
+      At cur = find(At{0, 0, 0, 0});
+      if (ok && !(cur.flags & kEnd)) ok = qk(cur);
+      while (ok && !(cur.flags & kEnd)) {
+        At s = cur;
+        s.next();
+        if (cur.flags & kLast) ok = pv(cur);
+        if (ok) s = find(s);
+        if (ok && !(s.flags & kEnd)) ok = qk(s);
+        if (ok && !(cur.flags & kLast)) ok = pv(cur);
+        cur = s;
       }
       if (lane == 0) {
         sh.s_step[x][cnt_s & 1] = -1;
