@@ -122,9 +122,16 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 template <int D, int NB>
 struct Shape {
   static constexpr int kBlocks = NB == 1 ? 4 : NB == 2 ? 3 : 2;
-  static constexpr int kStages = NB == 1 ? 2 : NB == 2 ? 4 : 6;
+  static constexpr int kStages = NB == 1 ? 2 : 4;
   static constexpr int kStage = 2 * kGroup * D;      // K and V of a group
+  // Three tiles keep the query fragments, each lane's own, in shared memory: 32
+  // requests of 2,500 tokens with 20 rows took 61.5 us with these 48 registers
+  // too (255 in all), 58.5 without.  (12 warps an SM, 168 registers, then spill:
+  // 94 us; the next group's scores beside this group's softmax: 61.4.)
+  static constexpr bool kQShared = NB == 3;
+  static constexpr int kQBytes = kQShared ? NB * (D / 16) * 32 * 8 : 0;
   static constexpr int kWarpBytes = kStages * kStage;
+  static constexpr int kBytes = kWarps * (kWarpBytes + kQBytes) + 1024;
 };
 
 struct RowInfo {
@@ -216,6 +223,7 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<D, NB>::kBlocks))
 
   uint8_t* ring = smem + warp * Sh::kWarpBytes;
   uint64_t* full = s_full[warp];
+  uint2* sq = reinterpret_cast<uint2*>(smem + kWarps * Sh::kWarpBytes + warp * Sh::kQBytes) + lane;
   RowInfo* ri = s_rows[warp];
   int in_st = 0, out_st = 0;     // ring stages of the next copy and the next use
   uint32_t out_phase = 0;        // phase of the stage in use
@@ -300,10 +308,11 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<D, NB>::kBlocks))
     for (int i = 0; i < kStages - 1; ++i) issue(i);
 
     // ---- Q: column g of tile nb is row rt * 8 NB + 8 nb + g, query r / G, head h * G + r % G
-    uint32_t qf[NB][KS][2];
+    uint32_t qf[Sh::kQShared ? 1 : NB][KS][2];
     int all_lo = 0, all_hi = INT_MAX;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
+      const int nq = Sh::kQShared ? 0 : nb;
       const int r = 8 * nb + g;
       const bool live = r < live_rows;
       const int rr = rt * 8 * NB + (live ? r : live_rows - 1);   // dead rows: zeros with the last row's limits
@@ -321,7 +330,7 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<D, NB>::kBlocks))
       float inv = 1.f;
       if constexpr (std::is_same<E, __half>::value) {
 #pragma unroll
-        for (int k = 0; k < KS; ++k) qf[nb][k][0] = raw[k].x, qf[nb][k][1] = raw[k].y;
+        for (int k = 0; k < KS; ++k) qf[nq][k][0] = raw[k].x, qf[nq][k][1] = raw[k].y;
       } else {
         float amax = 0.f;
 #pragma unroll
@@ -332,9 +341,13 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<D, NB>::kBlocks))
         const float mul = q_to_f16_scale(quad_max(amax), &inv);
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
-          qf[nb][k][0] = f32x2_to_f16x2(__uint_as_float(raw[k].x & 0xFFFF0000u) * mul, __uint_as_float(raw[k].x << 16) * mul);
-          qf[nb][k][1] = f32x2_to_f16x2(__uint_as_float(raw[k].y & 0xFFFF0000u) * mul, __uint_as_float(raw[k].y << 16) * mul);
+          qf[nq][k][0] = f32x2_to_f16x2(__uint_as_float(raw[k].x & 0xFFFF0000u) * mul, __uint_as_float(raw[k].x << 16) * mul);
+          qf[nq][k][1] = f32x2_to_f16x2(__uint_as_float(raw[k].y & 0xFFFF0000u) * mul, __uint_as_float(raw[k].y << 16) * mul);
         }
+      }
+      if constexpr (Sh::kQShared) {
+#pragma unroll
+        for (int k = 0; k < KS; ++k) sq[(nb * KS + k) * 32] = make_uint2(qf[0][k][0], qf[0][k][1]);
       }
       const int hi = row_hi(a, rows, i), lo = row_lo(a, rows, i);
       all_lo = max(all_lo, lo);
@@ -415,7 +428,14 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<D, NB>::kBlocks))
             widen<kInt8>(w0[k], f[0], f[2]);
             widen<kInt8>(w1[k], f[1], f[3]);
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) mma16816(s[nb], f, qf[nb][4 * c + k][0], qf[nb][4 * c + k][1]);
+            for (int nb = 0; nb < NB; ++nb) {
+              if constexpr (Sh::kQShared) {
+                const uint2 q = sq[(nb * KS + 4 * c + k) * 32];
+                mma16816(s[nb], f, q.x, q.y);
+              } else {
+                mma16816(s[nb], f, qf[nb][4 * c + k][0], qf[nb][4 * c + k][1]);
+              }
+            }
           }
         }
         const uint8_t* vsrc = src + kGroup * D;
@@ -702,7 +722,7 @@ cudaError_t launch(void (*kernel)(P...), unsigned grid, unsigned threads, size_t
 template <typename E, int D, bool kInt8, bool kCap, bool kBias, int NB>
 cudaError_t go(SplitArgs& a, int sms, cudaStream_t s) {
   using Sh = Shape<D, NB>;
-  constexpr size_t smem = kWarps * Sh::kWarpBytes + 1024;
+  constexpr size_t smem = Sh::kBytes;
   auto kernel = attend_split_kernel<E, D, kInt8, kCap, kBias, NB>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
