@@ -320,8 +320,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
       mbar_init(&sh.kv_empty[i], 2);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.s_full[i][0], 1);
-      mbar_init(&sh.s_full[i][1], 1);
+      mbar_init(&sh.s_full[i][0], 2);       // QK's commit, and s_step's store
+      mbar_init(&sh.s_full[i][1], 2);
       mbar_init(&sh.p_ready[i][0], 128);
       mbar_init(&sh.p_ready[i][1], 128);
       mbar_init(&sh.o_done[i][0], 1);
@@ -643,7 +643,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
         for (int kk = 0; kk < D / 16; ++kk)
           mma_ss(cs, qdesc + (((kk >> 2) * kHalf + (kk & 3) * 32) >> 4), db + (((kk >> 2) * kHalfKv + (kk & 3) * 32) >> 4),
                      idesc_qk, kk > 0);
-        if (lane == 0) sh.s_step[x][cnt_s & 1] = s.g;   // read behind the commit
+        if (lane == 0) {   // a commit publishes MMAs, not stores: an arrival of its own does
+          sh.s_step[x][cnt_s & 1] = s.g;
+          mbar_arrive(&sh.s_full[x][cnt_s & 1]);
+        }
         __syncwarp();
         commit(&sh.s_full[x][cnt_s & 1]);
         if (s.flags & kLast) {
@@ -701,6 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
       if (lane == 0) {
         sh.s_step[x][cnt_s & 1] = -1;
         mbar_arrive(&sh.s_full[x][cnt_s & 1]);
+        mbar_arrive(&sh.s_full[x][cnt_s & 1]);   // in the place of a QK
       }
       __syncwarp();
       // every MMA issued here completes before TMEM is released

@@ -430,6 +430,22 @@ def test_attend_page8_long_runs(lib, err, reqs, Hq, H, D, fmt, dtype, causal):
     assert int(err) == 0
 
 
+@pytest.mark.parametrize("reqs,Hq,H,D,fmt,dtype", [
+    ([(40, 40)] * 60, 16, 8, 64, "int8", "f16"), ([(30, 45), (70, 64), (25, 1)] * 30, 8, 4, 128, "e4m3", "bf16")])
+def test_attend_page8_segments_of_one_step(lib, err, reqs, Hq, H, D, fmt, dtype):
+    """A CTA's steps are a new (item, kv head) each: the softmax warps are told
+    of another one with every S, and take it for no other (ten times the same)."""
+    c = _attend_case(12, reqs, Hq, H, D, 16, fmt, dtype, False)
+    first = None
+    for _ in range(10):
+        lse = torch.empty(c["q"].shape[:2], device="cuda")
+        got = _run_attend(lib, c, err, max_q=max(n for n, _ in reqs), lse=lse)
+        if first is None:
+            first = got
+            _check_attend(c, got, lse)
+        assert torch.equal(got, first) and int(err) == 0
+
+
 def test_attend_page8_forms_agree(lib, err):
     """The bound on a sequence's queries picks the kernels, never the result's
     meaning: without one, and with one that is too small to be a bound."""
