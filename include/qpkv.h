@@ -597,6 +597,8 @@ qpkv_status qpkv_mla_sparse_decode(const qpkv_mla_params* params, void* stream);
  *   cu_seqlens       int32 [B]: inclusive prefix sums of new_lens (at most T)
  *   slot_mapping     int32 [num_tokens]: page * page_size + offset of each token
  *   positions        int32 [num_tokens]: L, L + 1, ... of its request
+ *   start_pos        int32 [B] or NULL: L, where qpkv_write_page8 appends, or -1
+ *                    for a refused request, of which it then writes nothing
  * Rows of slot_mapping / positions behind the last token get -1, so that T
  * may be the fixed size of a captured graph.  A request is refused (its
  * length and row stay, its tokens get slot and position -1) when the demand
@@ -605,7 +607,11 @@ qpkv_status qpkv_mla_sparse_decode(const qpkv_mla_params* params, void* stream);
  * tokens do not fit num_tokens, or for a negative length
  * (QPKV_DEV_ERR_BAD_LENGTH).  A request refused for want of pages still
  * counts in the demand of those behind it, so a smaller one does not
- * overtake it.  Page ids outside [0, num_pages) give slot -1 (and -1 in a
+ * overtake it.  cu_seqlens counts a refused request's tokens (their rows are
+ * part of the packed step all the same): write with start_pos from here, not
+ * with a copy of seqlens, or the rows of a refused request, which
+ * qpkv_rope_axes leaves unwritten, go into the page that its last tokens
+ * share.  Page ids outside [0, num_pages) give slot -1 (and -1 in a
  * new table entry) and QPKV_DEV_ERR_BAD_PAGE.
  * Errors: INVALID_ARG (null pointer, B < 1, non-positive sizes, num_tokens
  * or num_free negative), UNSUPPORTED (B > 8192, bt_stride or num_pages times
@@ -629,6 +635,7 @@ typedef struct qpkv_assign_params {
   int32_t* slot_mapping;
   int32_t* positions;
   int32_t* error_word;
+  int32_t* start_pos;    /* or NULL */
 } qpkv_assign_params;
 
 qpkv_status qpkv_assign_pages(const qpkv_assign_params* params, void* stream);
@@ -694,7 +701,8 @@ qpkv_status qpkv_rope_axes(const qpkv_rope_axes_params* params, void* stream);
  * left as they are.  A page may be written for one sequence only per call.
  * Pools: u8 (E4M3) or int8 [P, page_size, Hkv, D] (NHD) or [P, Hkv,
  * page_size, D] (HND); scales float [P, Hkv].  k, v: [T, Hkv, D] with strides
- * per token and head.  start_pos int32 [B] or NULL (all zero).
+ * per token and head.  start_pos int32 [B] or NULL (all zero); -1: nothing of
+ * the sequence is written (a request that qpkv_assign_pages refused).
  * Page ids outside [0, num_pages) are skipped (QPKV_DEV_ERR_BAD_PAGE), so are
  * positions past the table row and lengths that do not fit
  * (QPKV_DEV_ERR_BAD_LENGTH).

@@ -85,12 +85,15 @@ def _encode(x, fmt):
 
 def write_page8(k, v, cu, start_pos, block_table, pools, scales, fmt):
     """k, v float32 [T, H, D]; pools (k, v) [P, ps, H, D] and scales (k, v)
-    [P, H], updated in place."""
+    [P, H], updated in place.  A sequence that starts at -1 is not written."""
     ps = pools[0].shape[1]
     qmax = F32(448.0 if fmt == "e4m3" else 127.0)
     for x, pool, scale in zip((k, v), pools, scales):
         t = 0
         for b in range(len(cu)):
+            if start_pos[b] < 0:       # a refused request
+                t = int(cu[b])
+                continue
             p, end = int(start_pos[b]), int(start_pos[b]) + int(cu[b]) - t
             while p < end:
                 pg, o = int(block_table[b, p // ps]), p % ps

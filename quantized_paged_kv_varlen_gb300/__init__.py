@@ -110,7 +110,7 @@ class AssignParams(ctypes.Structure):
         (n, _p) for n in (
             "new_lens", "seqlens", "block_table", "free_pages", "free_count", "block_table_out",
             "seqlens_out", "free_count_out", "cu_seqlens", "slot_mapping", "positions",
-            "error_word")]
+            "error_word", "start_pos")]
 
 
 class RopeAxesParams(ctypes.Structure):
@@ -873,7 +873,8 @@ def _dtype_code(dtype, f32=False):
 
 def assign_pages(new_lens, seqlens, block_table, free_pages, free_count, page_size, num_pages,
                  num_tokens, block_table_out=None, seqlens_out=None, free_count_out=None,
-                 cu_seqlens=None, slot_mapping=None, positions=None, error_word=None):
+                 cu_seqlens=None, slot_mapping=None, positions=None, error_word=None,
+                 start_pos=None):
     """Pages and slots for the tokens of one step, from request lengths on the
     GPU.  new_lens, seqlens int32 [B] (tokens the step brings / tokens cached);
     block_table int32 [B, W]; free_pages int32 [F], a stack whose first
@@ -883,7 +884,11 @@ def assign_pages(new_lens, seqlens, block_table, free_pages, free_count, page_si
     free_count, cu_seqlens, slot_mapping, positions); the first three are new
     tensors, or the given outputs, which may be the inputs themselves.
     Refused requests (no pages, no room) keep their length and row and get
-    slot and position -1; the device error word says so."""
+    slot and position -1; the device error word says so.  start_pos int32 [B],
+    when given, receives what ``write_cache_page8`` takes under that name: the
+    cached tokens, or -1 for a refused request.  cu_seqlens counts a refused
+    request's tokens, so a write with a copy of seqlens instead would put them
+    into the page of its last tokens."""
     torch = _torch()
     lib = load()
     i32 = torch.int32
@@ -914,7 +919,8 @@ def assign_pages(new_lens, seqlens, block_table, free_pages, free_count, page_si
             _arr(slot_mapping, "slot_mapping", i32, (num_tokens,), dev),
             _arr(positions, "positions", i32, (num_tokens,), dev))
     p = AssignParams(B, num_tokens, page_size, num_pages, W, F, *ins, *ptrs,
-                     _error_ptr(error_word, dev))
+                     _error_ptr(error_word, dev),
+                     None if start_pos is None else _arr(start_pos, "start_pos", i32, (B,), dev))
     _check(lib.qpkv_assign_pages(ctypes.byref(p), stream), "qpkv_assign_pages")
     return block_table_out, seqlens_out, free_count_out, cu_seqlens, slot_mapping, positions
 
@@ -1014,7 +1020,9 @@ def write_cache_page8(k, v, cu_seqlens, block_table, k_pool, v_pool, k_scale, v_
     fine) to a cache in 8 bits with one scale per (page, kv head): pools uint8
     (E4M3) or int8 [P, page_size, Hkv, D] (kv_layout "HND": [P, Hkv,
     page_size, D]), scales float32 [P, Hkv].  A partly filled page's earlier
-    codes are rescaled when the new tokens raise its scale."""
+    codes are rescaled when the new tokens raise its scale.  start_pos int32
+    [B]: tokens cached before (None: 0); -1, as ``assign_pages`` gives it for a
+    refused request: nothing of that sequence is written."""
     torch = _torch()
     lib = load()
     dev, stream = _device_and_stream()

@@ -197,7 +197,7 @@ const char* qpkv_status_string(qpkv_status s) {
   }
 }
 
-int32_t qpkv_version(void) { return 200; }
+int32_t qpkv_version(void) { return 201; }
 
 size_t qpkv_struct_size(int32_t which) {
   switch (which) {

@@ -123,7 +123,8 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads) write_page8_kernel(c
   const int start = a.start != nullptr ? __ldg(a.start + b) : 0;
   const int nth = item - (t0 / ps + 2 * b);             // which page of the sequence's new tokens
   if (t0 < 0 || t1 < t0 || t1 > a.T || start < 0 || nth < 0) {
-    if (threadIdx.x == 0 && (t1 < t0 || t1 > a.T || start < 0)) report_error(a.err, kDevErrBadLength);
+    // a start of -1 is a refused request: its tokens have no place, and that has been reported
+    if (threadIdx.x == 0 && (t1 < t0 || t1 > a.T || start < -1)) report_error(a.err, kDevErrBadLength);
     return;
   }
   const long long page_no = static_cast<long long>(start / ps) + nth;

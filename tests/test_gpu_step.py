@@ -640,6 +640,75 @@ def test_step_grows_a_batch_in_a_replayed_graph(lib, err):
     assert int(count) == o_state[2] and int(err) == 0
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_step_leaves_the_pages_of_refused_requests_alone(lib, err, fmt):
+    """A draft refused for want of pages, a request served, a prompt piece too
+    long for its row and one past num_tokens, all but the served one with a
+    partly filled page: the step changes no code and no scale of theirs,
+    whatever their rows hold; served later, they give the oracle's results."""
+    B, H, Hq, D, ps, W, P, T = 4, 2, 8, 64, 16, 4, 16, 36
+    rng = np.random.default_rng(5)
+    cos, sin = lib.rope_table(1e4, W * ps, D)
+    axis = lib.axis_sections((12, 10, 10))
+    kp, vp = _pool(P, ps, H, D, fmt, False, 0), _pool(P, ps, H, D, fmt, False, 0)
+    ks, vs = torch.zeros(P, H, device="cuda"), torch.zeros(P, H, device="cuda")
+    table = torch.full((B, W), -1, dtype=torch.int32, device="cuda")
+    lens, pages, start = i32([0] * B), i32(rng.permutation(P)), i32([0] * B)
+    o_pools, o_scales = [_nhd(kp, False), _nhd(vp, False)], [np.zeros((P, H), np.float32) for _ in range(2)]
+    o_table, o_lens = np.full((B, W), -1, np.int32), np.zeros(B, np.int32)
+    count = i32([0])
+
+    def step_of(x, new, free, T):
+        nonlocal o_table, o_lens
+        count.fill_(free)
+        want = step.assign_pages(np.array(new), o_lens, o_table, pages.cpu().numpy(), free, ps, T)
+        o_start = np.where(np.isin(np.arange(B), want[6]), -1, o_lens)
+        _, _, _, cu, _, pos = lib.assign_pages(i32(new), lens, table, pages, count, ps, P, T, block_table_out=table,
+                                               seqlens_out=lens, free_count_out=count, start_pos=start, error_word=err)
+        word = int(err)
+        err.zero_()
+        assert np.array_equal(start.cpu().numpy(), o_start) and np.array_equal(cu.cpu().numpy(), want[3])
+        # what lies in rows that are not rotated: far larger than the cache's values
+        k = torch.full((T, H, D), 1e20, dtype=torch.bfloat16, device="cuda")
+        dev = x.cuda()
+        q, k = lib.rope_axes(dev[:, :Hq], pos.expand(3, T), axis, cos, sin, k=dev[:, Hq:Hq + H], k_out=k, error_word=err)
+        lib.write_cache_page8(k, dev[:, Hq + H:], cu, table, kp, vp, ks, vs, start_pos=start, error_word=err)
+        lse = torch.empty(T, Hq, device="cuda")
+        out = lib.attend_page8(q, kp, vp, ks, vs, table, cu, lens, lse=lse, error_word=err)
+        assert int(err) == 0
+        c, s = cos.cpu().numpy(), sin.cpu().numpy()
+        o_k = torch.tensor(step.rope_axes(x[:, Hq:Hq + H].float().numpy(), np.stack([want[5]] * 3), axis, c, s)).bfloat16()
+        step.write_page8(o_k.float().numpy(), x[:, Hq + H:].float().numpy(), want[3], o_start, want[0], o_pools, o_scales, fmt)
+        for got, w in ((kp, o_pools[0]), (vp, o_pools[1])):
+            same = _nhd(got, False) == w
+            if fmt == "e4m3":
+                same |= ((_nhd(got, False) | w) & 0x7F) == 0
+            assert same.all()
+        assert np.array_equal(ks.cpu().numpy(), o_scales[0]) and np.array_equal(vs.cpu().numpy(), o_scales[1])
+        o_table, o_lens = want[0], want[1]
+        assert np.array_equal(table.cpu().numpy(), o_table) and np.array_equal(lens.cpu().numpy(), o_lens)
+        return want, word, q, out, lse
+
+    def make(T, size=1.0):
+        return torch.tensor((size * rng.standard_normal((T, Hq + 2 * H, D))).astype(np.float32)).bfloat16()
+
+    held = [10, 21, 60, 5]
+    _, word, *_ = step_of(make(sum(held)), held, P, sum(held))
+    assert word == 0
+    keep = [t.clone() for t in (kp, vp, ks, vs)]
+    want, word, *_ = step_of(make(T, 50.0), [20, 5, 9, 4], 0, T)
+    assert want[6] == [0, 2, 3] and word == lib.DEV_ERR_NO_PAGES | lib.DEV_ERR_BAD_LENGTH
+    for b in (0, 2, 3):
+        own = table[b][table[b] >= 0].long()
+        for now, before in zip((kp, vp, ks, vs), keep):
+            assert torch.equal(now[own], before[own])
+    x = make(27)
+    want, word, q, out, lse = step_of(x, [20, 0, 3, 4], int((pages >= 0).sum()) - 9, 27)
+    assert want[6] == [] and word == 0
+    _check_attend(dict(q=q.cpu(), pools=o_pools, scales=o_scales, table=o_table, cu=want[3], lens=o_lens, T=27, slopes=None,
+                       prefix=None), out, lse)
+
+
 def test_step_entry_points_refuse_other_tensors(lib):
     c = _attend_case(1, [(1, 20)], 4, 2, 64, 16, "int8", "bf16", False)
     d = c["dev"]

@@ -90,6 +90,23 @@ def test_page_write_keeps_values_within_its_steps(fmt):
     assert (np.abs(got - x) <= times * half).all()
 
 
+def test_page_write_leaves_out_a_sequence_that_starts_at_minus_one():
+    """A request that the page assignment refused, between two served ones."""
+    rng = np.random.default_rng(4)
+    ps, H, D, cu, table = 16, 1, 64, [3, 23, 28], np.array([[2, -1], [0, -1], [1, -1]])
+    x = rng.standard_normal((28, H, D)).astype(np.float32)
+    x[3:23] = 1e20
+    pools = tuple(rng.integers(-127, 128, (3, ps, H, D)).astype(np.int8) for _ in range(2))
+    scales = tuple(rng.uniform(0.01, 0.03, (3, H)).astype(np.float32) for _ in range(2))
+    before = [a.copy() for a in pools + scales]
+    step.write_page8(x, x, cu, [4, -1, 0], table, pools, scales, "int8")
+    want = [a.copy() for a in before]
+    rest = np.r_[0:3, 23:28]
+    step.write_page8(x[rest], x[rest], [3, 8], [4, 0], table[[0, 2]], want[:2], want[2:], "int8")
+    for got, w, old in zip(pools + scales, want, before):
+        assert np.array_equal(got, w) and np.array_equal(got[0], old[0]) and not np.array_equal(got, old)
+
+
 @pytest.mark.parametrize("causal,window,prefix", [(True, 0, 0), (True, 5, 0), (True, 0, 9), (False, 0, 0)])
 def test_page_attention_against_sdpa(causal, window, prefix):
     rng = np.random.default_rng(5)
