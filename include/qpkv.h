@@ -753,8 +753,10 @@ qpkv_status qpkv_write_page8(const qpkv_write_page8_params* params, void* stream
  *   workspace     qpkv_attend_page8_workspace_bytes bytes, 16-byte aligned,
  *                 overwritten; calls that may overlap need one each
  * Queries enter the product with every bit (bf16 values below 2^-31 of their
- * row's largest flush), P as f16, sums in float32.  Value scales below 2^-100
- * count as 2^-100; scales must not be negative.
+ * row's largest flush), P as f16, sums in float32.  Value scales below 2^-80,
+ * zero among them, count as 2^-80; those of the pages that a row sees may lie
+ * 2^100 apart (beyond that, small weights under the smaller ones flush); scales
+ * must not be negative.
  * A key whose page id lies outside [0, num_pages) is skipped
  * (QPKV_DEV_ERR_BAD_PAGE).  A sequence whose rows or length do not fit the
  * arrays has no rows or no keys (QPKV_DEV_ERR_BAD_LENGTH).

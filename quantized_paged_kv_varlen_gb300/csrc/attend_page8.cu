@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<D, NB>::kBlocks))
 #pragma unroll 1
     for (int i = 0; i < count; ++i) {
       if ((i & 31) == 0) {     // before the copies of the next 32 groups are issued
-        const float vs = next_vs == 0.f ? 1.f : fmaxf(next_vs, kMinScale);
+        const float vs = fmaxf(next_vs, kMinScale);
         blk_ks = at >= 0 ? next_ks : __uint_as_float(kBadPageMark);
         blk_lv = log2f(vs);
         blk_rvs = 1.f / vs;

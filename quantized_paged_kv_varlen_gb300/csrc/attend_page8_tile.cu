@@ -570,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
     int issued = 0;
     for (int g = 0; ok;) {
       const Batch next = x.n > 0 ? fetch() : x;
-      const float sv = x.vs == 0.f ? 1.f : fmaxf(x.vs, kMinScale);
+      const float sv = fmaxf(x.vs, kMinScale);
       const float4 sc = make_float4(x.at >= 0 ? x.ks : __uint_as_float(kBadPageMark), log2f(sv), 1.f / sv, 0.f);
       const int n = x.n > 0 ? x.n : 1;     // the end is a step too
       for (int i = 0; i < n; ++i, ++g) {

@@ -11,9 +11,11 @@ namespace qpkv {
 // P = 2^(y - m): log2 of the row's largest P when m is set, and the largest
 // it may become before m moves.
 constexpr float kSetP = 7.0f, kMaxP = 15.0f;
-// Value scales below this count as this: log2 and reciprocal stay finite in
-// float32 (values that small are zero beside anything a model computes).
-constexpr float kMinScale = 7.888609e-31f;   // 2^-100
+// Value scales below this, zero among them, count as this: values that small
+// are zero beside anything a model computes, and the keys of such a page move
+// no row's m away from those that count.  P <= 2^kMaxP over it, summed over
+// fewer than 2^31 keys, stays in float32.
+constexpr float kMinScale = 8.271806e-25f;   // 2^-80
 
 struct Page8Args {
   int B, T, Hq, Hkv, G, ps, num_pages, bt_stride, causal, window, hnd;

@@ -481,6 +481,49 @@ def test_attend_page8_query_and_value_sizes(lib, err, size):
     _check_attend(c, got, lse, sm_scale=float(np.float32(scale)))
 
 
+@pytest.mark.parametrize("reqs,max_q", [([(1, 100), (2, 60), (1, 20)], 2), ([(90, 200), (1, 70)], 90)], ids=["split", "tiles"])
+@pytest.mark.parametrize("fmt,dtype", [("int8", "f16"), ("e4m3", "bf16")])
+def test_attend_page8_value_scales_of_zero(lib, err, reqs, max_q, fmt, dtype):
+    """Pages whose value scale is 0 add nothing, whatever their codes, and lower
+    nobody's weights: the others' scales are 2^-25 to 2^-30 of a usual one."""
+    c = _attend_case(14, reqs, 4, 2, 64, 16, fmt, dtype, False)
+    vs = c["scales"][1]
+    vs *= (2.0 ** -np.random.default_rng(1).integers(25, 31, vs.shape)).astype(np.float32)
+    if dtype == "f16":      # values that f16 holds
+        vs *= np.float32(2.0 ** 20)
+    vs[c["table"][0, 1]] = 0.0
+    vs[c["table"][1, 0], 1] = 0.0
+    c["dev"]["vs"].copy_(torch.tensor(vs))
+    lse = torch.empty(c["q"].shape[:2], device="cuda")
+    got = _run_attend(lib, c, err, max_q=max_q, lse=lse)
+    _check_attend(c, got, lse)
+    # a row that sees such pages only: its weights are as ever, its values count as 2^-80 of their codes
+    c["dev"]["vs"].zero_()
+    zero_lse = torch.empty_like(lse)
+    got = _run_attend(lib, c, err, max_q=max_q, lse=zero_lse)
+    top = 448.0 if fmt == "e4m3" else 127.0
+    assert float(got.float().abs().max()) <= 2.0 ** -80 * top * 1.01
+    # either lse is within the tolerance of this file
+    assert float((zero_lse - lse).abs().max()) <= 2.0 ** -16 * (4 + 2 * float(lse.abs().max())) and int(err) == 0
+
+
+@pytest.mark.parametrize("n", [1, 30], ids=["split", "tiles"])
+def test_attend_page8_denominators_stay_finite(lib, err, n):
+    """Four million keys of one weight under the smallest scale: the sum of
+    P / scale is 2^22 2^7 2^80 at least, and lse = ln(keys)."""
+    ps, L = 1024, 1 << 22
+    kp = torch.zeros(1, ps, 1, 64, dtype=torch.int8, device="cuda")
+    vp = torch.full_like(kp, 100)
+    ks, vs = torch.ones(1, 1, device="cuda"), torch.full((1, 1), 2.0 ** -110, device="cuda")
+    q = torch.randn(n, 1, 64, device="cuda", dtype=torch.bfloat16)
+    lse = torch.empty(n, 1, device="cuda")
+    got = lib.attend_page8(q, kp, vp, ks, vs, torch.zeros(1, L // ps, dtype=torch.int32, device="cuda"), i32([n]), i32([L]),
+                           causal=False, lse=lse, error_word=err)
+    # every P and every scale is a power of two; sums of 2^22 terms in runs of thousands, 2^-24 a step
+    assert float((lse.double() - np.log(L)).abs().max()) <= 2.0 ** -9
+    assert float((got.double() / (100 * 2.0 ** -80) - 1).abs().max()) <= 2.0 ** -8 + 2.0 ** -9 and int(err) == 0
+
+
 def test_attend_page8_skips_bad_pages_and_lengths(lib, err):
     c = _attend_case(4, [(1, 100), (2, 40), (1, 50)], 4, 2, 64, 16, "int8", "bf16", False)
     bad = int(c["table"][0, 2])
