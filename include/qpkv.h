@@ -748,7 +748,8 @@ qpkv_status qpkv_write_page8(const qpkv_write_page8_params* params, void* stream
  * last sequence are left as they are.  kv head of q head h: h / (Hq / Hkv).
  *   q, o          [T, Hq, D] of dtype, contiguous; lse float [T, Hq] or NULL
  *   cu_seqlens_q  int32 [B] inclusive prefix sums; seqlens_kv int32 [B] (L)
- *   block_table   int32 [B, bt_stride]; entries past L are never read
+ *   block_table   int32 [B, bt_stride]; entries past L are never read, nor those
+ *                 of pages that lie before the window of every row
  *   alibi_slopes  float [Hq] or NULL; prefix_lens int32 [B] or NULL
  *   workspace     qpkv_attend_page8_workspace_bytes bytes, 16-byte aligned,
  *                 overwritten; calls that may overlap need one each

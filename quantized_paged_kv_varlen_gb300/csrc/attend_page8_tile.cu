@@ -177,12 +177,13 @@ __device__ __forceinline__ int items_of(const TileArgs& a, const Rows& r) {
   return (r.n + 2 * a.tq - 1) / (2 * a.tq);
 }
 
-// Key tiles [k0, k0 + n) that some row of item p sees.
-__device__ __forceinline__ int key_tiles(const TileArgs& a, const Rows& r, int p, int* k0) {
+// Keys [lo, ...) that some row of item p sees, and how many key tiles they
+// touch (from lo / kN on).
+__device__ __forceinline__ int key_tiles(const TileArgs& a, const Rows& r, int p, int* lo) {
   const int i0 = p * 2 * a.tq, i1 = min(r.n, i0 + 2 * a.tq) - 1;
-  const int lo = row_lo(a.p, r, i0), hi = row_hi(a.p, r, i1);
-  *k0 = lo / kN;
-  return hi > lo ? (hi - 1) / kN - lo / kN + 1 : 0;
+  const int hi = row_hi(a.p, r, i1);
+  *lo = row_lo(a.p, r, i0);
+  return hi > *lo ? (hi - 1) / kN - *lo / kN + 1 : 0;
 }
 __device__ __forceinline__ int units_of(int key_tiles) { return key_tiles > 0 ? key_tiles + kOverhead : 0; }
 
@@ -250,7 +251,7 @@ struct Walk {
   long long u, u_begin, u_end;
   long long item_u0;     // first unit of the item
   Item it;
-  int k0, nk;            // the item's key tiles
+  int lo, nk;            // the item's first key, and its key tiles
   int h, first, count;   // kv head; steps [first, first + count) of nk, newest key tile first
   int skip;              // units of the segment
   int has_b, seg;
@@ -261,7 +262,7 @@ struct Walk {
       while (u >= item_u0 + static_cast<long long>(units_of(nk)) * a.p.Hkv) {
         item_u0 += static_cast<long long>(units_of(nk)) * a.p.Hkv;
         it.next(a);
-        nk = key_tiles(a, it.r, it.p, &k0);
+        nk = key_tiles(a, it.r, it.p, &lo);
       }
       const int per = units_of(nk);
       const long long local = u - item_u0;
@@ -285,11 +286,11 @@ struct Walk {
     const int s = chunk_of(sh.seq_prefix, idx);
     it.find(a, s * lay.per_seq, idx - sh.seq_prefix[s]);
     item_u0 = sh.unit_prefix[c];
-    nk = key_tiles(a, it.r, it.p, &k0);
+    nk = key_tiles(a, it.r, it.p, &lo);
     open(a);
   }
   __device__ __forceinline__ bool valid() const { return u < u_end; }
-  __device__ __forceinline__ int key_tile() const { return k0 + nk - 1 - first - j; }
+  __device__ __forceinline__ int key_tile() const { return lo / kN + nk - 1 - first - j; }
   // n steps on, at most to the segment's end
   __device__ __forceinline__ void advance(const TileArgs& a, int n) {
     j += n;
@@ -358,8 +359,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
       Item it;
       it.find(ta, s * lay.per_seq, x0 - sh.seq_prefix[s]);
       for (long long x = x0; x < x1; ++x) {
-        int k0;
-        units += static_cast<long long>(units_of(key_tiles(ta, it.r, it.p, &k0))) * a.Hkv;
+        int lo;
+        units += static_cast<long long>(units_of(key_tiles(ta, it.r, it.p, &lo))) * a.Hkv;
         if (x + 1 < x1) it.next(ta);
       }
     }
@@ -383,8 +384,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
     x.r0 = 0;
     if (it.r.n > 0 && tok >= it.r.t0 && tok < it.r.t0 + it.r.n) {
       const int i = tok - it.r.t0, p = i / (2 * ta.tq), iq = i - p * 2 * ta.tq;
-      int k0;
-      x.ng = key_tiles(ta, it.r, p, &k0);
+      int lo;
+      x.ng = key_tiles(ta, it.r, p, &lo);
       x.stride = units_of(x.ng);
       x.r0 = iq / ta.tq * kT + iq % ta.tq * a.G;
       const int sc = b / lay.per_seq;
@@ -397,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
         const int s = chunk_of(sh.seq_prefix, from);
         it.find(ta, s * lay.per_seq, from - sh.seq_prefix[s]);
         for (long long q = from; q < idx; ++q) {
-          x.u0 += static_cast<long long>(units_of(key_tiles(ta, it.r, it.p, &k0))) * a.Hkv;
+          x.u0 += static_cast<long long>(units_of(key_tiles(ta, it.r, it.p, &lo))) * a.Hkv;
           it.next(ta);
         }
       }
@@ -424,7 +425,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
     const int swap = c >> 2 & 1, c0 = 2 * (c & 3);
     const uint32_t off0 = (c >> 2) * kHalfKv + row0 * 128 + ((((c0 + swap) ^ row0) & 7) << 4);
     const uint32_t off1 = (c >> 2) * kHalfKv + row0 * 128 + ((((c0 + 1 - swap) ^ row0) & 7) << 4);
-    // keys without codes (`all` false: behind the last, in a bad page) become zero
+    // keys without codes (`all` false: behind the last, before the window, in a bad
+    // page) become zero
     auto store = [&](uint8_t* dst, const uint8_t* src, const Step& s, bool all) {
 #pragma unroll
       for (int k = 0; k < kVecs; ++k) {
@@ -550,7 +552,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
       x.i0 = w.it.p * 2 * ta.tq;
       x.piece = 2 * blockIdx.x + (w.u == w.u_begin ? 0 : 1);
       const int gi = (x.j0 >> 4) - mine * kGroups + grp;
-      if (mine < x.n && gi * 16 < x.len) {
+      // 16 keys that lie wholly before the window of every row are no keys: their
+      // page may have been given back
+      if (mine < x.n && gi * 16 < x.len && gi >= w.lo / 16) {
         const int pg = gi / gpp;
         const int page = __ldg(a.bt + static_cast<size_t>(w.it.b) * a.bt_stride + pg);
         if (page >= 0 && page < a.num_pages) {

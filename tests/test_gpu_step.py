@@ -446,6 +446,27 @@ def test_attend_page8_segments_of_one_step(lib, err, reqs, Hq, H, D, fmt, dtype)
         assert torch.equal(got, first) and int(err) == 0
 
 
+@pytest.mark.parametrize("reqs", [[(130, 700)], [(300, 900), (40, 333), (1, 500)], [(1, 400), (3, 777)]], ids=["piece", "mixed", "split"])
+@pytest.mark.parametrize("fmt,dtype,ps", [("e4m3", "bf16", 16), ("int8", "f16", 32)])
+@pytest.mark.parametrize("entry", ["none", "junk"])
+def test_attend_page8_pages_before_the_window(lib, err, reqs, fmt, dtype, ps, entry):
+    """Pages that lie before every row's window may be given back: their entries
+    are -1, or those of a page that holds NaN codes and scales, and are not read."""
+    window = 70
+    c = _attend_case(15, reqs, 4, 2, 128, ps, fmt, dtype, False)
+    junk = sorted(set(range(c["pools"][0].shape[0])) - set(c["table"].reshape(-1).tolist()))[0]
+    c["dev"]["ks"][junk] = float("nan")
+    c["dev"]["vs"][junk] = float("inf")
+    for b, (n, L) in enumerate(reqs):
+        first = max(0, L - n + 1 - window) // ps
+        assert first > 0
+        c["dev"]["table"][b, :first] = -1 if entry == "none" else junk
+    lse = torch.empty(c["q"].shape[:2], device="cuda")
+    got = _run_attend(lib, c, err, max_q=max(n for n, _ in reqs), lse=lse, window=window)
+    assert int(err) == 0
+    _check_attend(c, got, lse, window=window)
+
+
 def test_attend_page8_forms_agree(lib, err):
     """The bound on a sequence's queries picks the kernels, never the result's
     meaning: without one, and with one that is too small to be a bound."""
