@@ -738,7 +738,8 @@ qpkv_status qpkv_write_page8(const qpkv_write_page8_params* params, void* stream
 /* Attention of varlen queries over the cache qpkv_write_page8 writes, from
  * single tokens to whole prompts.  Query i of sequence b (n rows, L cached
  * tokens, the new ones among them) has position at = L - n + i;
- *   x(i, j) = sm_scale * q_i . K_j, then cap * tanh(x / cap) with logit_cap > 0,
+ *   x(i, j) = sm_scale * q_i . K_j, then cap * tanh(x / cap) with logit_cap > 0
+ *             (off by 2e-5 at most up to a cap of 64, by 2^-19 of itself above),
  *             then + alibi_slopes[head] * (j - at) when given
  *   o_i = sum_j softmax_j(x(i, .)) V_j,  lse_i = ln sum_j exp(x(i, j))
  * over the keys j with

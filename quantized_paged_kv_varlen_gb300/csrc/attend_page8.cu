@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<D, NB>::kBlocks))
                 const RowInfo& q = ri[8 * nb + 2 * t + x];
                 o = fmaf(q.slope, static_cast<float>(j0 + g + 8 * e) - q.at, o);
               }
-              if constexpr (kCap) v = fmaf(a.cap_log2, tanh_of(v * f), o);
+              if constexpr (kCap) v = fmaf(a.cap_log2, a.far_cap ? tanh_far(v * f) : tanh_of(v * f), o);
               else v = fmaf(v, f, o);
             }
           }

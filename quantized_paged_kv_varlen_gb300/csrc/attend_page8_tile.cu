@@ -302,7 +302,12 @@ struct Walk {
   }
 };
 
-template <typename E, int D, bool kInt8, bool kCap, bool kBias>
+// Scores without a cap, with one up to kNearCap, with one above: forms of their
+// own, as the far caps' code beside the near ones' cost those 7 % (a prompt of
+// 8192: 925 us against 860).
+enum : int { kNone = 0, kNear = 1, kFar = 2 };
+
+template <typename E, int D, bool kInt8, int kCap, bool kBias>
 __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                        const __grid_constant__ CUtensorMap v_map, const __grid_constant__ TileArgs ta) {
   using L = Smem<D>;
@@ -768,30 +773,56 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
       tmem_ld32(srow + 32, v[1]);
       float rvs[kGroups], top = -INFINITY;
       tmem_ld_wait();
+      if constexpr (kCap == kFar) {
+        // 16 columns at a time through TMEM: unrolled, all 64 do not fit the instruction
+        // cache (a prompt of 8192 with a cap of 1000: 1.53 ms against 1.18)
+#pragma unroll 1
+        for (int q = 0; q < kGroups; ++q) {
+          uint32_t w[16];
+          tmem_ld16(srow + 16 * q, w);
+          const float4 s4 = gs[q];
+          const bool bad = __float_as_uint(s4.x) == kBadPageMark;
+          const float f = bad ? 0.f : sc * s4.x, off = bad ? -INFINITY : s4.y - m;
+          tmem_ld_wait();
 #pragma unroll
-      for (int q = 0; q < kGroups; ++q) {
-        uint32_t(&w)[32] = v[q >> 1];
-        const float4 s4 = gs[q];
-        rvs[q] = s4.z;
-        const bool bad = __float_as_uint(s4.x) == kBadPageMark;
-        const float f = bad ? 0.f : sc * s4.x, off = bad ? -INFINITY : s4.y - m;
-        const int w0 = 16 * (q & 1);
-        if constexpr (!kCap && !kBias) {
-          const uint64_t f2 = f32x2_pack(f, f), o2 = f32x2_pack(off, off);
-#pragma unroll
-          for (int i = w0; i < w0 + 16; i += 2) {
-            const float2 z = f32x2_unpack(
-                f32x2_fma(f32x2_pack(__uint_as_float(w[i]), __uint_as_float(w[i + 1])), f2, o2));
-            w[i] = __float_as_uint(z.x);
-            w[i + 1] = __float_as_uint(z.y);
+          for (int i = 0; i < 16; ++i) {
+            const float o = kBias ? fmaf(slope, static_cast<float>(j0 + 16 * q + i - at), off) : off;
+            w[i] = __float_as_uint(fmaf(a.cap_log2, tanh_far(__uint_as_float(w[i]) * f), o));
           }
-        } else {
+          tmem_st16(srow + 16 * q, w);
+        }
+        tmem_st_wait();
+        tmem_ld32(srow, v[0]);
+        tmem_ld32(srow + 32, v[1]);
 #pragma unroll
-          for (int i = w0; i < w0 + 16; ++i) {
-            float o = off;
-            if constexpr (kBias) o = fmaf(slope, static_cast<float>(j0 + 32 * (q >> 1) + i - at), o);
-            const float s = __uint_as_float(w[i]);
-            w[i] = __float_as_uint(kCap ? fmaf(a.cap_log2, tanh_of(s * f), o) : fmaf(s, f, o));
+        for (int q = 0; q < kGroups; ++q) rvs[q] = gs[q].z;
+        tmem_ld_wait();
+      } else {
+#pragma unroll
+        for (int q = 0; q < kGroups; ++q) {
+          uint32_t(&w)[32] = v[q >> 1];
+          const float4 s4 = gs[q];
+          rvs[q] = s4.z;
+          const bool bad = __float_as_uint(s4.x) == kBadPageMark;
+          const float f = bad ? 0.f : sc * s4.x, off = bad ? -INFINITY : s4.y - m;
+          const int w0 = 16 * (q & 1);
+          if constexpr (!kCap && !kBias) {
+            const uint64_t f2 = f32x2_pack(f, f), o2 = f32x2_pack(off, off);
+#pragma unroll
+            for (int i = w0; i < w0 + 16; i += 2) {
+              const float2 z = f32x2_unpack(
+                  f32x2_fma(f32x2_pack(__uint_as_float(w[i]), __uint_as_float(w[i + 1])), f2, o2));
+              w[i] = __float_as_uint(z.x);
+              w[i + 1] = __float_as_uint(z.y);
+            }
+          } else {
+#pragma unroll
+            for (int i = w0; i < w0 + 16; ++i) {
+              float o = off;
+              if constexpr (kBias) o = fmaf(slope, static_cast<float>(j0 + 32 * (q >> 1) + i - at), o);
+              const float s = __uint_as_float(w[i]);
+              w[i] = __float_as_uint(kCap ? fmaf(a.cap_log2, tanh_of(s * f), o) : fmaf(s, f, o));
+            }
           }
         }
       }
@@ -911,7 +942,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
   }
 }
 
-template <typename E, int D, bool kInt8, bool kCap, bool kBias>
+template <typename E, int D, bool kInt8, int kCap, bool kBias>
 cudaError_t go(const TileArgs& a, int sms, cudaStream_t stream) {
   auto kernel = attend_tile_kernel<E, D, kInt8, kCap, kBias>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
@@ -940,8 +971,9 @@ cudaError_t go(const TileArgs& a, int sms, cudaStream_t stream) {
 template <typename E, int D, bool kInt8>
 cudaError_t pick2(const TileArgs& a, int sms, cudaStream_t s) {
   const bool cap = a.p.cap_log2 > 0.f, bias = a.p.slopes != nullptr;
-  if (cap) return bias ? go<E, D, kInt8, true, true>(a, sms, s) : go<E, D, kInt8, true, false>(a, sms, s);
-  return bias ? go<E, D, kInt8, false, true>(a, sms, s) : go<E, D, kInt8, false, false>(a, sms, s);
+  if (a.p.far_cap) return bias ? go<E, D, kInt8, kFar, true>(a, sms, s) : go<E, D, kInt8, kFar, false>(a, sms, s);
+  if (cap) return bias ? go<E, D, kInt8, kNear, true>(a, sms, s) : go<E, D, kInt8, kNear, false>(a, sms, s);
+  return bias ? go<E, D, kInt8, kNone, true>(a, sms, s) : go<E, D, kInt8, kNone, false>(a, sms, s);
 }
 
 template <typename E>

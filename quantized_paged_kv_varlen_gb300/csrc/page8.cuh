@@ -16,6 +16,9 @@ constexpr float kSetP = 7.0f, kMaxP = 15.0f;
 // no row's m away from those that count.  P <= 2^kMaxP over it, summed over
 // fewer than 2^31 keys, stays in float32.
 constexpr float kMinScale = 8.271806e-25f;   // 2^-80
+// A cap multiplies the error of tanh_of: up to this one to 2e-5 of a logit at
+// most, above it scores would drown in it (0.1 of a logit at a cap of 1e6).
+constexpr float kNearCap = 64.f;
 
 struct Page8Args {
   int B, T, Hq, Hkv, G, ps, num_pages, bt_stride, causal, window, hnd;
@@ -23,6 +26,7 @@ struct Page8Args {
   float scale_log2;        // softmax scale * log2(e)
   float scale_cap;         // softmax scale / cap
   float cap_log2;          // cap * log2(e), 0: no cap
+  int far_cap;             // a cap above kNearCap
   const int32_t *cu, *lens, *bt, *prefix;
   const float *slopes, *ks, *vs;
   const void* q;
@@ -43,6 +47,7 @@ inline Page8Args page8_args(const qpkv_attend_page8_params& p) {
   a.scale_log2 = scale * kLog2e;
   a.scale_cap = p.logit_cap > 0.f ? scale / p.logit_cap : 0.f;
   a.cap_log2 = p.logit_cap > 0.f ? p.logit_cap * kLog2e : 0.f;
+  a.far_cap = p.logit_cap > kNearCap;
   a.hnd = p.kv_layout == QPKV_KV_LAYOUT_HND;
   a.cu = p.cu_seqlens_q, a.lens = p.seqlens_kv, a.bt = p.block_table, a.prefix = p.prefix_lens;
   a.slopes = p.alibi_slopes, a.ks = p.k_scale, a.vs = p.v_scale;
@@ -153,6 +158,17 @@ __device__ __forceinline__ float tanh_of(float x) {
   const float d = 1.f + fast_exp2(x * (2.f * kLog2e));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
   return fmaf(-2.f, r, 1.f);
+}
+// tanh(x) for caps above kNearCap, good to 2^-19 of itself: below 1/2 Taylor's series
+// up to x^11 (off by its next term, 9e-7 of x), from there on the form above
+// (3e-7, which is 7e-7 of tanh(1/2)).
+__device__ __forceinline__ float tanh_far(float x) {
+  const float t = x * x;
+  float p = fmaf(-1382.f / 155925.f, t, 62.f / 2835.f);
+  p = fmaf(p, t, -17.f / 315.f);
+  p = fmaf(p, t, 2.f / 15.f);
+  p = fmaf(p, t, -1.f / 3.f);
+  return fabsf(x) < 0.5f ? fmaf(x * t, p, x) : tanh_of(x);
 }
 
 // The power of two that takes a row of bf16 values with the given largest

@@ -545,6 +545,22 @@ def test_attend_page8_denominators_stay_finite(lib, err, n):
     assert float((got.double() / (100 * 2.0 ** -80) - 1).abs().max()) <= 2.0 ** -8 + 2.0 ** -9 and int(err) == 0
 
 
+@pytest.mark.parametrize("cap", [2.0, 1e3, 1e6, 1e9])
+@pytest.mark.parametrize("reqs,max_q", [(DECODE, 1), ([(1, 300), (5, 130), (3, 77)], 5), ([(130, 400), (1, 50)], 130)],
+                         ids=["decode", "drafts", "tiles"])
+@pytest.mark.parametrize("slopes", [False, True])
+def test_attend_page8_caps_of_any_size(lib, err, cap, reqs, max_q, slopes):
+    """A cap far above the scores is no cap: the capped score's error stays
+    relative to the score (2^-19 of it), not to the cap.  Scores of |x| < 2^8 so
+    stay within the 2^-11 and the 2^-17 (1 + |x|) of this file."""
+    for i, (fmt, dtype) in enumerate((("int8", "f16"), ("e4m3", "bf16"))):
+        c = _attend_case(16 + i, reqs, 6, 2, (64, 128)[i], 16, fmt, dtype, False, slopes=slopes)
+        lse = torch.empty(c["q"].shape[:2], device="cuda")
+        got = _run_attend(lib, c, err, max_q=max_q, lse=lse, logit_cap=cap)
+        _check_attend(c, got, lse, logit_cap=cap)
+    assert int(err) == 0
+
+
 def test_attend_page8_skips_bad_pages_and_lengths(lib, err):
     c = _attend_case(4, [(1, 100), (2, 40), (1, 50)], 4, 2, 64, 16, "int8", "bf16", False)
     bad = int(c["table"][0, 2])
