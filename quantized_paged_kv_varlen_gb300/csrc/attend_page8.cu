@@ -137,7 +137,8 @@ struct Shape {
 struct RowInfo {
   int lo, hi;         // keys the row sees
   float sc;           // logit multiplier
-  float slope, at;    // bias: slope * (j - at), log2 units
+  float slope, at;    // bias: slope * (j - at), log2 units; at and j from the end of the
+                      // cache, as float32 holds no odd position beyond 2^24
 };
 
 template <typename E, int D, bool kInt8, bool kCap, bool kBias, int NB>
@@ -358,7 +359,7 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<D, NB>::kBlocks))
         x.hi = hi;
         x.sc = inv * (kCap ? a.scale_cap : a.scale_log2);
         x.slope = kBias ? __ldg(a.slopes + head) * kLog2e : 0.f;
-        x.at = static_cast<float>(sp.len - sp.n + i);
+        x.at = static_cast<float>(i - sp.n);
         ri[r] = x;
       }
     }
@@ -467,7 +468,7 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<D, NB>::kBlocks))
               float o = off;
               if constexpr (kBias) {
                 const RowInfo& q = ri[8 * nb + 2 * t + x];
-                o = fmaf(q.slope, static_cast<float>(j0 + g + 8 * e) - q.at, o);
+                o = fmaf(q.slope, static_cast<float>(j0 + g + 8 * e - sp.len) - q.at, o);
               }
               if constexpr (kCap) v = fmaf(a.cap_log2, a.far_cap ? tanh_far(v * f) : tanh_of(v * f), o);
               else v = fmaf(v, f, o);

@@ -561,6 +561,24 @@ def test_attend_page8_caps_of_any_size(lib, err, cap, reqs, max_q, slopes):
     assert int(err) == 0
 
 
+@pytest.mark.parametrize("n", [3, 40], ids=["split", "tiles"])
+def test_attend_page8_bias_at_far_positions(lib, err, n):
+    """Behind 2^24 tokens float32 holds every second position only; the bias
+    takes the distance of a key, which is small, and gives what it gives for
+    the same pages near the start."""
+    c = _attend_case(17, [(n, 217)], 2, 1, 64, 16, "int8", "f16", False)
+    c["slopes"] = np.array([0.5, 1.0], np.float32)
+    c["dev"]["slopes"] = torch.tensor(c["slopes"]).cuda()
+    far = 1 << 24
+    d = c["dev"]
+    d["table"] = torch.cat([torch.zeros(1, far // 16, dtype=torch.int32, device="cuda"), d["table"]], 1).contiguous()
+    d["lens"] = d["lens"] + far
+    lse = torch.empty(c["q"].shape[:2], device="cuda")
+    got = _run_attend(lib, c, err, max_q=n, lse=lse, window=100)
+    assert int(err) == 0
+    _check_attend(c, got, lse, window=100)
+
+
 def test_attend_page8_skips_bad_pages_and_lengths(lib, err):
     c = _attend_case(4, [(1, 100), (2, 40), (1, 50)], 4, 2, 64, 16, "int8", "bf16", False)
     bad = int(c["table"][0, 2])
