@@ -745,8 +745,9 @@ qpkv_status qpkv_write_page8(const qpkv_write_page8_params* params, void* stream
  * over the keys j with
  *   j < L, and when causal j <= at or j < prefix_lens[b] (a prefix whose
  *   tokens see one another), and with window > 0 also j > at - window.
- * Rows that see no key get o = 0 and lse = -inf; rows of o and lse behind the
- * last sequence are left as they are.  kv head of q head h: h / (Hq / Hkv).
+ * Rows that see no key get o = 0 and lse = -inf, rows with a NaN score NaN;
+ * rows of o and lse behind the last sequence are left as they are.  kv head of
+ * q head h: h / (Hq / Hkv).
  *   q, o          [T, Hq, D] of dtype, contiguous; lse float [T, Hq] or NULL
  *   cu_seqlens_q  int32 [B] inclusive prefix sums; seqlens_kv int32 [B] (L)
  *   block_table   int32 [B, bt_stride]; entries past L are never read, nor those

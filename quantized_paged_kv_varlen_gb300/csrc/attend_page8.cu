@@ -555,13 +555,8 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<D, NB>::kBlocks))
       }
       __syncwarp();   // the stage may be filled again
     }
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-      for (int x = 0; x < 2; ++x)
-        if (!(seen >> (2 * nb + x) & 1)) m[nb][x] = -INFINITY;
-
-    // ---- the run's part of this task: dims [VB g, VB g + VB) of columns 2t, 2t + 1
+    // ---- the run's part of this task: dims [VB g, VB g + VB) of columns 2t, 2t + 1.
+    // l = 0: no key seen; NaN (of a NaN score, which moves no m) goes into o and lse.
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
@@ -572,7 +567,7 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<D, NB>::kBlocks))
         if (whole_task) {
           const int rr = rt * 8 * NB + r, i = rr / a.G, head = h * a.G + (rr - i * a.G);
           const size_t row = static_cast<size_t>(sp.t0 + i) * a.Hq + head;
-          const float so = lsum > 0.f ? 1.f / lsum : 0.f;
+          const float so = lsum == 0.f ? 0.f : 1.f / lsum;
           uint32_t w[NT];
 #pragma unroll
           for (int n = 0; n < NT; ++n) w[n] = pack_out<E>(O[nb][n][2 + x] * so, O[nb][n][x] * so);
@@ -580,13 +575,13 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<D, NB>::kBlocks))
 #pragma unroll
           for (int n = 0; n < NT / 4; ++n) out[n] = make_uint4(w[4 * n], w[4 * n + 1], w[4 * n + 2], w[4 * n + 3]);
           if (g == 0 && a.lse != nullptr)
-            a.lse[row] = lsum > 0.f ? (m[nb][x] + log2f(lsum)) * kLn2 : -INFINITY;
+            a.lse[row] = lsum == 0.f ? -INFINITY : (m[nb][x] + log2f(lsum)) * kLn2;
         } else {
           float4* out = reinterpret_cast<float4*>(sa.part_o + (piece * (8 * NB) + r) * D + VB * g);
 #pragma unroll
           for (int n = 0; n < NT / 2; ++n)
             out[n] = make_float4(O[nb][2 * n][x], O[nb][2 * n][2 + x], O[nb][2 * n + 1][x], O[nb][2 * n + 1][2 + x]);
-          if (g == 0) sa.part_ml[piece * (8 * NB) + r] = make_float2(m[nb][x], lsum);
+          if (g == 0) sa.part_ml[piece * (8 * NB) + r] = make_float2(lsum == 0.f ? -INFINITY : m[nb][x], lsum);
         }
       }
     }
@@ -688,12 +683,12 @@ __global__ void __launch_bounds__(kPer > 8 ? 32 * kPer : 256) attend_join_kernel
     }
     if (write) {
       const size_t row = static_cast<size_t>(tok) * a.Hq + head;
-      const float so = l > 0.f ? 1.f / l : 0.f;
+      const float so = l == 0.f ? 0.f : 1.f / l;
       E* out = static_cast<E*>(a.o) + row * D + lane * EPL;
 #pragma unroll
       for (int e = 0; e < EPL; e += 2)
         *reinterpret_cast<uint32_t*>(out + e) = pack_out<E>(acc[e + 1] * so, acc[e] * so);
-      if (lane == 0 && a.lse != nullptr) a.lse[row] = l > 0.f ? (M + log2f(l)) * kLn2 : -INFINITY;
+      if (lane == 0 && a.lse != nullptr) a.lse[row] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
     }
     if (kPer > 1) return;
   }

@@ -893,9 +893,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
         // ---- the segment's rows, once its last PV has landed (and with it the one before)
         if (!warp_await(&sh.o_done[x][(cnt - 1) & 1], ((cnt - 1) >> 1) & 1, sh, a.err)) break;
         tc_fence_after_sync();
-        const float lse2 = seen && l > 0.f ? m + log2f(l) : -INFINITY;
+        // l = 0: no key seen; NaN (of a NaN score, which moves no m) goes into o and lse
+        const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
         if (flags & kWholeTask) {
-          const float so = l > 0.f ? 1.f / l : 0.f;
+          const float so = l == 0.f ? 0.f : 1.f / l;
           E* out = static_cast<E*>(a.o) + row * D;
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
@@ -914,7 +915,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
               }
             }
           }
-          if (live && a.lse != nullptr) a.lse[row] = lse2 > -INFINITY ? lse2 * kLn2 : -INFINITY;
+          if (live && a.lse != nullptr) a.lse[row] = lse2 * kLn2;
         } else {
           float* out = ta.part_o + row * D;
 #pragma unroll 1
@@ -928,7 +929,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
               for (int i = 0; i < 8; ++i) o4[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
             }
           }
-          if (live) ta.part_ml[row] = make_float2(seen ? m : -INFINITY, l);
+          if (live) ta.part_ml[row] = make_float2(l == 0.f ? -INFINITY : m, l);
         }
         tc_fence_before_sync();
       }

@@ -579,6 +579,37 @@ def test_attend_page8_bias_at_far_positions(lib, err, n):
     _check_attend(c, got, lse, window=100)
 
 
+@pytest.mark.parametrize("reqs,max_q", [([(1, 9), (1, 30), (2, 40)], 2), ([(1, 9000), (3, 30)], 3), ([(60, 300), (1, 40)], 60),
+                                        ([(60, 60)] * 200, 60)], ids=["whole", "pieces", "tiles", "whole_tiles"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_attend_page8_nan_queries_give_nan(lib, err, reqs, max_q, dtype):
+    """A query with a NaN: NaN in its own rows of o and lse and in no others.
+    (Those may round otherwise than beside a number: a warp's rows look at their
+    running maxima together, m = maximum - 7 moves when one of them needs it, and
+    P = 2^(y - m) rounds to f16 at other places.  So the others are held to this
+    file's tolerance, which any m within the range of P keeps.)"""
+    c = _attend_case(18, reqs, 4, 2, 64, 16, "int8", dtype, False)
+    T = c["T"]
+
+    class Rows(np.ndarray):     # a request of one page: an index of one element is still an array
+        def __getitem__(self, i):
+            return np.asarray(self)[np.asarray(i) if isinstance(i, torch.Tensor) else i]
+
+    want, want_lse, size = _attend_64bit({**c, **{k: [x.view(Rows) for x in c[k]] for k in ("pools", "scales")}})
+    lse = torch.empty(T, 4, device="cuda")
+    rows = torch.zeros(T, 4, dtype=torch.bool, device="cuda")
+    rows[0, 1] = rows[T // 2, 2] = rows[T - 1, 0] = True
+    c["dev"]["q"][rows] = float("nan")
+    got = _run_attend(lib, c, err, max_q=max_q, lse=lse)
+    assert torch.isnan(got[rows]).all() and torch.isnan(lse[rows]).all() and int(err) == 0
+    eps = torch.finfo(got.dtype).eps / 2
+    flush = 2.0 ** -32 * float(c["scales"][1].max()) * 127 * max(L for _, L in reqs)
+    tol = eps * want.abs() + 2.0 ** -10 * size * (1 + eps) + flush + (2.0 ** -25 if dtype == "f16" else 0)
+    assert ((got.double() - want).abs() <= tol)[~rows].all()
+    off = (lse - want_lse)[~rows].abs().max()
+    assert float(off) <= 2.0 ** -17 * (4 + 2 * float(want_lse.abs().max()))
+
+
 def test_attend_page8_skips_bad_pages_and_lengths(lib, err):
     c = _attend_case(4, [(1, 100), (2, 40), (1, 50)], 4, 2, 64, 16, "int8", "bf16", False)
     bad = int(c["table"][0, 2])
