@@ -1083,6 +1083,8 @@ def attend_page8(q, k_pool, v_pool, k_scale, v_scale, block_table, cu_seqlens_q,
     else:
         if workspace.get_device() != dev:
             raise ValueError("workspace must live on the current device")
+        if not workspace.is_contiguous():   # its bytes would not be those it is said to have
+            raise ValueError("workspace must be contiguous")
         n = workspace.numel() * workspace.element_size()
     p = AttendPage8Params(
         B, T, max_seqlen_q, Hq, H, D, ps, P, W, _dtype_code(dtype), fmt, layout,

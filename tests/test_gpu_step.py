@@ -863,3 +863,15 @@ def test_step_entry_points_refuse_other_tensors(lib):
         lib.rope_axes(x, i32([[0, 1, 2]]), bytes([1] * 32), cos, sin)
     with pytest.raises(ValueError):
         lib.rope_axes(x, i32([[0, 1, 2]]), bytes(16), cos, sin)
+
+
+def test_attend_page8_refuses_a_workspace_with_gaps(lib):
+    """An expanded byte or every second one: as many elements as asked for, but
+    not their bytes in a row."""
+    c = _attend_case(1, [(1, 20)], 4, 2, 64, 16, "int8", "bf16", False)
+    d = c["dev"]
+    n = lib.attend_page8_workspace(1, 1, 4, 2, 64).numel()
+    for ws in (torch.empty(1, dtype=torch.uint8, device="cuda").expand(n), torch.empty(2 * n, dtype=torch.uint8, device="cuda")[::2],
+               torch.empty(n, dtype=torch.uint8)):
+        with pytest.raises(ValueError):
+            lib.attend_page8(d["q"], d["kp"], d["vp"], d["ks"], d["vs"], d["table"], d["cu"], d["lens"], workspace=ws)
