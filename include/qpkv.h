@@ -763,7 +763,8 @@ qpkv_status qpkv_write_page8(const qpkv_write_page8_params* params, void* stream
  * A key whose page id lies outside [0, num_pages) is skipped
  * (QPKV_DEV_ERR_BAD_PAGE).  A sequence whose rows or length do not fit the
  * arrays has no rows or no keys (QPKV_DEV_ERR_BAD_LENGTH).
- * max_seqlen_q (a host bound on any n, <= 0: unknown) only picks the kernels.
+ * max_seqlen_q (a host bound on any n, <= 0: unknown) only picks the kernels,
+ * whose times differ: a batch of single tokens wants 1 here.
  * sm_scale <= 0 selects 1/sqrt(D).
  * Errors: INVALID_ARG (null or misaligned pointers, negative sizes, a cap
  * that is negative, below 1e-20 but not 0, or not finite), UNSUPPORTED (D not 64 or 128, page_size

@@ -38,9 +38,13 @@
 // last piece may be partial and go to the workspace for the join kernel.  Each
 // (item, kv head) counts kOverhead units more than its key tiles, for its
 // queries' load and its results' store (a causal prompt begins with many items
-// of one key tile).  9: the prompt of 8192 534 us, against 680 (4), 631 (5), 575
-// (6), 544 (7), 541 (12); over thirteen batches of prompts and pieces 7 to 12 are
-// within 1 %.
+// of one key tile).  9: the prompt of 8192 took 534 us when this was measured (516
+// now), against 680 (4), 631 (5), 575 (6), 544 (7), 541 (12); over thirteen
+// batches of prompts and pieces 7 to 12 were within 1 %.
+//
+// The prompt of 8192 with options, us: plain 516, window of 1024 204, bias 627,
+// cap of 50 864 (an exponential and a reciprocal a score more), both 1027, a cap
+// above kNearCap 1183.
 #include <climits>
 
 #include "common.cuh"

@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kWarps * 32) rope_axes_kernel(const __grid_con
       for (int e = 0; e < V; ++e) d[e] = -d[e];
     }
     using VE = Vec<E, V>;
-#pragma unroll 1   // more warps rather than more loads a warp: 59 us against 66 (unroll 4) for 16384 tokens
+#pragma unroll 1   // more warps rather than more loads a warp: 57 us against 66 (unroll 4) for 16384 tokens
     for (int h = h0 + hl; h < h1; h += side) {
       const bool isq = h < a.Hq;
       const int hh = isq ? h : h - a.Hq;

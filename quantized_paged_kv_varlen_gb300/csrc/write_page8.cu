@@ -261,7 +261,7 @@ cudaError_t go(const WriteArgs& a, cudaStream_t stream) {
   WriteArgs w = a;
   // up to eight heads one after another, the next one's loads ahead of the work
   // on this one's, while that leaves every SM eight blocks (8 prompts of 32
-  // heads: 177 us with one, 112 with two, 97 with eight)
+  // heads: 177 us with one, 112 with two, 97 with eight; 93 now, with the redo by words)
   const long long pieces = (a.T / a.ps + 2ll * a.B) * 2;
   w.rounds = 8;
   while (w.rounds > 1 && (a.H < groups * w.rounds || pieces * (a.H / (groups * w.rounds)) < 152 * 8)) w.rounds /= 2;
