@@ -598,7 +598,8 @@ qpkv_status qpkv_mla_sparse_decode(const qpkv_mla_params* params, void* stream);
  *   slot_mapping     int32 [num_tokens]: page * page_size + offset of each token
  *   positions        int32 [num_tokens]: L, L + 1, ... of its request
  *   start_pos        int32 [B] or NULL: L, where qpkv_write_page8 appends, or -1
- *                    for a refused request, of which it then writes nothing
+ *                    for a refused request, of which it then writes nothing;
+ *                    may be the seqlens array, when that is not seqlens_out
  * Rows of slot_mapping / positions behind the last token get -1, so that T
  * may be the fixed size of a captured graph.  A request is refused (its
  * length and row stay, its tokens get slot and position -1) when the demand

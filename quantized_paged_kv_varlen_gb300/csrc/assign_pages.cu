@@ -132,12 +132,12 @@ __global__ void __launch_bounds__(kThreads, 1) assign_pages_kernel(const qpkv_as
   for (int b = me; b < B; b += step) {
     const int n = s_end[b] - (b > 0 ? s_end[b - 1] : 0);
     p.cu_seqlens[b] = s_end[b];
-    if (p.start_pos != nullptr) p.start_pos[b] = s_first[b] >= 0 ? s_old[b] : -1;
     if (s_first[b] >= 0) {
       p.seqlens_out[b] = s_old[b] + n;
     } else if (p.seqlens_out != p.seqlens) {
       p.seqlens_out[b] = p.seqlens[b];
     }
+    if (p.start_pos != nullptr) p.start_pos[b] = s_first[b] >= 0 ? s_old[b] : -1;   // may be seqlens itself
   }
   // free page i of the demand
   auto fresh = [&](int i) -> int {

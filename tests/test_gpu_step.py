@@ -103,6 +103,20 @@ def test_assign_pages_refuses_what_does_not_fit(lib, err):
     assert got[4].tolist() == [-1] and got[0][3].tolist() == [-1, -1] and int(err) == lib.DEV_ERR_BAD_PAGE
 
 
+def test_assign_pages_start_pos_may_take_the_lengths_place(lib, err):
+    """start_pos over seqlens, the grown lengths elsewhere: every length is read
+    before its place is written, a refused request's too."""
+    new, lens, table, pages, count, P = _assign_case(40, 1500, 5, 16, 70, 30, 600)
+    T = int(new.sum())
+    want = step.assign_pages(new, lens, table, pages, count, 16, T)
+    d = [i32(x) for x in (new, lens, table, pages, [count])]
+    got = lib.assign_pages(*d, 16, P, T, error_word=err, start_pos=d[1])
+    assert len(want[6]) > 100 and int(err) == lib.DEV_ERR_NO_PAGES
+    for g, w in zip(got, want):
+        assert np.array_equal(g.cpu().numpy().reshape(-1), np.asarray(w).reshape(-1))
+    assert np.array_equal(d[1].cpu().numpy(), np.where(np.isin(np.arange(1500), want[6]), -1, lens))
+
+
 # ------------------------------------------------------------ rotary positions
 
 @pytest.mark.parametrize("T,Hq,Hkv,D,sections,inter,dtype,fused", [
