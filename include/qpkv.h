@@ -99,7 +99,9 @@ int32_t qpkv_version(void);
  * languages can check their mirror of the layout:
  * which = 0 -> qpkv_write_params, 1 -> qpkv_prefill_params,
  * 2 -> qpkv_mla_params, 3 -> qpkv_assign_params, 4 -> qpkv_rope_axes_params,
- * 5 -> qpkv_write_page8_params, 6 -> qpkv_attend_page8_params.  Unknown
+ * 5 -> qpkv_write_page8_params, 6 -> qpkv_attend_page8_params,
+ * 7 -> qpkv_write_group4_params, 8 -> qpkv_read_group4_params,
+ * 9 -> qpkv_select_pages_params, 10 -> qpkv_attend_group4_params.  Unknown
  * `which` returns 0. */
 size_t qpkv_struct_size(int32_t which);
 
@@ -811,6 +813,222 @@ size_t qpkv_attend_page8_workspace_bytes(int32_t num_seqs, int32_t num_tokens, i
                                          int32_t num_heads_kv, int32_t head_dim);
 
 qpkv_status qpkv_attend_page8(const qpkv_attend_page8_params* params, void* stream);
+
+/* ----------------------------------------------------- a cache in 4 bits
+ * The entry points below keep a paged cache in 4 bits and attend to it:
+ *   qpkv_write_group4   rotate k (and q), append k, v, renew key bounds
+ *   qpkv_read_group4    cached tokens back as bf16 / f16
+ *   qpkv_select_pages   the pages each query token attends to, by key bounds
+ *   qpkv_attend_group4  attention over all keys, or over the pages selected
+ * Like the entry points above they plan nothing on the host, wait for the
+ * kernel before them on the stream, and may be captured.
+ *
+ * A value is an E2M1 code (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign) times an
+ * E4M3 scale that it shares with 16 channels of its token and head, times
+ * k_mul[head] or v_mul[head] (positive floats, NULL: ones).  Sixteen tokens
+ * of a page and head lie together, 9 D bytes: 16 rows of D / 2 bytes of codes
+ * (byte c: channel 2c in the low half, 2c + 1 in the high), then 16 rows of
+ * D / 16 scales.  Pools: u8 [P, Hkv, page_size / 16, 9 D], K and V each.
+ * Codes times scales are exact in f16 and bf16. */
+
+/* Append k, v.  New token t of sequence b goes to position p = start_pos[b] +
+ * (t - begin_b), page block_table[b, p / page_size].  With rope tables the
+ * first rot_dim elements of k (and of q, to q_out) are rotated before, pair i
+ * being elements i and i + rot_dim / 2, by table row p; products and sums are
+ * rounded to float32 one by one.  k is quantised from there, q rounded once
+ * to its type.  For each 16 channels x of a token, x / mul first where given,
+ *   s = E4M3(min(448, amax / 6)),  code = E2M1(x / s)  (both to nearest, ties
+ *   to even, divisions IEEE float32); s = 0 gives zero codes; a NaN or an
+ *   infinity among the 16 gives s = NaN, which all 16 then read as.
+ * With k_bounds the pages written get the bounds of their cached keys (those
+ * at positions below start_pos[b] + the new tokens) in units of the pool: per
+ * channel floor(min / u) and ceil(max / u) with u, the smallest 2^e >= 2^-10
+ * that keeps them within +-127, in bound_scale; u = inf (and zeros) when a
+ * scale is NaN.  They depend on the page's codes alone.
+ *   k, v, q, q_out  [T, H, D] of dtype with strides per token and head, q_out
+ *                 may be q with equal strides; q NULL: none
+ *   k_bounds      int8 [P, Hkv, 2, D] (min, max) or NULL; bound_scale float
+ *                 [P, Hkv]
+ *   start_pos     int32 [B] or NULL (all zero); -1: nothing of the sequence is
+ *                 written, q_out included (a request that qpkv_assign_pages refused)
+ * Slots behind the new tokens, other pages and rows behind the last sequence
+ * are left as they are.  A page may be written for one sequence only per call.
+ * A sequence whose rows do not fit T, or whose positions leave the rope
+ * tables, is left out (QPKV_DEV_ERR_BAD_LENGTH), so are positions past the
+ * table row; page ids outside [0, num_pages) are skipped
+ * (QPKV_DEV_ERR_BAD_PAGE).
+ * Errors: INVALID_ARG (null pointers, non-positive sizes, one of the tables or
+ * of k_bounds / bound_scale without the other, q without tables or q_out,
+ * pointers not 16-byte aligned (scales and mul: 4), strides not multiples of 8
+ * elements), UNSUPPORTED (D not 64 or 128, page_size not a multiple of 16,
+ * rot_dim not a multiple of 32 or above D, dtype, sizes whose blocks exceed a
+ * grid), CUDA. */
+typedef struct qpkv_write_group4_params {
+  int32_t num_seqs;      /* B */
+  int32_t num_tokens;    /* T */
+  int32_t num_heads_q;   /* ignored without q */
+  int32_t num_heads_kv;
+  int32_t head_dim;      /* 64 or 128 */
+  int32_t page_size;
+  int32_t num_pages;
+  int32_t bt_stride;
+  int32_t dtype;         /* QPKV_DTYPE_BF16 or _F16 */
+  int32_t rot_dim;       /* ignored without tables */
+  int32_t rope_max_pos;  /* rows of the tables */
+  int32_t pad0;
+  int64_t k_stride_t, k_stride_h, v_stride_t, v_stride_h;
+  int64_t q_stride_t, q_stride_h, q_out_stride_t, q_out_stride_h;
+  const int32_t* cu_seqlens_q;
+  const int32_t* start_pos;
+  const int32_t* block_table;
+  const void* k;
+  const void* v;
+  const void* q;
+  void* q_out;
+  const float* rope_cos; /* [rope_max_pos, rot_dim / 2] or NULL */
+  const float* rope_sin;
+  const float* k_mul;    /* [Hkv] or NULL */
+  const float* v_mul;
+  void* k_pool;
+  void* v_pool;
+  void* k_bounds;
+  float* bound_scale;
+  int32_t* error_word;
+} qpkv_write_group4_params;
+
+qpkv_status qpkv_write_group4(const qpkv_write_group4_params* params, void* stream);
+
+/* Cached tokens back: row t of sequence b is the token at position
+ * start_pos[b] + (t - begin_b) (start_pos NULL: zero), code * scale * mul
+ * rounded once to dtype.  k_out, v_out [T, Hkv, D], contiguous; either may be
+ * NULL.  Rows of a sequence that starts at -1, of a bad page
+ * (QPKV_DEV_ERR_BAD_PAGE), past the table row or with lengths that do not fit
+ * (QPKV_DEV_ERR_BAD_LENGTH), and behind the last sequence are left as they are.
+ * Errors: as qpkv_write_group4. */
+typedef struct qpkv_read_group4_params {
+  int32_t num_seqs;
+  int32_t num_tokens;
+  int32_t num_heads_kv;
+  int32_t head_dim;
+  int32_t page_size;
+  int32_t num_pages;
+  int32_t bt_stride;
+  int32_t dtype;
+  const int32_t* cu_seqlens_q;
+  const int32_t* start_pos;
+  const int32_t* block_table;
+  const void* k_pool;
+  const void* v_pool;
+  const float* k_mul;
+  const float* v_mul;
+  void* k_out;
+  void* v_out;
+  int32_t* error_word;
+} qpkv_read_group4_params;
+
+qpkv_status qpkv_read_group4(const qpkv_read_group4_params* params, void* stream);
+
+/* The pages that each query token attends to.  Query i of sequence b (n rows,
+ * L cached tokens, the new ones among them) has position at = L - n + i; its
+ * candidates are the pages of the keys at - window < j <= at (window 0: from
+ * the first).  For each kv head, with a = max |q| over the G = Hq / Hkv query
+ * heads that share it and c = RNE(q * 127 / a) (0 where a is 0 or not finite),
+ *   score(page) = bound_scale[page] * max over the G heads of
+ *                 sum_d max(c_d * min_d, c_d * max_d)
+ * (whole numbers below 2^24, one float32 product; +inf where the scale is inf):
+ * a bound, in units of its own, on what any key of the page can score.  The
+ * `first` first and the `last` last candidates are taken, then the highest
+ * scores, of equal ones the lower page.
+ *   q             [T, Hq, D] of dtype, contiguous
+ *   selected      int32 [T, Hkv, num_selected]: places in the sequence's row of
+ *                 block_table (page p holds keys [p * page_size, ...)), ascending,
+ *                 -1 behind the last; all -1 for a row without keys; rows behind
+ *                 the last sequence are left as they are
+ *   max_seqlen_q  a bound on any n (<= 0: unknown); picks the kernel only
+ * A page id outside [0, num_pages) is no candidate (QPKV_DEV_ERR_BAD_PAGE); a
+ * sequence whose rows or length do not fit has none (QPKV_DEV_ERR_BAD_LENGTH).
+ * Errors: INVALID_ARG (null or misaligned pointers, negative sizes, first < 0,
+ * last < 1, first + last > num_selected), UNSUPPORTED (D, page_size, Hq % Hkv,
+ * Hq / Hkv above 128, dtype, bt_stride above 2^18, bt_stride * page_size above
+ * 2^31 - 65, T * Hkv * num_selected or T * Hq above 2^31), CUDA. */
+typedef struct qpkv_select_pages_params {
+  int32_t num_seqs;
+  int32_t num_tokens;
+  int32_t max_seqlen_q;
+  int32_t num_heads_q;
+  int32_t num_heads_kv;
+  int32_t head_dim;
+  int32_t page_size;
+  int32_t num_pages;
+  int32_t bt_stride;
+  int32_t dtype;
+  int32_t num_selected;
+  int32_t first;
+  int32_t last;
+  int32_t window;
+  const int32_t* cu_seqlens_q;
+  const int32_t* seqlens_kv;
+  const int32_t* block_table;
+  const void* q;
+  const void* k_bounds;
+  const float* bound_scale;
+  int32_t* selected;
+  int32_t* error_word;
+} qpkv_select_pages_params;
+
+qpkv_status qpkv_select_pages(const qpkv_select_pages_params* params, void* stream);
+
+/* Attention of varlen queries over the cache in 4 bits: the formulas, masks,
+ * empty rows, cu_seqlens_q, seqlens_kv, prefix_lens, alibi_slopes, logit_cap,
+ * window, max_seqlen_q, workspace and errors of qpkv_attend_page8, K and V as
+ * qpkv_write_group4 stored them.  With `selected` (int32 [T, Hkv,
+ * num_selected], from qpkv_select_pages or elsewhere) a row sees only keys of
+ * the pages listed for its token and kv head; -1 lists none, a place that holds
+ * no key of the sequence is skipped (QPKV_DEV_ERR_BAD_INDEX), a page listed
+ * twice counts twice.  A NaN scale makes NaN what sees its token: a K scale the
+ * whole row, a V scale the 16 channels; rows that do not see the token are not
+ * touched by it. */
+typedef struct qpkv_attend_group4_params {
+  int32_t num_seqs;
+  int32_t num_tokens;
+  int32_t max_seqlen_q;
+  int32_t num_heads_q;
+  int32_t num_heads_kv;
+  int32_t head_dim;
+  int32_t page_size;
+  int32_t num_pages;
+  int32_t bt_stride;
+  int32_t dtype;
+  int32_t causal;
+  int32_t window;
+  int32_t num_selected;  /* ignored without selected */
+  float sm_scale;
+  float logit_cap;
+  int32_t pad0;
+  const int32_t* cu_seqlens_q;
+  const int32_t* seqlens_kv;
+  const int32_t* block_table;
+  const int32_t* prefix_lens;
+  const int32_t* selected;
+  const float* alibi_slopes;
+  const void* q;
+  const void* k_pool;
+  const void* v_pool;
+  const float* k_mul;
+  const float* v_mul;
+  void* o;
+  float* lse;
+  void* workspace;
+  size_t workspace_bytes;
+  int32_t* error_word;
+} qpkv_attend_group4_params;
+
+/* Device workspace bytes of qpkv_attend_group4, with or without selected pages
+ * (0 for arguments it refuses). */
+size_t qpkv_attend_group4_workspace_bytes(int32_t num_seqs, int32_t num_tokens, int32_t num_heads_q,
+                                          int32_t num_heads_kv, int32_t head_dim);
+
+qpkv_status qpkv_attend_group4(const qpkv_attend_group4_params* params, void* stream);
 
 #ifdef __cplusplus
 }

@@ -19,6 +19,8 @@ __all__ = [
     "write_cache_mla", "DecodePlan", "PAGE_ROW_MLA",
     "assign_pages", "axis_sections", "rope_axes", "write_cache_page8", "attend_page8",
     "attend_page8_workspace",
+    "write_cache_group4", "read_cache_group4", "select_pages", "attend_group4",
+    "attend_group4_workspace",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -148,6 +150,54 @@ class AttendPage8Params(ctypes.Structure):
         ("workspace_bytes", ctypes.c_size_t), ("error_word", _p)]
 
 
+class WriteGroup4Params(ctypes.Structure):
+    """Mirror of ``qpkv_write_group4_params`` (include/qpkv.h)."""
+    _fields_ = [(n, _i32) for n in (
+        "num_seqs", "num_tokens", "num_heads_q", "num_heads_kv", "head_dim", "page_size",
+        "num_pages", "bt_stride", "dtype", "rot_dim", "rope_max_pos", "pad0")] + [
+        (n, ctypes.c_int64) for n in (
+            "k_stride_t", "k_stride_h", "v_stride_t", "v_stride_h", "q_stride_t", "q_stride_h",
+            "q_out_stride_t", "q_out_stride_h")] + [
+        (n, _p) for n in (
+            "cu_seqlens_q", "start_pos", "block_table", "k", "v", "q", "q_out", "rope_cos",
+            "rope_sin", "k_mul", "v_mul", "k_pool", "v_pool", "k_bounds", "bound_scale",
+            "error_word")]
+
+
+class ReadGroup4Params(ctypes.Structure):
+    """Mirror of ``qpkv_read_group4_params`` (include/qpkv.h)."""
+    _fields_ = [(n, _i32) for n in (
+        "num_seqs", "num_tokens", "num_heads_kv", "head_dim", "page_size", "num_pages",
+        "bt_stride", "dtype")] + [
+        (n, _p) for n in (
+            "cu_seqlens_q", "start_pos", "block_table", "k_pool", "v_pool", "k_mul", "v_mul",
+            "k_out", "v_out", "error_word")]
+
+
+class SelectPagesParams(ctypes.Structure):
+    """Mirror of ``qpkv_select_pages_params`` (include/qpkv.h)."""
+    _fields_ = [(n, _i32) for n in (
+        "num_seqs", "num_tokens", "max_seqlen_q", "num_heads_q", "num_heads_kv", "head_dim",
+        "page_size", "num_pages", "bt_stride", "dtype", "num_selected", "first", "last",
+        "window")] + [
+        (n, _p) for n in (
+            "cu_seqlens_q", "seqlens_kv", "block_table", "q", "k_bounds", "bound_scale",
+            "selected", "error_word")]
+
+
+class AttendGroup4Params(ctypes.Structure):
+    """Mirror of ``qpkv_attend_group4_params`` (include/qpkv.h)."""
+    _fields_ = [(n, _i32) for n in (
+        "num_seqs", "num_tokens", "max_seqlen_q", "num_heads_q", "num_heads_kv", "head_dim",
+        "page_size", "num_pages", "bt_stride", "dtype", "causal", "window", "num_selected")] + [
+        ("sm_scale", ctypes.c_float), ("logit_cap", ctypes.c_float), ("pad0", _i32)] + [
+        (n, _p) for n in (
+            "cu_seqlens_q", "seqlens_kv", "block_table", "prefix_lens", "selected",
+            "alibi_slopes", "q", "k_pool", "v_pool", "k_mul", "v_mul", "o", "lse",
+            "workspace")] + [
+        ("workspace_bytes", ctypes.c_size_t), ("error_word", _p)]
+
+
 def _declare(lib):
     S = ctypes.c_size_t
     P64 = ctypes.POINTER(ctypes.c_int64)
@@ -183,6 +233,11 @@ def _declare(lib):
         "qpkv_write_page8": (_i32, [ctypes.POINTER(WritePage8Params), _p]),
         "qpkv_attend_page8_workspace_bytes": (S, [_i32, _i32, _i32, _i32, _i32]),
         "qpkv_attend_page8": (_i32, [ctypes.POINTER(AttendPage8Params), _p]),
+        "qpkv_write_group4": (_i32, [ctypes.POINTER(WriteGroup4Params), _p]),
+        "qpkv_read_group4": (_i32, [ctypes.POINTER(ReadGroup4Params), _p]),
+        "qpkv_select_pages": (_i32, [ctypes.POINTER(SelectPagesParams), _p]),
+        "qpkv_attend_group4_workspace_bytes": (S, [_i32, _i32, _i32, _i32, _i32]),
+        "qpkv_attend_group4": (_i32, [ctypes.POINTER(AttendGroup4Params), _p]),
         "qpkv_error_status": (_i32, [_i32]),
         "qpkv_error_check": (_i32, [_p, ctypes.POINTER(_i32)]),
         "qpkv_selftest_wait_timeout": (_i32, [ctypes.c_int64, _p, _p]),
@@ -1098,4 +1153,218 @@ def attend_page8(q, k_pool, v_pool, k_scale, v_scale, block_table, cu_seqlens_q,
         None if lse is None else _arr(lse, "lse", f32, (T, Hq), dev),
         workspace.data_ptr(), n, _error_ptr(error_word, dev))
     _check(lib.qpkv_attend_page8(ctypes.byref(p), stream), "qpkv_attend_page8")
+    return out
+
+
+# ------------------------------------------------------------- a cache in 4 bits
+
+def _pools4(k_pool, v_pool, block_table, B, D, dev):
+    """Check a 4-bit cache's arguments: ((H, D, page size, pages, table
+    stride), pointers of the table and pools).  D: head_dim, or None to take
+    it from the pools."""
+    torch = _torch()
+    u8, shape = torch.uint8, k_pool.shape
+    if len(shape) != 4:
+        raise ValueError("pools must be [P, Hkv, page_size / 16, 9 * D]")
+    P, H, blocks, width = shape
+    if D is None:
+        D = width // 9
+    if width != 9 * D:
+        raise ValueError(f"pools must be [P, Hkv, page_size / 16, {9 * D}], got {list(shape)}")
+    W = block_table.shape[1]
+    return ((H, D, 16 * blocks, P, W),
+            (_arr(block_table, "block_table", torch.int32, (B, W), dev),
+             _arr(k_pool, "k_pool", u8, shape, dev), _arr(v_pool, "v_pool", u8, shape, dev)))
+
+
+def _mul(t, name, H, dev):
+    return None if t is None else _arr(t, name, _torch().float32, (H,), dev)
+
+
+def write_cache_group4(k, v, cu_seqlens, block_table, k_pool, v_pool, start_pos=None,
+                       rope_cos=None, rope_sin=None, q=None, q_out=None, k_bounds=None,
+                       bound_scale=None, k_mul=None, v_mul=None, error_word=None):
+    """Append k, v [T, Hkv, D] (bf16 or f16; slices of a fused projection are
+    fine) to a cache in 4 bits: E2M1 codes with an E4M3 scale for 16 channels,
+    pools uint8 [P, Hkv, page_size / 16, 9 * D] (include/qpkv.h has the
+    layout).  With rope_cos / rope_sin (float32 [max_pos, R/2],
+    ``rope_table(theta, max_pos, R)``, R a multiple of 32 up to D) the first R
+    elements of k are rotated at each token's position on the way, and those
+    of q [T, Hq, D], which goes to q_out (new and contiguous, or given, then
+    maybe q itself), returned.  k_bounds (int8 [P, Hkv, 2, D]) and bound_scale
+    (float32 [P, Hkv]) receive the key bounds of the pages written, for
+    ``select_pages``.  k_mul, v_mul float32 [Hkv]: factors the cache is kept
+    without; give them to every call over this cache.  start_pos int32 [B]:
+    tokens cached before (None: 0); -1, as ``assign_pages`` gives it for a
+    refused request: nothing of that sequence is written."""
+    torch = _torch()
+    lib = load()
+    i32, f32 = torch.int32, torch.float32
+    dev, stream = _device_and_stream()
+    (T, H, D), dtype = k.shape, k.dtype
+    B = cu_seqlens.shape[0]
+    (Hp, D, ps, P, W), (bt, kpool, vpool) = _pools4(k_pool, v_pool, block_table, B, D, dev)
+    kp, k_t, k_h = _heads(k, "k", dtype, (T, Hp, D), dev)
+    vp, v_t, v_h = _heads(v, "v", dtype, (T, Hp, D), dev)
+    if (rope_cos is None) != (rope_sin is None):
+        raise ValueError("rope_cos and rope_sin go together")
+    if (k_bounds is None) != (bound_scale is None):
+        raise ValueError("k_bounds and bound_scale go together")
+    cos = sin = qp = qo = None
+    rows = half = Hq = q_t = q_h = qo_t = qo_h = 0
+    if rope_cos is not None:
+        rows, half = rope_cos.shape
+        cos = _arr(rope_cos, "rope_cos", f32, (rows, half), dev)
+        sin = _arr(rope_sin, "rope_sin", f32, (rows, half), dev)
+    if q is not None:
+        if rope_cos is None:
+            raise ValueError("rotating q needs the RoPE tables")
+        Hq = q.shape[1]
+        qp, q_t, q_h = _heads(q, "q", dtype, (T, Hq, D), dev)
+        if q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=dtype, device=q.device)
+        qo, qo_t, qo_h = _heads(q_out, "q_out", dtype, (T, Hq, D), dev)
+    p = WriteGroup4Params(
+        B, T, Hq, H, D, ps, P, W, _dtype_code(dtype), 2 * half, rows, 0, k_t, k_h, v_t, v_h,
+        q_t, q_h, qo_t, qo_h, _arr(cu_seqlens, "cu_seqlens", i32, (B,), dev),
+        None if start_pos is None else _arr(start_pos, "start_pos", i32, (B,), dev),
+        bt, kp, vp, qp, qo, cos, sin, _mul(k_mul, "k_mul", H, dev), _mul(v_mul, "v_mul", H, dev),
+        kpool, vpool,
+        None if k_bounds is None else _arr(k_bounds, "k_bounds", torch.int8, (P, H, 2, D), dev),
+        None if bound_scale is None else _arr(bound_scale, "bound_scale", f32, (P, H), dev),
+        _error_ptr(error_word, dev))
+    _check(lib.qpkv_write_group4(ctypes.byref(p), stream), "qpkv_write_group4")
+    return q_out
+
+
+def read_cache_group4(k_pool, v_pool, cu_seqlens, block_table, num_tokens, start_pos=None,
+                      k_mul=None, v_mul=None, dtype=None, k_out=None, v_out=None,
+                      error_word=None):
+    """Tokens of a 4-bit cache back: (k, v) [num_tokens, Hkv, D] of dtype
+    (bf16 or f16; None: that of k_out, else bf16), new tensors or k_out and
+    v_out.  Row t of sequence b (cu_seqlens: inclusive prefix sums of the
+    counts) is its token at position start_pos[b] + (t - the rows before;
+    None: 0).  Rows of a sequence that starts at -1, and behind the last
+    sequence, are not written."""
+    torch = _torch()
+    lib = load()
+    i32 = torch.int32
+    dev, stream = _device_and_stream()
+    B, T = cu_seqlens.shape[0], num_tokens
+    (H, D, ps, P, W), (bt, kpool, vpool) = _pools4(k_pool, v_pool, block_table, B, None, dev)
+    if dtype is None:
+        dtype = torch.bfloat16 if k_out is None else k_out.dtype
+    if k_out is None:
+        k_out = torch.empty((T, H, D), dtype=dtype, device=k_pool.device)
+    if v_out is None:
+        v_out = torch.empty((T, H, D), dtype=dtype, device=k_pool.device)
+    p = ReadGroup4Params(
+        B, T, H, D, ps, P, W, _dtype_code(dtype),
+        _arr(cu_seqlens, "cu_seqlens", i32, (B,), dev),
+        None if start_pos is None else _arr(start_pos, "start_pos", i32, (B,), dev),
+        bt, kpool, vpool, _mul(k_mul, "k_mul", H, dev), _mul(v_mul, "v_mul", H, dev),
+        _arr(k_out, "k_out", dtype, (T, H, D), dev), _arr(v_out, "v_out", dtype, (T, H, D), dev),
+        _error_ptr(error_word, dev))
+    _check(lib.qpkv_read_group4(ctypes.byref(p), stream), "qpkv_read_group4")
+    return k_out, v_out
+
+
+def select_pages(q, k_bounds, bound_scale, block_table, cu_seqlens_q, seqlens_kv, page_size,
+                 num_selected, first=0, last=1, window=0, max_seqlen_q=0, out=None,
+                 error_word=None):
+    """The pages that each query token attends to: int32 [T, Hkv,
+    num_selected], places in the sequence's row of block_table, ascending, -1
+    behind the last (also the form of ``mla_sparse_decode``'s block lists).
+    q [T, Hq, D] (bf16 or f16); k_bounds int8 [P, Hkv, 2, D] and bound_scale
+    float32 [P, Hkv] as ``write_cache_group4`` keeps them; cu_seqlens_q,
+    seqlens_kv as for ``attend_group4``.  Candidates are the pages up to the
+    token's own (of the last ``window`` keys only, with a window); the
+    ``first`` first and ``last`` last of them are always taken, then those
+    with the highest bound on what a query of the kv head's group can score in
+    them, ties to the lower page.  max_seqlen_q: a bound on the queries of a
+    sequence (0: T); it picks the kernel only."""
+    torch = _torch()
+    lib = load()
+    i32 = torch.int32
+    dev, stream = _device_and_stream()
+    T, Hq, D = shape = q.shape
+    B = cu_seqlens_q.shape[0]
+    P, H = bound_scale.shape
+    W = block_table.shape[1]
+    if H < 1 or Hq % H != 0:
+        raise ValueError(f"{Hq} query heads over {H} kv heads")
+    if out is None:
+        out = torch.empty((T, H, num_selected), dtype=i32, device=q.device)
+    p = SelectPagesParams(
+        B, T, max_seqlen_q, Hq, H, D, page_size, P, W, _dtype_code(q.dtype), num_selected, first,
+        last, window, _arr(cu_seqlens_q, "cu_seqlens_q", i32, (B,), dev),
+        _arr(seqlens_kv, "seqlens_kv", i32, (B,), dev),
+        _arr(block_table, "block_table", i32, (B, W), dev), _arr(q, "q", q.dtype, shape, dev),
+        _arr(k_bounds, "k_bounds", torch.int8, (P, H, 2, D), dev),
+        _arr(bound_scale, "bound_scale", torch.float32, (P, H), dev),
+        _arr(out, "out", i32, (T, H, num_selected), dev), _error_ptr(error_word, dev))
+    _check(lib.qpkv_select_pages(ctypes.byref(p), stream), "qpkv_select_pages")
+    return out
+
+
+def attend_group4_workspace(num_seqs, num_tokens, num_heads_q, num_heads_kv, head_dim,
+                            device="cuda"):
+    """A device workspace large enough for ``attend_group4``."""
+    torch = _torch()
+    n = int(load().qpkv_attend_group4_workspace_bytes(int(num_seqs), int(num_tokens),
+                                                      int(num_heads_q), int(num_heads_kv),
+                                                      int(head_dim)))
+    return torch.empty(((n + 15) // 16) * 16, dtype=torch.uint8, device=device)
+
+
+def attend_group4(q, k_pool, v_pool, block_table, cu_seqlens_q, seqlens_kv, max_seqlen_q=0,
+                  sm_scale=None, causal=True, logit_cap=0.0, window=0, alibi_slopes=None,
+                  prefix_lens=None, selected=None, k_mul=None, v_mul=None, out=None, lse=None,
+                  workspace=None, error_word=None):
+    """Attention of varlen queries (bf16 or f16 [T, Hq, D]) over the cache
+    ``write_cache_group4`` writes, from single tokens to whole prompts; returns
+    o [T, Hq, D] (``lse`` float32 [T, Hq] filled when given).  Arguments as
+    ``attend_page8``, and: k_mul, v_mul float32 [Hkv], those the cache was
+    written with; selected int32 [T, Hkv, n]: each row sees only keys of the
+    pages listed for its token and kv head (``select_pages``; -1 lists none, a
+    page listed twice counts twice)."""
+    torch = _torch()
+    lib = load()
+    i32, f32 = torch.int32, torch.float32
+    dev, stream = _device_and_stream()
+    T, Hq, D = shape = q.shape
+    B, dtype = cu_seqlens_q.shape[0], q.dtype
+    (H, D, ps, P, W), (bt, kpool, vpool) = _pools4(k_pool, v_pool, block_table, B, D, dev)
+    qp = _arr(q, "q", dtype, shape, dev)
+    n_sel = 0
+    if selected is not None:
+        n_sel = selected.shape[-1]
+        if n_sel < 1:
+            raise ValueError("selected must list one page at least")
+    if out is None:
+        out = torch.empty_like(q)
+        op = out.data_ptr()
+    else:
+        op = _arr(out, "out", dtype, shape, dev)
+    if workspace is None:
+        n = lib.qpkv_attend_group4_workspace_bytes(B, T, Hq, H, D)
+        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+    else:
+        if workspace.get_device() != dev:
+            raise ValueError("workspace must live on the current device")
+        if not workspace.is_contiguous():   # its bytes would not be those it is said to have
+            raise ValueError("workspace must be contiguous")
+        n = workspace.numel() * workspace.element_size()
+    p = AttendGroup4Params(
+        B, T, max_seqlen_q, Hq, H, D, ps, P, W, _dtype_code(dtype), 1 if causal else 0, window,
+        n_sel, sm_scale if sm_scale else 0.0, logit_cap, 0,
+        _arr(cu_seqlens_q, "cu_seqlens_q", i32, (B,), dev),
+        _arr(seqlens_kv, "seqlens_kv", i32, (B,), dev), bt,
+        None if prefix_lens is None else _arr(prefix_lens, "prefix_lens", i32, (B,), dev),
+        None if selected is None else _arr(selected, "selected", i32, (T, H, n_sel), dev),
+        None if alibi_slopes is None else _arr(alibi_slopes, "alibi_slopes", f32, (Hq,), dev),
+        qp, kpool, vpool, _mul(k_mul, "k_mul", H, dev), _mul(v_mul, "v_mul", H, dev), op,
+        None if lse is None else _arr(lse, "lse", f32, (T, Hq), dev),
+        workspace.data_ptr(), n, _error_ptr(error_word, dev))
+    _check(lib.qpkv_attend_group4(ctypes.byref(p), stream), "qpkv_attend_group4")
     return out

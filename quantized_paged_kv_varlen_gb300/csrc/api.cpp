@@ -208,6 +208,10 @@ size_t qpkv_struct_size(int32_t which) {
     case 4: return sizeof(qpkv_rope_axes_params);
     case 5: return sizeof(qpkv_write_page8_params);
     case 6: return sizeof(qpkv_attend_page8_params);
+    case 7: return sizeof(qpkv_write_group4_params);
+    case 8: return sizeof(qpkv_read_group4_params);
+    case 9: return sizeof(qpkv_select_pages_params);
+    case 10: return sizeof(qpkv_attend_group4_params);
     default: return 0;
   }
 }

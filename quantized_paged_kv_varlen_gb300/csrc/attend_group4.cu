@@ -1,0 +1,741 @@
+// Attention over the paged cache in 4 bits (group4.cuh has the layout): the
+// split form for few query rows, and for rows that attend to selected pages.
+//
+//   x(r, j) = sm_scale * k_mul * q_r . K_j     K, V: codes times scales
+//   x = cap * tanh(x / cap)        with a cap
+//   x = x + slope_h * (j - at_r)   with a bias, at_r the position of row r
+//   o_r = v_mul * sum_j softmax_j(x(r, .)) V_j,  j in [lo_r, hi_r)
+//
+// Every row's visible keys are one interval (page8.cuh), or with selected pages
+// the part of it that lies in them.
+//
+// The work is cut as in attend_page8.cu: units of 16 tokens in equal runs, one
+// per warp, warps on their own, pieces joined afterwards.  A unit is two untiled
+// bulk copies (K and V, 9 D bytes each, codes and scales together), issued by
+// two lanes into a ring of the warp's own.  With selected pages every (token,
+// kv head, row tile) is a task of as many units as the list has room for; units
+// that list nothing are passed over.
+//
+// Tokens are the rows of m16n8k16, query rows its 8 columns.  A code times its
+// scale is exact in f16, so fragments are one conversion and one packed product
+// per two values:
+//   S^T = K Q^T      a thread holds a quarter of tokens p(g) and p(g) + 8, whose
+//                    dims are the k index in an order Q follows
+//   O^T += V^T P^T   thread (g, t) holds chunk g of the four tokens p(2t), p(2t +
+//                    1) and those + 8; codes of two tokens are interleaved nibble
+//                    by nibble, so that one conversion gives a dim of both
+// (g = lane / 4, t = lane % 4, p(2t + e) = 2t + (e xor t % 2): neighbouring rows of
+// 64 bytes alternate for both reads, so that banks differ.)
+//
+// A NaN scale of V must reach only the rows that see its token, and P = 0 does
+// not cancel it: where some row of a tile does not see some key of a unit, such
+// scales count as zero and the rows that see the token get their NaN afterwards.
+#include <climits>
+#include <type_traits>
+
+#include "attend_split.cuh"
+#include "common.cuh"
+#include "group4.cuh"
+#include "internal.h"
+#include "page8.cuh"
+
+namespace qpkv {
+namespace {
+
+struct SplitArgs {
+  Page8Args p;
+  int workers;             // warps / side
+  int side;                // kv heads that neighbouring warps take over the same tokens
+  int tile;                // query rows of a tile (8 NB), and of a piece in the workspace
+  float* part_o;           // [2 * workers][tile][D]
+  float2* part_ml;         // [2 * workers][tile] (m, l)
+  TokenInfo* info;         // [T]
+  const int32_t* sel;      // [T, Hkv, n_sel] or null: all keys
+  int n_sel;
+};
+
+// Units of sequence b: groups [g0, g0 + ng) for each of nt row tiles and Hkv heads.
+struct Span {
+  int t0, n, len, g0, ng, nt;
+};
+
+__device__ __forceinline__ Span span_of(const Page8Args& a, int tile, int b, int* err) {
+  Span s = {0, 0, 0, 0, 0, 0};
+  Rows r = rows_of(a, b, err);
+  s.t0 = r.t0;
+  s.n = r.n;
+  s.len = r.len;
+  if (r.n <= 0 || r.n * a.G > a.split_rows) return s;   // none, or in tiles of 128
+  const int hi = row_hi(a, r, r.n - 1), lo = row_lo(a, r, 0);
+  if (hi > lo) {
+    s.g0 = lo / kGroup;
+    s.ng = (hi + kGroup - 1) / kGroup - s.g0;
+    s.nt = (r.n * a.G + tile - 1) / tile;
+  }
+  return s;
+}
+
+// Blocks per SM and ring stages: more query rows take registers from warps,
+// and the ring gets what shared memory the warps leave.
+template <int D, int NB>
+struct Shape {
+  static constexpr int kBlocks = NB == 1 ? 4 : NB == 2 ? 3 : 2;
+  static constexpr int kStages = 4;
+  static constexpr int kBlock = Group4<D>::kBlock;
+  static constexpr int kStage = 2 * kBlock;          // K and V of a group
+  // three tiles keep the query fragments, each lane's own, in shared memory
+  static constexpr bool kQShared = NB == 3;
+  static constexpr int kQBytes = kQShared ? NB * (D / 16) * 32 * 8 : 0;
+  static constexpr int kWarpBytes = kStages * kStage;
+  static constexpr int kBytes = kWarps * (kWarpBytes + kQBytes) + 1024;
+};
+
+template <typename E, int D, bool kCap, bool kBias, int NB>
+__global__ void __launch_bounds__(kWarps * 32, (Shape<D, NB>::kBlocks))
+    attend_split4_kernel(const __grid_constant__ SplitArgs sa) {
+  using L = Group4<D>;
+  using Sh = Shape<D, NB>;
+  constexpr int kStages = Sh::kStages;
+  constexpr int KS = D / 16;      // k steps of K Q^T
+  constexpr int NT = D / 16;      // 16-dim tiles of O: rows g, g + 8 are dims 2i, 2i + 1 of chunk g
+  constexpr int KW = D / 32;      // words of a K token a thread takes
+  constexpr int VB = D / 8;       // dims of a V token a thread takes
+  constexpr int VW = VB / 8;      // words of them
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  __shared__ uint64_t s_full[kWarps][kStages];
+  __shared__ long long s_prefix[kWarps * 32 + 1];
+  __shared__ long long w_sum[kWarps];
+  __shared__ RowInfo s_rows[kWarps][8 * NB];
+  const Page8Args& a = sa.p;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, t = lane & 3;
+  if (lane == 0) {
+    for (int s = 0; s < kStages; ++s) mbar_init(&s_full[warp][s], 1);
+    fence_mbar_init();
+  }
+  // No early launch of the dependents: join blocks that wait on an SM keep
+  // blocks of this kernel's next launch off it.
+  griddep_wait();
+
+  const int hgroups = a.Hkv / sa.side;
+  const int per = (a.B + kWarps * 32 - 1) / (kWarps * 32);
+  const bool listed = sa.sel != nullptr;
+  const int gpp = a.ps / kGroup;
+  // with a list: row tiles of a token, units of a task
+  const int list_nt = (a.G + 8 * NB - 1) / (8 * NB), list_ng = listed ? sa.n_sel * gpp : 0;
+  long long total;
+  if (listed) {
+    total = static_cast<long long>(a.T) * hgroups * list_nt * list_ng;
+  } else {
+    // ---- units before each block of `per` sequences
+    const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b) {
+      const Span s = span_of(a, 8 * NB, b, blockIdx.x == 0 ? a.err : nullptr);
+      mine += static_cast<long long>(s.ng) * s.nt * hgroups;
+    }
+    long long inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long u = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += u;
+    }
+    if (lane == 31) w_sum[warp] = inc;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) inc += w_sum[w];
+    s_prefix[tid + 1] = inc;
+    if (tid == 0) s_prefix[0] = 0;
+    __syncthreads();
+    total = s_prefix[kWarps * 32];
+  }
+  long long run = (total + sa.workers - 1) / sa.workers;
+  run = run < kMinRun ? kMinRun : run;
+  for (int tok = blockIdx.x + gridDim.x * tid; tok < a.T; tok += gridDim.x * kWarps * 32) {
+    const int b = seq_of_token(a.cu, a.B, tok);
+    TokenInfo x;
+    x.run = run;
+    x.kind = 0;
+    if (listed) {
+      const Rows r = rows_of(a, b, a.err);
+      x.ng = r.n > 0 && tok >= r.t0 && tok < r.t0 + r.n ? list_ng : -1;
+      x.u0 = static_cast<long long>(tok) * hgroups * list_nt * list_ng;
+      x.stride = list_ng;
+      x.nt = list_nt;
+      x.r0 = 0;
+    } else {
+      const Span s = span_of(a, 8 * NB, b, nullptr);
+      if (s.n * a.G > a.split_rows) continue;   // the tiled form's
+      x.u0 = s_prefix[b / per];
+      for (int c = b / per * per; c < b; ++c) {
+        const Span y = span_of(a, 8 * NB, c, nullptr);
+        x.u0 += static_cast<long long>(y.ng) * y.nt * hgroups;
+      }
+      x.ng = s.n > 0 && tok >= s.t0 && tok < s.t0 + s.n ? s.ng : -1;
+      x.stride = s.ng;
+      x.nt = s.nt;
+      x.r0 = (tok - s.t0) * a.G;
+    }
+    sa.info[tok] = x;
+  }
+  const int me = blockIdx.x * kWarps + warp;
+  const int worker = me / sa.side;
+  long long u = worker * run;
+  const long long u_end = u + run < total ? u + run : total;
+  const long long u_begin = u;
+  if (u >= u_end) return;
+
+  uint8_t* ring = smem + warp * Sh::kWarpBytes;
+  uint64_t* full = s_full[warp];
+  uint2* sq = reinterpret_cast<uint2*>(smem + kWarps * Sh::kWarpBytes + warp * Sh::kQBytes) + lane;
+  RowInfo* ri = s_rows[warp];
+  int in_st = 0, out_st = 0;     // ring stages of the next copy and the next use
+  uint32_t out_phase = 0;        // phase of the stage in use
+  // a thread's pieces of a block
+  const int pg = 2 * (g >> 1) + ((g ^ (g >> 1)) & 1);                 // p(g)
+  const int p0 = 2 * t + (t & 1), p1 = 2 * t + 1 - (t & 1);           // p(2t), p(2t + 1)
+  const int ka = pg * L::kRow + t * (KW * 4);
+  const int ksa = L::kScaleAt + pg * L::kScales + t * (D / 64);
+  const int vsa = L::kScaleAt + (D == 128 ? g : g >> 1);
+  // the sequence of unit u
+  int b = 0;
+  long long before = 0;
+  Span sp = {0, 0, 0, 0, 0, 0};
+  if (!listed) {
+    int lo = 0, hi = kWarps * 32 - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (u < s_prefix[mid + 1]) hi = mid; else lo = mid + 1;
+    }
+    b = lo * per;
+    before = s_prefix[lo];
+    sp = span_of(a, 8 * NB, b, nullptr);
+  }
+
+  while (u < u_end) {
+    int task, first, ng, token_i = 0;     // token_i: the query of a listed task
+    if (listed) {
+      const long long in_t = static_cast<long long>(hgroups) * list_nt * list_ng;
+      const int tok = static_cast<int>(u / in_t);
+      const long long local = u - tok * in_t;
+      ng = list_ng;
+      task = static_cast<int>(local / ng);
+      first = static_cast<int>(local - static_cast<long long>(task) * ng);
+      b = warp_last_at_most(a.B, tok, [&](int m) { return static_cast<long long>(__ldg(a.cu + m - 1)); });
+      const Rows r = rows_of(a, b, nullptr);
+      sp.t0 = r.t0, sp.n = r.n, sp.len = r.len, sp.nt = list_nt;
+      token_i = tok - r.t0;
+      if (token_i < 0 || token_i >= r.n) {      // behind the last sequence: its rows stay as they are
+        u += min(in_t - local, u_end - u);
+        continue;
+      }
+    } else {
+      long long in_b = static_cast<long long>(sp.ng) * sp.nt * hgroups;
+      while (u >= before + in_b) {   // a run may cross into later sequences
+        before += in_b;
+        ++b;
+        sp = span_of(a, 8 * NB, b, nullptr);
+        in_b = static_cast<long long>(sp.ng) * sp.nt * hgroups;
+      }
+      const long long local = u - before;
+      ng = sp.ng;
+      task = static_cast<int>(local / ng);
+      first = static_cast<int>(local - static_cast<long long>(task) * ng);
+    }
+    const int hg = task / sp.nt, rt = task - hg * sp.nt, h = hg * sa.side + me % sa.side;
+    const int count = static_cast<int>(min(static_cast<long long>(ng - first), u_end - u));
+    const bool whole_task = count == ng;
+    const size_t piece = 2 * static_cast<size_t>(me) + (u == u_begin ? 0 : 1);
+    // from the newest group back: with a distance bias the scores then fall, and
+    // the running maximum is set once instead of moving with every group
+    const int glast = (listed ? 0 : sp.g0) + first + count - 1;
+    const int live_rows = min(8 * NB, (listed ? a.G : sp.n * a.G) - rt * 8 * NB);
+
+    // ---- the ring.  Lane l looks up group 32 k + l of the run: its block in the
+    // pools and its first key, 32 groups at a time.
+    const int32_t* bt = a.bt + static_cast<size_t>(b) * a.bt_stride;
+    const int32_t* list = listed ? sa.sel + (static_cast<size_t>(sp.t0 + token_i) * a.Hkv + h) * sa.n_sel : nullptr;
+    int list_lo = 0, list_hi = 0;      // keys that the listed token sees
+    if (listed) {
+      Rows rows;
+      rows.t0 = sp.t0, rows.n = sp.n, rows.len = sp.len;
+      rows.prefix = a.prefix != nullptr ? __ldg(a.prefix + b) : 0;
+      list_lo = row_lo(a, rows, token_i);
+      list_hi = row_hi(a, rows, token_i);
+    }
+    int at = -1, next_j0 = -1;         // block of the group (-1: no keys), its first key
+    auto lookup = [&](int i0) {
+      const int i = i0 + lane;
+      at = -1;
+      if (i < count) {
+        const int gi = glast - i, slot = gi / gpp, in = gi - slot * gpp;
+        int no = slot;                 // the page's place in the table row
+        if (listed) {
+          no = __ldg(list + slot);
+          if (no < 0 || no >= a.bt_stride || static_cast<long long>(no) * a.ps >= sp.len) {
+            if (no != -1) report_error(a.err, kDevErrBadIndex);
+            return;
+          }
+        }
+        next_j0 = no * a.ps + in * kGroup;
+        if (listed && (next_j0 >= list_hi || next_j0 + kGroup <= list_lo)) return;
+        const int page = __ldg(bt + no);
+        if (page >= 0 && page < a.num_pages) {
+          at = (page * a.Hkv + h) * gpp + in;
+        } else {
+          report_error(a.err, kDevErrBadPage);
+        }
+      }
+    };
+    auto issue = [&](int i) {
+      if (i < count) {
+        if ((i & 31) == 0) lookup(i);
+        __syncwarp();
+        const int block = __shfl_sync(0xffffffffu, at, i & 31);
+        if (block >= 0) {
+          if (lane == 0) mbar_arrive_expect_tx(&full[in_st], Sh::kStage);
+          __syncwarp();
+          if (lane < 2)
+            bulk_load(ring + in_st * Sh::kStage + lane * Sh::kBlock,
+                      (lane == 0 ? a.k : a.v) + static_cast<size_t>(block) * Sh::kBlock, Sh::kBlock, &full[in_st]);
+          __syncwarp();
+        } else if (lane == 0) {
+          mbar_arrive(&full[in_st]);   // nothing comes; the stage is skipped
+        }
+        in_st = in_st + 1 == kStages ? 0 : in_st + 1;
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) issue(i);
+    const float kmul = a.ks != nullptr ? __ldg(a.ks + h) : 1.f, vmul = a.vs != nullptr ? __ldg(a.vs + h) : 1.f;
+
+    // ---- Q: column g of tile nb is row rt * 8 NB + 8 nb + g, query r / G, head h * G + r % G
+    uint32_t qf[Sh::kQShared ? 1 : NB][KS][2];
+    int all_lo = 0, all_hi = INT_MAX;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      const int nq = Sh::kQShared ? 0 : nb;
+      const int r = 8 * nb + g;
+      const bool live = r < live_rows;
+      const int rr = rt * 8 * NB + (live ? r : live_rows - 1);   // dead rows: zeros with the last row's limits
+      const int i = listed ? token_i : rr / a.G, head = h * a.G + (listed ? rr : rr - i * a.G);
+      Rows rows;
+      rows.t0 = sp.t0, rows.n = sp.n, rows.len = sp.len;
+      rows.prefix = a.prefix != nullptr ? __ldg(a.prefix + b) : 0;
+      const E* src = static_cast<const E*>(a.q) + (static_cast<size_t>(sp.t0 + i) * a.Hq + head) * D;
+      uint2 raw[KS];
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        const int dim = D / 4 * t + 4 * k;
+        raw[k] = live ? __ldg(reinterpret_cast<const uint2*>(src + dim)) : make_uint2(0, 0);
+      }
+      float inv = 1.f;
+      if constexpr (std::is_same<E, __half>::value) {
+#pragma unroll
+        for (int k = 0; k < KS; ++k) qf[nq][k][0] = raw[k].x, qf[nq][k][1] = raw[k].y;
+      } else {
+        float amax = 0.f;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(raw[k].x << 16)), fabsf(__uint_as_float(raw[k].x & 0xFFFF0000u))));
+          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(raw[k].y << 16)), fabsf(__uint_as_float(raw[k].y & 0xFFFF0000u))));
+        }
+        const float mul = q_to_f16_scale(quad_max(amax), &inv);
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          qf[nq][k][0] = f32x2_to_f16x2(__uint_as_float(raw[k].x & 0xFFFF0000u) * mul, __uint_as_float(raw[k].x << 16) * mul);
+          qf[nq][k][1] = f32x2_to_f16x2(__uint_as_float(raw[k].y & 0xFFFF0000u) * mul, __uint_as_float(raw[k].y << 16) * mul);
+        }
+      }
+      if constexpr (Sh::kQShared) {
+#pragma unroll
+        for (int k = 0; k < KS; ++k) sq[(nb * KS + k) * 32] = make_uint2(qf[0][k][0], qf[0][k][1]);
+      }
+      const int hi = row_hi(a, rows, i), lo = row_lo(a, rows, i);
+      all_lo = max(all_lo, lo);
+      all_hi = min(all_hi, hi);
+      if (t == 0) {
+        RowInfo x;
+        x.lo = lo;
+        x.hi = hi;
+        x.sc = inv * (kCap ? a.scale_cap : a.scale_log2) * kmul;
+        x.slope = kBias ? __ldg(a.slopes + head) * kLog2e : 0.f;
+        x.at = static_cast<float>(i - sp.n);
+        ri[r] = x;
+      }
+    }
+    // keys that every row of the tile sees
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+      all_lo = max(all_lo, __shfl_xor_sync(0xffffffffu, all_lo, o));
+      all_hi = min(all_hi, __shfl_xor_sync(0xffffffffu, all_hi, o));
+    }
+    __syncwarp();
+    float sc[NB][2];    // columns 2t, 2t + 1
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) sc[nb][0] = ri[8 * nb + 2 * t].sc, sc[nb][1] = ri[8 * nb + 2 * t + 1].sc;
+
+    float O[NB][NT][4];
+    float m[NB][2], l[NB][2];   // m is 0 until the row has seen a key
+    uint32_t seen = 0;          // bit 2 nb + x: it has
+    bool fresh = true;          // some row has not (the same in all lanes)
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+      for (int i = 0; i < NT; ++i) O[nb][i][0] = O[nb][i][1] = O[nb][i][2] = O[nb][i][3] = 0.f;
+      m[nb][0] = m[nb][1] = 0.f;
+      l[nb][0] = l[nb][1] = 0.f;
+    }
+
+    int blk_j0 = -1;         // of the 32 groups at hand, one per lane; -1: no keys
+#pragma unroll 1
+    for (int i = 0; i < count; ++i) {
+      if ((i & 31) == 0) blk_j0 = at >= 0 ? next_j0 : -1;     // before the copies of the next 32 groups are issued
+      issue(i + kStages - 1);
+      const int j0 = __shfl_sync(0xffffffffu, blk_j0, i & 31);
+      if (!mbar_wait(&full[out_st], out_phase)) {
+        if (lane == 0) report_error(a.err, kDevErrTimeout);
+        // the copies still on their way land (or are given up) before the warp ends
+        for (int k = 1; k < kStages && i + k < count; ++k) {
+          out_phase ^= out_st + 1 == kStages;
+          out_st = out_st + 1 == kStages ? 0 : out_st + 1;
+          mbar_wait(&full[out_st], out_phase);
+        }
+        return;
+      }
+      __syncwarp();
+      const uint8_t* src = ring + out_st * Sh::kStage;
+      out_phase ^= out_st + 1 == kStages;
+      out_st = out_st + 1 == kStages ? 0 : out_st + 1;
+      if (j0 >= 0) {
+        float s[NB][4] = {};     // token p(g): columns 2t, 2t + 1; token p(g) + 8: the same
+        {
+          uint32_t w[2][KW], sc[2][D / 64];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint8_t* kp = src + ka + e * 8 * L::kRow;
+            if constexpr (KW == 4) {
+              const uint4 x = *reinterpret_cast<const uint4*>(kp);
+              w[e][0] = x.x, w[e][1] = x.y, w[e][KW - 2] = x.z, w[e][KW - 1] = x.w;
+              const uint32_t both = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(src + ksa + e * 8 * L::kScales));
+              sc[e][0] = __byte_perm(both, 0, 0x1010), sc[e][D / 64 - 1] = __byte_perm(both, 0, 0x3232);
+            } else {
+              const uint2 x = *reinterpret_cast<const uint2*>(kp);
+              w[e][0] = x.x, w[e][1] = x.y;
+              sc[e][0] = e4m3_to_f16x2_both(src[ksa + e * 8 * L::kScales]);
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < KW; ++k) {
+            uint32_t f0[4], f1[4];
+            e2m1x8_to_f16(w[0][k], f0);
+            e2m1x8_to_f16(w[1][k], f1);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f0[e] = f16x2_mul(f0[e], sc[0][k >> 1]), f1[e] = f16x2_mul(f1[e], sc[1][k >> 1]);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const uint32_t f[4] = {f0[2 * x], f1[2 * x], f0[2 * x + 1], f1[2 * x + 1]};
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) {
+                if constexpr (Sh::kQShared) {
+                  const uint2 q = sq[(nb * KS + 2 * k + x) * 32];
+                  mma16816(s[nb], f, q.x, q.y);
+                } else {
+                  mma16816(s[nb], f, qf[nb][2 * k + x][0], qf[nb][2 * k + x][1]);
+                }
+              }
+            }
+          }
+        }
+        const uint8_t* vsrc = src + Sh::kBlock;
+        uint32_t vw[4][VW], vsc[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int r = (c & 1 ? p1 : p0) + (c >> 1) * 8;
+          const uint8_t* vp = vsrc + r * L::kRow + VW * 4 * g;
+          if constexpr (VW == 2) {
+            const uint2 x = *reinterpret_cast<const uint2*>(vp);
+            vw[c][0] = x.x, vw[c][VW - 1] = x.y;
+          } else {
+            vw[c][0] = *reinterpret_cast<const uint32_t*>(vp);
+          }
+          vsc[c] = vsrc[vsa + r * L::kScales];
+        }
+        // ---- y - m in log2 units, y with log2 of the value scale
+        float z[NB][4];
+        bool up = fresh;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float f = sc[nb][x], off = -m[nb][x];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float& v = z[nb][2 * e + x];
+              v = s[nb][2 * e + x];
+              float o = off;
+              if constexpr (kBias) {
+                const RowInfo& q = ri[8 * nb + 2 * t + x];
+                o = fmaf(q.slope, static_cast<float>(j0 + pg + 8 * e - sp.len) - q.at, o);
+              }
+              if constexpr (kCap) v = fmaf(a.cap_log2, a.far_cap ? tanh_far(v * f) : tanh_of(v * f), o);
+              else v = fmaf(v, f, o);
+            }
+          }
+        }
+        uint32_t nan = 0;      // tokens whose V scale of this chunk is NaN and counts as zero
+        if (j0 < all_lo || j0 + kGroup > all_hi) {   // some row does not see some key
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const RowInfo& q = ri[8 * nb + 2 * t + (e & 1)];
+              const int j = j0 + pg + 8 * (e >> 1);
+              if (j < q.lo || j >= q.hi) z[nb][e] = -INFINITY;
+            }
+          }
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            // tokens behind the last may hold anything
+            if (j0 + (c & 1 ? p1 : p0) + 8 * (c >> 1) >= sp.len) {
+              vsc[c] = 0;
+#pragma unroll
+              for (int k = 0; k < VW; ++k) vw[c][k] = 0;
+            }
+            if (e4m3_is_nan(vsc[c])) nan |= 1u << ((c & 1 ? p1 : p0) + 8 * (c >> 1)), vsc[c] = 0;
+          }
+          nan |= __shfl_xor_sync(0xffffffffu, nan, 1);
+          nan |= __shfl_xor_sync(0xffffffffu, nan, 2);
+        }
+        // a row's first key, or one that exceeds the range of P
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+          up |= fmaxf(fmaxf(z[nb][0], z[nb][1]), fmaxf(z[nb][2], z[nb][3])) > kMaxP;
+        if (__any_sync(0xffffffffu, up)) {
+          uint32_t now = 0;
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const bool was = seen >> (2 * nb + x) & 1;
+              // the row's maximum so far lies between m + kSetP and m + kMaxP: m only grows
+              const float top = col_max(fmaxf(z[nb][x], z[nb][2 + x])) - kSetP;
+              const float d = was ? fmaxf(top, 0.f) : top;      // the move of m
+              if (d > -INFINITY) {
+                now |= 1u << (2 * nb + x);
+                m[nb][x] += d;
+                z[nb][x] -= d;
+                z[nb][2 + x] -= d;
+                const float f = was ? fast_exp2(-d) : 0.f;
+                l[nb][x] *= f;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                  O[nb][n][x] *= f;
+                  O[nb][n][2 + x] *= f;
+                }
+              }
+            }
+          }
+          seen |= now;
+          fresh = __any_sync(0xffffffffu, seen != (1u << 2 * NB) - 1);
+        }
+        uint32_t pf[NB][2];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          float p[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) p[e] = fast_exp2(z[nb][e]);
+          l[nb][0] += p[0] + p[2];
+          l[nb][1] += p[1] + p[3];
+          pf[nb][0] = transpose8(f32x2_to_f16x2(p[1], p[0]));
+          pf[nb][1] = transpose8(f32x2_to_f16x2(p[3], p[2]));
+        }
+        // ---- O^T += V^T P^T
+        const uint32_t v01 = e4m3x2_to_f16x2(static_cast<uint16_t>(vsc[0] | vsc[1] << 8));
+        const uint32_t v23 = e4m3x2_to_f16x2(static_cast<uint16_t>(vsc[2] | vsc[3] << 8));
+#pragma unroll
+        for (int k = 0; k < VW; ++k) {
+          // byte i: dims 8 k + 2 i (even) and 8 k + 2 i + 1 (odd) of two tokens
+          uint32_t even[2][4], odd[2][4];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t u0 = vw[2 * e][k], u1 = vw[2 * e + 1][k], low = 0x0F0F0F0Fu, f = e ? v23 : v01;
+            e2m1x8_to_f16((u0 & low) | (u1 << 4 & ~low), even[e]);
+            e2m1x8_to_f16((u0 >> 4 & low) | (u1 & ~low), odd[e]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) even[e][i] = f16x2_mul(even[e][i], f), odd[e][i] = f16x2_mul(odd[e][i], f);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t f[4] = {even[0][i], odd[0][i], even[1][i], odd[1][i]};
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) mma16816(O[nb][4 * k + i], f, pf[nb][0], pf[nb][1]);
+          }
+        }
+        if (__builtin_expect(nan != 0, 0)) {     // differs between chunks; no shuffle in here
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const RowInfo& q = ri[8 * nb + 2 * t + x];
+              for (uint32_t bits = nan; bits != 0; bits &= bits - 1) {
+                const int j = j0 + __ffs(bits) - 1;
+                if (j < q.lo || j >= q.hi) continue;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) O[nb][n][x] = O[nb][n][2 + x] = __uint_as_float(0x7FC00000u);
+              }
+            }
+          }
+        }
+      }
+      __syncwarp();   // the stage may be filled again
+    }
+    // ---- the run's part of this task: dims [VB g, VB g + VB) of columns 2t, 2t + 1.
+    // l = 0: no key seen; NaN (of a NaN score, which moves no m) goes into o and lse.
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int r = 8 * nb + 2 * t + x;
+        const float lsum = col_sum(l[nb][x]);
+        if (r >= live_rows) continue;
+        if (whole_task) {
+          const int rr = rt * 8 * NB + r, i = listed ? token_i : rr / a.G, head = h * a.G + (listed ? rr : rr - i * a.G);
+          const size_t row = static_cast<size_t>(sp.t0 + i) * a.Hq + head;
+          const float so = lsum == 0.f ? 0.f : vmul / lsum;
+          uint32_t w[NT];
+#pragma unroll
+          for (int n = 0; n < NT; ++n) w[n] = pack_out<E>(O[nb][n][2 + x] * so, O[nb][n][x] * so);
+          uint4* out = reinterpret_cast<uint4*>(static_cast<E*>(a.o) + row * D + VB * g);
+#pragma unroll
+          for (int n = 0; n < NT / 4; ++n) out[n] = make_uint4(w[4 * n], w[4 * n + 1], w[4 * n + 2], w[4 * n + 3]);
+          if (g == 0 && a.lse != nullptr)
+            a.lse[row] = lsum == 0.f ? -INFINITY : (m[nb][x] + log2f(lsum)) * kLn2;
+        } else {
+          float4* out = reinterpret_cast<float4*>(sa.part_o + (piece * (8 * NB) + r) * D + VB * g);
+#pragma unroll
+          for (int n = 0; n < NT / 2; ++n)
+            out[n] = make_float4(O[nb][2 * n][x] * vmul, O[nb][2 * n][2 + x] * vmul, O[nb][2 * n + 1][x] * vmul, O[nb][2 * n + 1][2 + x] * vmul);
+          if (g == 0) sa.part_ml[piece * (8 * NB) + r] = make_float2(lsum == 0.f ? -INFINITY : m[nb][x], lsum);
+        }
+      }
+    }
+    __syncwarp();
+    u += count;
+  }
+}
+
+template <typename E, int D, bool kCap, bool kBias, int NB>
+cudaError_t go(SplitArgs& a, int sms, cudaStream_t s) {
+  using Sh = Shape<D, NB>;
+  constexpr size_t smem = Sh::kBytes;
+  auto kernel = attend_split4_kernel<E, D, kCap, kBias, NB>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  const unsigned blocks = static_cast<unsigned>(sms * Sh::kBlocks);
+  a.workers = static_cast<int>(blocks) * kWarps / a.side;   // side divides kWarps * 2, blocks is even
+  return launch(kernel, blocks, kWarps * 32, smem, s, a);
+}
+
+template <typename E, int D, bool kCap, bool kBias>
+cudaError_t pick3(SplitArgs& a, int sms, cudaStream_t s) {
+  switch (a.tile / 8) {
+    case 1: return go<E, D, kCap, kBias, 1>(a, sms, s);
+    case 2: return go<E, D, kCap, kBias, 2>(a, sms, s);
+    default: return go<E, D, kCap, kBias, 3>(a, sms, s);
+  }
+}
+
+template <typename E, int D>
+cudaError_t pick2(SplitArgs& a, int sms, cudaStream_t s) {
+  const bool cap = a.p.cap_log2 > 0.f, bias = a.p.slopes != nullptr;
+  if (cap) return bias ? pick3<E, D, true, true>(a, sms, s) : pick3<E, D, true, false>(a, sms, s);
+  return bias ? pick3<E, D, false, true>(a, sms, s) : pick3<E, D, false, false>(a, sms, s);
+}
+
+template <typename E>
+cudaError_t pick(SplitArgs& a, int D, int sms, cudaStream_t s) {
+  return D == 64 ? pick2<E, 64>(a, sms, s) : pick2<E, 128>(a, sms, s);
+}
+
+constexpr int kBlocks[3] = {Shape<128, 1>::kBlocks, Shape<128, 2>::kBlocks, Shape<128, 3>::kBlocks};
+
+// With selected pages: the split form, whose tiles hold a token's heads.
+Plan list_plan(int G) {
+  Plan p;
+  p.tiled = false, p.split = true;
+  p.tile = 8 * (G <= 8 ? 1 : G <= 16 ? 2 : 3);
+  p.split_rows = INT_MAX;
+  return p;
+}
+
+}  // namespace
+
+size_t attend_group4_workspace_bytes(int B, int T, int Hq, int Hkv, int D) {
+  // whatever max_seqlen_q will be, and with a list
+  const int G = Hq / Hkv;
+  size_t most = sizes(list_plan(G), T, D, kAttendMaxSms, kBlocks).total();
+  for (int q = 1; ; q = q * 2 < T ? q * 2 : T) {
+    const size_t n = sizes(plan_for(B, T, q, G), T, D, kAttendMaxSms, kBlocks).total();
+    most = n > most ? n : most;
+    if (q >= T || static_cast<long long>(q) * G > 2 * kSplitRows) break;
+  }
+  const size_t n = sizes(plan_for(B, T, T, G), T, D, kAttendMaxSms, kBlocks).total();
+  return n > most ? n : most;
+}
+
+cudaError_t launch_attend_group4(const qpkv_attend_group4_params& p, cudaStream_t stream) {
+  SplitArgs a;
+  Page8Args& x = a.p;
+  x.B = p.num_seqs, x.T = p.num_tokens, x.Hq = p.num_heads_q, x.Hkv = p.num_heads_kv;
+  x.G = p.num_heads_q / p.num_heads_kv;
+  x.ps = p.page_size, x.num_pages = p.num_pages, x.bt_stride = p.bt_stride;
+  x.causal = p.causal ? 1 : 0;
+  x.window = p.window;
+  x.scale_log2 = p.sm_scale * kLog2e;
+  x.scale_cap = p.logit_cap > 0.f ? p.sm_scale / p.logit_cap : 0.f;
+  x.cap_log2 = p.logit_cap > 0.f ? p.logit_cap * kLog2e : 0.f;
+  x.far_cap = p.logit_cap > kNearCap;
+  x.hnd = 1;
+  x.cu = p.cu_seqlens_q, x.lens = p.seqlens_kv, x.bt = p.block_table, x.prefix = p.prefix_lens;
+  x.slopes = p.alibi_slopes, x.ks = p.k_mul, x.vs = p.v_mul;
+  x.q = p.q;
+  x.k = static_cast<const uint8_t*>(p.k_pool), x.v = static_cast<const uint8_t*>(p.v_pool);
+  x.o = p.o, x.lse = p.lse, x.err = p.error_word;
+  a.sel = p.selected, a.n_sel = p.num_selected;
+  int sms = sm_count();
+  if (sms > kAttendMaxSms) sms = kAttendMaxSms;
+  const Plan plan = p.selected != nullptr ? list_plan(x.G) : plan_for(p.num_seqs, p.num_tokens, p.max_seqlen_q, x.G);
+  x.split_rows = plan.split_rows;
+  a.side = x.Hkv % 8 == 0 ? 8 : x.Hkv % 4 == 0 ? 4 : x.Hkv % 2 == 0 ? 2 : 1;
+  a.tile = plan.tile;
+  const Sizes sz = sizes(plan, p.num_tokens, p.head_dim, sms, kBlocks);
+  uint8_t* ws = static_cast<uint8_t*>(p.workspace);
+  a.info = reinterpret_cast<TokenInfo*>(ws);
+  a.part_o = reinterpret_cast<float*>(ws + sz.info);
+  a.part_ml = reinterpret_cast<float2*>(ws + sz.info + sz.o);
+  TileArgs t;
+  t.p = x;
+  t.tq = x.G <= 128 ? 128 / x.G : 1;
+  t.info = a.info;
+  t.part_o = reinterpret_cast<float*>(ws + sz.info + sz.o + sz.ml);
+  t.part_ml = reinterpret_cast<float2*>(ws + sz.info + sz.o + sz.ml + sz.to);
+  const bool f16 = p.dtype == QPKV_DTYPE_F16;
+  cudaError_t e = cudaSuccess;
+  if (plan.split) {
+    const int even = sms - (sms & 1);   // an even number of blocks
+    e = f16 ? pick<__half>(a, p.head_dim, even, stream) : pick<__nv_bfloat16>(a, p.head_dim, even, stream);
+  }
+  if (e == cudaSuccess && plan.tiled) e = launch_attend_tiles4(t, p.head_dim, f16, sms, stream);
+  if (e != cudaSuccess) return e;
+  JoinArgs j;
+  j.T = p.num_tokens, j.Hq = p.num_heads_q, j.G = x.G;
+  j.info = a.info;
+  j.set[0] = {a.part_o, a.part_ml, a.tile, a.side};
+  j.set[1] = {t.part_o, t.part_ml, 256, 1};
+  j.o = p.o, j.lse = p.lse;
+  if (f16) return p.head_dim == 64 ? join<__half, 64>(j, sms, stream) : join<__half, 128>(j, sms, stream);
+  return p.head_dim == 64 ? join<__nv_bfloat16, 64>(j, sms, stream) : join<__nv_bfloat16, 128>(j, sms, stream);
+}
+
+}  // namespace qpkv

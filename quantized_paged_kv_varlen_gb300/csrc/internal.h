@@ -88,6 +88,15 @@ cudaError_t launch_write_page8(const qpkv_write_page8_params& p, cudaStream_t st
 size_t attend_page8_workspace_bytes(int B, int T, int Hq, int Hkv, int D);
 cudaError_t launch_attend_page8(const qpkv_attend_page8_params& p, cudaStream_t stream);
 
+// The cache in 4 bits (write_group4.cu, attend_group4.cu) and the choice of its
+// pages (select_pages.cu).
+constexpr int kSelectMaxPages = 1 << 18;   // pages of a table row
+cudaError_t launch_write_group4(const qpkv_write_group4_params& p, cudaStream_t stream);
+cudaError_t launch_read_group4(const qpkv_read_group4_params& p, cudaStream_t stream);
+cudaError_t launch_select_pages(const qpkv_select_pages_params& p, cudaStream_t stream);
+size_t attend_group4_workspace_bytes(int B, int T, int Hq, int Hkv, int D);
+cudaError_t launch_attend_group4(const qpkv_attend_group4_params& p, cudaStream_t stream);
+
 // The library-owned device error word of the current device (errors.cu),
 // used by the entry points when the caller passes no word; NULL on failure.
 int32_t* default_error_word();

@@ -116,7 +116,7 @@ struct alignas(16) TokenInfo {
   int pad[3];
 };
 
-// The tiled form (attend_page8_tile.cu): 128 / G whole queries per tile, two
+// The tiled form (attend_tile.cuh): 128 / G whole queries per tile, two
 // tiles per item, one worker per CTA.
 struct TileArgs {
   Page8Args p;
@@ -126,6 +126,8 @@ struct TileArgs {
   TokenInfo* info;    // [T]
 };
 cudaError_t launch_attend_tiles(const TileArgs& a, int head_dim, bool int8, bool f16, int sms, cudaStream_t stream);
+// The same over the 4-bit cache: ks and vs hold a factor per kv head, or are null.
+cudaError_t launch_attend_tiles4(const TileArgs& a, int head_dim, bool f16, int sms, cudaStream_t stream);
 
 // Four 8-bit codes as two pairs of f16 (exact).
 template <bool kInt8>

@@ -1,0 +1,367 @@
+// The pages that each query token attends to, by a cheap score of every page
+// ("KvQuantSparseFlashAttention" README, 参数说明 row sparse_indices: block-wise
+// index lists per query token and kv head, which come from outside there).
+//
+//   c = RNE(q * 127 / a), a = max |q| over the G heads of a kv head
+//   score(page) = scale(page) * max_g sum_d max(c_gd min_d, c_gd max_d)
+//               = scale(page) * max_g (c_g^+ . max + c_g^- . min)
+// a bound on what any key between the page's bounds can score.  Sums are whole
+// numbers of at most 127 * 127 * 128 < 2^21, so f16 products summed in float32
+// by the tensor core are exact and so is the order of the scores.
+//
+// The bounds are read once, 2 D bytes a (page, head): HBM- or L2-bound.  A
+// cluster of 1 to 8 blocks takes one (token, kv head): few rows over long caches
+// still fill the GPU.  Scores:
+// warps take 16 pages at a time as the rows of m16n8k16, heads as its 8 columns
+// (padded with copies); a thread's bytes of a page are 16-byte chunks whose
+// channels are the k index in an order that the queries follow.  Scores become
+// integers of the same order in shared memory; the n-th largest is found eight bits
+// at a time by histograms that the cluster adds up through distributed shared
+// memory, ties go to the lower page by counting.
+#include <cooperative_groups.h>
+#include <type_traits>
+
+#include "common.cuh"
+#include "group4.cuh"
+#include "internal.h"
+#include "page8.cuh"
+
+namespace qpkv {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kMaxKeys = 48 * 1024;      // scores of a block in shared memory
+
+struct SelectArgs {
+  int B, T, Hq, H, G, ps, num_pages, bt_stride, n, first, last, window;
+  const int32_t *cu, *lens, *bt;
+  const void* q;
+  const int8_t* bounds;
+  const float* bscale;
+  int32_t* out;
+  int* err;
+};
+
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// An unsigned integer that orders like the float; finite and infinite scores are above 0.
+__device__ __forceinline__ uint32_t key_of(float s) {
+  const uint32_t u = __float_as_uint(s);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+template <typename E>
+__device__ __forceinline__ float to_f32(uint32_t half_word) {
+  if constexpr (std::is_same<E, __half>::value) {
+    return __half2float(__ushort_as_half(static_cast<unsigned short>(half_word)));
+  } else {
+    return __uint_as_float(half_word << 16);
+  }
+}
+
+// c of an element: RNE(q * 127 / a).  q has 11 significant bits at most, so
+// q * 127 is exact and the quotient, off by half a step, never crosses a tie
+// that it does not meet.
+template <typename E>
+__device__ __forceinline__ float code_of(uint32_t half_word, float a) {
+  return rintf(__fdiv_rn(to_f32<E>(half_word) * 127.f, a));
+}
+
+template <typename E, int D, int NB>
+__global__ void __launch_bounds__(kThreads) select_pages_kernel(const __grid_constant__ SelectArgs a) {
+  constexpr int KC = D / 32;          // 16-byte chunks of a page's 2 D bounds per thread
+  extern __shared__ uint32_t s_key[];
+  __shared__ uint32_t s_hist[4][256], s_sum[256];
+  __shared__ int s_gt[kWarps], s_eq[kWarps];
+  __shared__ int2 s_total;
+  __shared__ float s_amax[kWarps];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int row = blockIdx.x / C, tok = row / a.H, h = row - tok * a.H;
+  const int b = warp_last_at_most(a.B, tok, [&](int m) { return static_cast<long long>(__ldg(a.cu + m - 1)); });
+  // equal prefix sums: the last of them is the one with the rows
+  const int t0 = seq_begin(a.cu, b), n_q = __ldg(a.cu + b) - t0;
+  if (tok < t0 || tok >= t0 + n_q) return;                // behind the last sequence
+  int len = __ldg(a.lens + b);
+  if (t0 < 0 || t0 + static_cast<long long>(n_q) > a.T || len < 0 || len > static_cast<long long>(a.bt_stride) * a.ps) {
+    if (tid == 0) report_error(a.err, kDevErrBadLength);
+    len = 0;
+  }
+  int32_t* out = a.out + static_cast<size_t>(row) * a.n;
+  const long long at = static_cast<long long>(len) - n_q + (tok - t0);
+  if (len == 0 || at < 0) {
+    if (rank == 0)
+      for (int i = tid; i < a.n; i += kThreads) out[i] = -1;
+    return;
+  }
+  const int p_hi = static_cast<int>(at / a.ps);
+  const int p_lo = a.window > 0 ? static_cast<int>(max(0ll, at + 1 - a.window) / a.ps) : 0;
+  const int share = (p_hi - p_lo + C) / C;                // candidates of a block
+  const int p0 = min(p_lo + rank * share, p_hi + 1), count = min(share, p_hi + 1 - p0);
+  const int32_t* bt = a.bt + static_cast<size_t>(b) * a.bt_stride + p0;
+
+  for (int i = tid; i < 4 * 256; i += kThreads) (&s_hist[0][0])[i] = 0;
+  // ---- the queries: their largest magnitude, then c
+  const uint16_t* q = static_cast<const uint16_t*>(a.q) + (static_cast<size_t>(tok) * a.Hq + h * a.G) * D;
+  float amax;
+  {
+    uint32_t top = 0;     // magnitudes are ordered like their bits
+    for (int i = tid; i < a.G * D / 8; i += kThreads) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(q) + i);
+      top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
+    }
+    const uint32_t one = __reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16));
+    if (lane == 0) s_amax[warp] = __uint_as_float(one);
+    __syncthreads();
+    uint32_t all = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) all = max(all, __float_as_uint(s_amax[w]));
+    amax = to_f32<E>(all);
+  }
+  const bool scored = amax > 0.f && amax < INFINITY;
+
+  // ---- scores
+  for (int c0 = 0; c0 < a.G; c0 += 8 * NB) {
+    // columns: heads c0 .. c0 + 8 NB, those behind the last are copies of others
+    uint32_t qf[NB][4 * KC][2];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      const uint16_t* qh = q + static_cast<size_t>((c0 + 8 * nb + g) % a.G) * D;
+#pragma unroll
+      for (int c = 0; c < KC; ++c) {
+        const int dim0 = (16 * (t + 4 * c)) % D;
+        const bool is_max = c >= KC / 2;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint2 w = __ldg(reinterpret_cast<const uint2*>(qh + dim0 + 4 * k));
+          float x[4] = {0.f, 0.f, 0.f, 0.f};
+          if (scored) {
+            x[0] = code_of<E>(w.x & 0xFFFFu, amax), x[1] = code_of<E>(w.x >> 16, amax);
+            x[2] = code_of<E>(w.y & 0xFFFFu, amax), x[3] = code_of<E>(w.y >> 16, amax);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] = is_max ? fmaxf(x[e], 0.f) : fminf(x[e], 0.f);
+          qf[nb][4 * c + k][0] = f32x2_to_f16x2(x[1], x[0]);
+          qf[nb][4 * c + k][1] = f32x2_to_f16x2(x[3], x[2]);
+        }
+      }
+    }
+    for (int i0 = warp * 32; i0 < count; i0 += kWarps * 32) {
+      // 32 pages, a lane looks up one
+      int page = -1;
+      float scale = 0.f;
+      if (i0 + lane < count) {
+        page = __ldg(bt + i0 + lane);
+        if (page < 0 || page >= a.num_pages) {
+          report_error(a.err, kDevErrBadPage);
+          page = -1;
+        } else {
+          scale = __ldg(a.bscale + static_cast<size_t>(page) * a.H + h);
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        uint4 x[2][KC];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int pg = __shfl_sync(0xffffffffu, page, 16 * s + 8 * e + g);
+          const uint4* src = reinterpret_cast<const uint4*>(a.bounds + (static_cast<size_t>(pg < 0 ? 0 : pg) * a.H + h) * 2 * D) + t;
+#pragma unroll
+          for (int c = 0; c < KC; ++c) x[e][c] = pg < 0 ? make_uint4(0, 0, 0, 0) : __ldg(src + 4 * c);
+        }
+        float d[NB][4] = {};
+#pragma unroll
+        for (int c = 0; c < KC; ++c) {
+          const uint32_t w0[4] = {x[0][c].x, x[0][c].y, x[0][c].z, x[0][c].w};
+          const uint32_t w1[4] = {x[1][c].x, x[1][c].y, x[1][c].z, x[1][c].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t f[4];
+            widen<true>(w0[k], f[0], f[2]);
+            widen<true>(w1[k], f[1], f[3]);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) mma16816(d[nb], f, qf[nb][4 * c + k][0], qf[nb][4 * c + k][1]);
+          }
+        }
+        float m0 = fmaxf(d[0][0], d[0][1]), m1 = fmaxf(d[0][2], d[0][3]);
+#pragma unroll
+        for (int nb = 1; nb < NB; ++nb) {
+          m0 = fmaxf(m0, fmaxf(d[nb][0], d[nb][1]));
+          m1 = fmaxf(m1, fmaxf(d[nb][2], d[nb][3]));
+        }
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+          m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
+          m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+        }
+        // lane 4 g (+ 1) has pages g (+ 8)
+        const int mine = 16 * s + (t == 0 ? g : g + 8);
+        const float sc = __shfl_sync(0xffffffffu, scale, mine);
+        const int pg = __shfl_sync(0xffffffffu, page, mine), i = i0 + mine;
+        if (t < 2 && i < count) {
+          const int p = p0 + i;
+          uint32_t key = 0;
+          if (pg >= 0) {
+            key = p - p_lo < a.first || p_hi - p < a.last ? 0xFFFFFFFFu
+                  : key_of(sc == INFINITY ? INFINITY : (t == 0 ? m0 : m1) * sc);
+          }
+          s_key[i] = c0 == 0 ? key : max(key, s_key[i]);
+        }
+      }
+    }
+    __syncwarp();    // a warp's keys are its own until all columns are through
+  }
+  __syncthreads();
+
+  // ---- the n-th largest key, `need` of those that equal it among the n.  A thread
+  // takes keys tid * per ...: an odd number apart, so that banks differ.
+  uint32_t prefix = 0;
+  int need = a.n;
+  for (int pass = 0; pass < 4; ++pass) {
+    const int shift = 24 - 8 * pass;
+    for (int i = tid; i < count; i += kThreads) {
+      const uint32_t key = s_key[i];
+      if (key != 0 && (pass == 0 || key >> (shift + 8) == prefix)) atomicAdd(&s_hist[pass][key >> shift & 255], 1u);
+    }
+    const uint32_t* sums = s_hist[pass];
+    if (C > 1) {
+      cluster.sync();
+      uint32_t sum = 0;
+      for (int r = 0; r < C; ++r) sum += *cluster.map_shared_rank(&s_hist[pass][tid], r);
+      s_sum[tid] = sum;
+      sums = s_sum;
+    }
+    __syncthreads();
+    // every warp for itself: bins of lane l are 255 - 8 l and the seven below it
+    int bin[8], mine = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) mine += bin[k] = static_cast<int>(sums[255 - 8 * lane - k]);
+    int upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += u;
+    }
+    if (pass == 0 && __shfl_sync(0xffffffffu, upto, 31) <= a.n) {   // all of them
+      prefix = 0;
+      need = 0;
+      break;
+    }
+    const uint32_t reach = __ballot_sync(0xffffffffu, upto >= need);
+    const int who = __ffs(reach) - 1;
+    int before = upto - mine, digit = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (before + bin[k] >= need) {
+        digit = 255 - 8 * lane - k;
+        break;
+      }
+      before += bin[k];
+    }
+    need -= __shfl_sync(0xffffffffu, before, who);
+    prefix = prefix << 8 | __shfl_sync(0xffffffffu, digit, who);
+    if (C > 1) __syncthreads();     // s_sum is read before it is written again
+  }
+
+  // ---- write them in their order
+  const int per = ((count + kThreads - 1) / kThreads) | 1;
+  const int i0 = min(count, tid * per), i1 = min(count, i0 + per);
+  int gt = 0, eq = 0;
+  for (int i = i0; i < i1; ++i) {
+    const uint32_t key = s_key[i];
+    gt += key > prefix;
+    eq += key == prefix && key != 0;
+  }
+  int gt_at = gt, eq_at = eq;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, gt_at, o), v = __shfl_up_sync(0xffffffffu, eq_at, o);
+    if (lane >= o) gt_at += u, eq_at += v;
+  }
+  if (lane == 31) s_gt[warp] = gt_at, s_eq[warp] = eq_at;
+  gt_at -= gt, eq_at -= eq;
+  __syncthreads();
+  int2 all = make_int2(0, 0);
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) gt_at += s_gt[w], eq_at += s_eq[w];
+    all.x += s_gt[w], all.y += s_eq[w];
+  }
+  if (C > 1) {
+    if (tid == 0) s_total = all;
+    cluster.sync();
+    all = make_int2(0, 0);
+    for (int r = 0; r < C; ++r) {
+      const int2 x = *cluster.map_shared_rank(&s_total, r);
+      if (r < rank) gt_at += x.x, eq_at += x.y;
+      all.x += x.x, all.y += x.y;
+    }
+    cluster.sync();     // nobody leaves while its totals are read
+  }
+  for (int i = i0; i < i1; ++i) {
+    const uint32_t key = s_key[i];
+    const bool is_eq = key == prefix && key != 0;
+    if (key > prefix || (is_eq && eq_at < need)) out[gt_at + min(eq_at, need)] = p0 + i;
+    gt_at += key > prefix;
+    eq_at += is_eq;
+  }
+  if (rank == 0)
+    for (int i = all.x + min(all.y, need) + tid; i < a.n; i += kThreads) out[i] = -1;
+}
+
+template <typename E, int D, int NB>
+cudaError_t go(const SelectArgs& a, int C, cudaStream_t stream) {
+  auto kernel = select_pages_kernel<E, D, NB>;
+  const size_t smem = static_cast<size_t>((a.bt_stride + C - 1) / C) * 4;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxKeys * 4);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.T) * a.H * C);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = C;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+template <typename E>
+cudaError_t pick(const SelectArgs& a, int D, int C, cudaStream_t s) {
+  if (D == 64) return a.G <= 8 ? go<E, 64, 1>(a, C, s) : go<E, 64, 2>(a, C, s);
+  return a.G <= 8 ? go<E, 128, 1>(a, C, s) : go<E, 128, 2>(a, C, s);
+}
+
+}  // namespace
+
+cudaError_t launch_select_pages(const qpkv_select_pages_params& p, cudaStream_t stream) {
+  SelectArgs a;
+  a.B = p.num_seqs, a.T = p.num_tokens, a.Hq = p.num_heads_q, a.H = p.num_heads_kv, a.G = p.num_heads_q / p.num_heads_kv;
+  a.ps = p.page_size, a.num_pages = p.num_pages, a.bt_stride = p.bt_stride;
+  a.n = p.num_selected, a.first = p.first, a.last = p.last, a.window = p.window;
+  a.cu = p.cu_seqlens_q, a.lens = p.seqlens_kv, a.bt = p.block_table;
+  a.q = p.q, a.bounds = static_cast<const int8_t*>(p.k_bounds), a.bscale = p.bound_scale;
+  a.out = p.selected, a.err = p.error_word;
+  // blocks of a row: as many as leave an SM two, of 64 pages at least
+  const long long rows = static_cast<long long>(a.T) * a.H;
+  int C = 1;
+  while (C < 8 && ((rows * C * 2 <= 2 * 152 && a.bt_stride / (2 * C) >= 64) || (a.bt_stride + C - 1) / C > kMaxKeys)) C *= 2;
+  return p.dtype == QPKV_DTYPE_F16 ? pick<__half>(a, p.head_dim, C, stream) : pick<__nv_bfloat16>(a, p.head_dim, C, stream);
+}
+
+}  // namespace qpkv
