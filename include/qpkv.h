@@ -987,7 +987,12 @@ qpkv_status qpkv_select_pages(const qpkv_select_pages_params* params, void* stre
  * no key of the sequence is skipped (QPKV_DEV_ERR_BAD_INDEX), a page listed
  * twice counts twice.  A NaN scale makes NaN what sees its token: a K scale the
  * whole row, a V scale the 16 channels; rows that do not see the token are not
- * touched by it. */
+ * touched by it.
+ * Calls with `selected`, and those with bt_stride * page_size <= 4096 and at most
+ * 24 query rows of a (sequence, kv head) by max_seqlen_q, use no workspace: it may
+ * be NULL (elsewhere that is WORKSPACE_TOO_SMALL).  UNSUPPORTED too: num_pages *
+ * Hkv * page_size / 16 above 2^31 - 1; with `selected` T * Hq or num_selected *
+ * page_size above that. */
 typedef struct qpkv_attend_group4_params {
   int32_t num_seqs;
   int32_t num_tokens;
@@ -1023,8 +1028,7 @@ typedef struct qpkv_attend_group4_params {
   int32_t* error_word;
 } qpkv_attend_group4_params;
 
-/* Device workspace bytes of qpkv_attend_group4, with or without selected pages
- * (0 for arguments it refuses). */
+/* Device workspace bytes of qpkv_attend_group4 (0 for arguments it refuses). */
 size_t qpkv_attend_group4_workspace_bytes(int32_t num_seqs, int32_t num_tokens, int32_t num_heads_q,
                                           int32_t num_heads_kv, int32_t head_dim);
 

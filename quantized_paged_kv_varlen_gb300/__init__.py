@@ -43,6 +43,7 @@ DEV_ERR_BAD_LENGTH = 8
 DEV_ERR_NO_PAGES = 16
 
 ERR_UNSUPPORTED = 2
+ERR_WORKSPACE_TOO_SMALL = 3
 ERR_CUDA = 4
 ERR_DEVICE = 5
 ERR_TIMEOUT = 6
@@ -1346,15 +1347,13 @@ def attend_group4(q, k_pool, v_pool, block_table, cu_seqlens_q, seqlens_kv, max_
         op = out.data_ptr()
     else:
         op = _arr(out, "out", dtype, shape, dev)
-    if workspace is None:
-        n = lib.qpkv_attend_group4_workspace_bytes(B, T, Hq, H, D)
-        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
-    else:
+    n, ws = 0, None
+    if workspace is not None:
         if workspace.get_device() != dev:
             raise ValueError("workspace must live on the current device")
         if not workspace.is_contiguous():   # its bytes would not be those it is said to have
             raise ValueError("workspace must be contiguous")
-        n = workspace.numel() * workspace.element_size()
+        n, ws = workspace.numel() * workspace.element_size(), workspace.data_ptr()
     p = AttendGroup4Params(
         B, T, max_seqlen_q, Hq, H, D, ps, P, W, _dtype_code(dtype), 1 if causal else 0, window,
         n_sel, sm_scale if sm_scale else 0.0, logit_cap, 0,
@@ -1365,6 +1364,12 @@ def attend_group4(q, k_pool, v_pool, block_table, cu_seqlens_q, seqlens_kv, max_
         None if alibi_slopes is None else _arr(alibi_slopes, "alibi_slopes", f32, (Hq,), dev),
         qp, kpool, vpool, _mul(k_mul, "k_mul", H, dev), _mul(v_mul, "v_mul", H, dev), op,
         None if lse is None else _arr(lse, "lse", f32, (T, Hq), dev),
-        workspace.data_ptr(), n, _error_ptr(error_word, dev))
-    _check(lib.qpkv_attend_group4(ctypes.byref(p), stream), "qpkv_attend_group4")
+        ws, n, _error_ptr(error_word, dev))
+    status = lib.qpkv_attend_group4(ctypes.byref(p), stream)
+    if status == ERR_WORKSPACE_TOO_SMALL and workspace is None:   # a call that needs one
+        n = lib.qpkv_attend_group4_workspace_bytes(B, T, Hq, H, D)
+        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+        p.workspace, p.workspace_bytes = workspace.data_ptr(), n
+        status = lib.qpkv_attend_group4(ctypes.byref(p), stream)
+    _check(status, "qpkv_attend_group4")
     return out

@@ -125,18 +125,22 @@ qpkv_status qpkv_attend_group4(const qpkv_attend_group4_params* p, void* stream)
   if (!heads_fit(p->num_heads_q, p->num_heads_kv, p->num_tokens)) return QPKV_ERR_UNSUPPORTED;
   // blocks of 16 tokens of the pools, and units of a listed task
   if (static_cast<int64_t>(p->num_pages) * p->num_heads_kv > INT32_MAX / (p->page_size / 16)) return QPKV_ERR_UNSUPPORTED;
-  if (p->selected != nullptr && static_cast<int64_t>(p->num_selected) * p->page_size > INT32_MAX - 64)
+  if (p->selected != nullptr &&
+      (static_cast<int64_t>(p->num_selected) * p->page_size > INT32_MAX - 64 ||
+       static_cast<int64_t>(p->num_tokens) * p->num_heads_q > INT32_MAX))
     return QPKV_ERR_UNSUPPORTED;
   if (p->num_seqs == 0 || p->num_tokens == 0) return QPKV_OK;
   if (p->cu_seqlens_q == nullptr || p->seqlens_kv == nullptr || p->block_table == nullptr || p->q == nullptr ||
-      p->k_pool == nullptr || p->v_pool == nullptr || p->o == nullptr || p->workspace == nullptr)
+      p->k_pool == nullptr || p->v_pool == nullptr || p->o == nullptr)
     return QPKV_ERR_INVALID_ARG;
   if (!aligned(p->q, 16) || !aligned(p->k_pool, 16) || !aligned(p->v_pool, 16) || !aligned(p->o, 16) ||
       !aligned(p->workspace, 16) || !aligned(p->k_mul, 4) || !aligned(p->v_mul, 4) || !aligned(p->lse, 4) ||
       !aligned(p->selected, 4) || !aligned(p->alibi_slopes, 4) || !aligned(p->prefix_lens, 4))
     return QPKV_ERR_INVALID_ARG;
-  if (p->workspace_bytes < qpkv_attend_group4_workspace_bytes(p->num_seqs, p->num_tokens, p->num_heads_q,
-                                                              p->num_heads_kv, p->head_dim))
+  if (attend_group4_needs_workspace(*p) &&
+      (p->workspace == nullptr ||
+       p->workspace_bytes < qpkv_attend_group4_workspace_bytes(p->num_seqs, p->num_tokens, p->num_heads_q,
+                                                               p->num_heads_kv, p->head_dim)))
     return QPKV_ERR_WORKSPACE_TOO_SMALL;
   qpkv_attend_group4_params w = *p;
   if (w.error_word == nullptr && (w.error_word = default_error_word()) == nullptr) return QPKV_ERR_CUDA;

@@ -94,6 +94,7 @@ constexpr int kSelectMaxPages = 1 << 18;   // pages of a table row
 cudaError_t launch_write_group4(const qpkv_write_group4_params& p, cudaStream_t stream);
 cudaError_t launch_read_group4(const qpkv_read_group4_params& p, cudaStream_t stream);
 cudaError_t launch_select_pages(const qpkv_select_pages_params& p, cudaStream_t stream);
+bool attend_group4_needs_workspace(const qpkv_attend_group4_params& p);
 size_t attend_group4_workspace_bytes(int B, int T, int Hq, int Hkv, int D);
 cudaError_t launch_attend_group4(const qpkv_attend_group4_params& p, cudaStream_t stream);
 

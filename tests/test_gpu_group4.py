@@ -375,7 +375,9 @@ CASES = [
 def test_attend_all_keys(lib, err, reqs, Hq, H, D, ps, dtype, case_kw, kw):
     c = _attend_case(Hq + D, reqs, Hq, H, D, ps, dtype, pad=3, **case_kw)
     wanted = _want_attend(c, **kw)
-    for max_q in (0, max(n for n, _ in reqs)):
+    W = c["table"].shape[1]
+    for max_q, width in ((0, W), (max(n for n, _ in reqs), W), (max(n for n, _ in reqs), 5000), (1, W)):   # a wide table: keys by the thousand
+        c["table"] = np.concatenate([c["table"][:, :W], np.full((len(reqs), max(0, width - W)), -1, np.int32)], 1)
         out = torch.full_like(c["q"], 7.0, device="cuda")
         lse = torch.full(c["q"].shape[:2], 7.0, device="cuda")
         got = _run_attend(lib, c, err, max_q=max_q, out=out, lse=lse, **kw)
@@ -606,8 +608,9 @@ def test_bindings_refuse(lib):
     for kw in (dict(selected=i32(np.zeros((4, H, 0)))), dict(selected=i32(np.zeros((3, H, 2)))), dict(workspace=pool[:, :1]), dict(v_mul=bs)):
         with pytest.raises((ValueError, TypeError)):
             lib.attend_group4(x, pool, pool, table, cu, cu, **kw)
+    wide = i32(np.zeros((1, 300)))
     with pytest.raises(lib.QpkvError):
-        lib.attend_group4(x, pool, pool, table, cu, cu, workspace=pool)
+        lib.attend_group4(x, pool, pool, wide, cu, cu, workspace=pool)
     e = torch.empty(0, H, D, dtype=torch.bfloat16, device="cuda")      # nothing to do
     none, no_table = i32([]), i32(np.zeros((0, 1)))
     lib.write_cache_group4(e, e, none, no_table, pool, pool)

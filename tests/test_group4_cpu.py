@@ -96,7 +96,7 @@ def _attend(q):
     n = q.load().qpkv_attend_group4_workspace_bytes(2, 5, 8, 2, 128)
     assert n > 0
     return _fill(q.AttendGroup4Params(), num_seqs=2, num_tokens=5, num_heads_q=8, num_heads_kv=2, head_dim=128, page_size=16,
-                 num_pages=4, bt_stride=2, num_selected=3, workspace_bytes=n)
+                 num_pages=4, bt_stride=300, num_selected=3, workspace_bytes=n)
 
 
 @pytest.mark.parametrize("change,want", SHARED + [
@@ -104,7 +104,8 @@ def _attend(q):
     (dict(logit_cap=float("inf")), INVALID), (dict(logit_cap=1e-30), INVALID), (dict(sm_scale=float("inf")), INVALID), (dict(num_selected=0), INVALID),
     (dict(num_selected=1 << 28), UNSUPPORTED), (dict(num_heads_q=7), UNSUPPORTED), (dict(num_pages=1 << 30), UNSUPPORTED),
     (dict(num_tokens=1 << 30), UNSUPPORTED), (dict(q=None), INVALID), (dict(o=FAKE + 4), INVALID), (dict(k_pool=FAKE + 8), INVALID),
-    (dict(selected=FAKE + 1), INVALID), (dict(workspace=None), INVALID), (dict(workspace=FAKE + 1), INVALID), (dict(workspace_bytes=64), SMALL)])
+    (dict(selected=FAKE + 1), INVALID), (dict(selected=None, workspace=None), SMALL), (dict(workspace=FAKE + 1), INVALID),
+    (dict(selected=None, workspace_bytes=64), SMALL), (dict(selected=None, bt_stride=2, max_seqlen_q=9, workspace=None, num_heads_q=10), SMALL)])
 def test_attend_refuses(q, change, want):
     assert _call(q.load().qpkv_attend_group4, _attend(q), **change) == want
 
