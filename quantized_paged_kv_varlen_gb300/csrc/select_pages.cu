@@ -31,7 +31,6 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxKeys = 48 * 1024;      // scores of a block in shared memory
 
 struct SelectArgs {
@@ -74,8 +73,9 @@ __device__ __forceinline__ float code_of(uint32_t half_word, float a) {
   return rintf(__fdiv_rn(to_f32<E>(half_word) * 127.f, a));
 }
 
-template <typename E, int D, int NB>
+template <typename E, int D, int NB, int kThreads>
 __global__ void __launch_bounds__(kThreads) select_pages_kernel(const __grid_constant__ SelectArgs a) {
+  constexpr int kWarps = kThreads / 32;
   constexpr int KC = D / 32;          // 16-byte chunks of a page's 2 D bounds per thread
   extern __shared__ uint32_t s_key[];
   __shared__ uint32_t s_hist[4][256], s_sum[256];
@@ -227,6 +227,7 @@ __global__ void __launch_bounds__(kThreads) select_pages_kernel(const __grid_con
   // takes keys tid * per ...: an odd number apart, so that banks differ.
   uint32_t prefix = 0;
   int need = a.n;
+#pragma unroll 1
   for (int pass = 0; pass < 4; ++pass) {
     const int shift = 24 - 8 * pass;
     for (int i = tid; i < count; i += kThreads) {
@@ -236,9 +237,11 @@ __global__ void __launch_bounds__(kThreads) select_pages_kernel(const __grid_con
     const uint32_t* sums = s_hist[pass];
     if (C > 1) {
       cluster.sync();
-      uint32_t sum = 0;
-      for (int r = 0; r < C; ++r) sum += *cluster.map_shared_rank(&s_hist[pass][tid], r);
-      s_sum[tid] = sum;
+      for (int i = tid; i < 256; i += kThreads) {
+        uint32_t sum = 0;
+        for (int r = 0; r < C; ++r) sum += *cluster.map_shared_rank(&s_hist[pass][i], r);
+        s_sum[i] = sum;
+      }
       sums = s_sum;
     }
     __syncthreads();
@@ -259,17 +262,24 @@ __global__ void __launch_bounds__(kThreads) select_pages_kernel(const __grid_con
     }
     const uint32_t reach = __ballot_sync(0xffffffffu, upto >= need);
     const int who = __ffs(reach) - 1;
-    int before = upto - mine, digit = 0;
+    int before = upto - mine, digit = 0, in_bin = 0;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       if (before + bin[k] >= need) {
         digit = 255 - 8 * lane - k;
+        in_bin = bin[k];
         break;
       }
       before += bin[k];
     }
     need -= __shfl_sync(0xffffffffu, before, who);
     prefix = prefix << 8 | __shfl_sync(0xffffffffu, digit, who);
+    // a bin that is taken whole: all keys from its first on
+    if (pass < 3 && need == __shfl_sync(0xffffffffu, in_bin, who) && prefix != 0) {
+      prefix = (prefix << shift) - 1;
+      need = 0;
+      break;
+    }
     if (C > 1) __syncthreads();     // s_sum is read before it is written again
   }
 
@@ -319,9 +329,276 @@ __global__ void __launch_bounds__(kThreads) select_pages_kernel(const __grid_con
     for (int i = all.x + min(all.y, need) + tid; i < a.n; i += kThreads) out[i] = -1;
 }
 
-template <typename E, int D, int NB>
+// Prompts: a warp takes `kTok` neighbouring tokens of a sequence for one kv head,
+// 16 columns of queries at most, scores all their pages and chooses for each; the
+// warps of a block take neighbouring tiles, so that the bounds come from L1.
+// (A block a token: 4 pieces of 250 tokens over 10,000, 28 heads, 147 us.)
+constexpr int kRowWarps = 8;
+
+struct RowsArgs {
+  SelectArgs s;
+  int warps, stride;       // of a block; keys of a token
+  int tiles;
+};
+
+template <typename E, int D, int kGp>
+__global__ void __launch_bounds__(kRowWarps * 32) select_rows_kernel(const __grid_constant__ RowsArgs ra) {
+  constexpr int KC = D / 32;
+  constexpr int kTok = kGp >= 4 ? 16 / kGp : 4;
+  constexpr int NB = kGp >= 4 ? 2 : 1;
+  const SelectArgs& a = ra.s;
+  extern __shared__ uint32_t s_mem[];
+  __shared__ uint32_t s_hist[kRowWarps][256];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  uint32_t* keys = s_mem + static_cast<size_t>(warp) * kTok * ra.stride;
+  uint32_t* hist = s_hist[warp];
+  griddep_wait();
+  griddep_launch_dependents();
+  // ---- the tile: sequence b owns tiles [floor(cu[b-1] / kTok) + b, ...)
+  const int h = blockIdx.x % a.H, tile = static_cast<int>(blockIdx.x / a.H) * ra.warps + warp;
+  if (tile >= ra.tiles) return;
+  const int b = warp_last_at_most(a.B, tile, [&](int m) { return static_cast<long long>(__ldg(a.cu + m - 1)) / kTok + m; });
+  const int t0 = seq_begin(a.cu, b), n_q = __ldg(a.cu + b) - t0;
+  const int i0 = (tile - (t0 / kTok + b)) * kTok;
+  if (n_q <= 0 || i0 < 0 || i0 >= n_q) return;
+  int len = __ldg(a.lens + b);
+  if (t0 < 0 || t0 + static_cast<long long>(n_q) > a.T || len < 0 || len > static_cast<long long>(a.bt_stride) * a.ps) {
+    if (lane == 0) report_error(a.err, kDevErrBadLength);
+    len = 0;
+  }
+  const int live = min(min(kTok, n_q - i0), a.T - t0 - i0);      // (rows behind the arrays' are none)
+  if (t0 < 0 || live <= 0) return;
+  const long long at0 = static_cast<long long>(len) - n_q + i0;
+  // candidates of the tile: from its first token's first to its last token's last
+  const long long at1 = at0 + live - 1;
+  const int p_lo = a.window > 0 ? static_cast<int>(max(0ll, at0 + 1 - a.window) / a.ps) : 0;
+  const int count = len > 0 && at1 >= 0 ? static_cast<int>(at1 / a.ps) - p_lo + 1 : 0;
+  // ---- the queries: each token's largest magnitude, then c
+  const uint16_t* q = static_cast<const uint16_t*>(a.q);
+  float amax[kTok];
+#pragma unroll
+  for (int k = 0; k < kTok; ++k) {
+    uint32_t top = 0;
+    const uint4* src = reinterpret_cast<const uint4*>(q + (static_cast<size_t>(t0 + i0 + (k < live ? k : 0)) * a.Hq + h * a.G) * D);
+    for (int i = lane; i < a.G * D / 8; i += 32) {
+      const uint4 v = __ldg(src + i);
+      top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
+    }
+    amax[k] = to_f32<E>(__reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16)));
+  }
+  uint32_t qf[NB][4 * KC][2];
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    // column 8 nb + g: heads of a token side by side, copies behind the last
+    const int col = 8 * nb + g, k = min(col / kGp, kTok - 1) < live ? min(col / kGp, kTok - 1) : 0;
+    float top = amax[0];
+#pragma unroll
+    for (int x = 1; x < kTok; ++x) top = k == x ? amax[x] : top;
+    const bool scored = top > 0.f && top < INFINITY;
+    const uint16_t* qh = q + (static_cast<size_t>(t0 + i0 + k) * a.Hq + h * a.G + (col % kGp) % a.G) * D;
+#pragma unroll
+    for (int c = 0; c < KC; ++c) {
+      const int dim0 = (16 * (t + 4 * c)) % D;
+      const bool is_max = c >= KC / 2;
+#pragma unroll
+      for (int w4 = 0; w4 < 4; ++w4) {
+        const uint2 w = __ldg(reinterpret_cast<const uint2*>(qh + dim0 + 4 * w4));
+        float x[4] = {0.f, 0.f, 0.f, 0.f};
+        if (scored) {
+          x[0] = code_of<E>(w.x & 0xFFFFu, top), x[1] = code_of<E>(w.x >> 16, top);
+          x[2] = code_of<E>(w.y & 0xFFFFu, top), x[3] = code_of<E>(w.y >> 16, top);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = is_max ? fmaxf(x[e], 0.f) : fminf(x[e], 0.f);
+        qf[nb][4 * c + w4][0] = f32x2_to_f16x2(x[1], x[0]);
+        qf[nb][4 * c + w4][1] = f32x2_to_f16x2(x[3], x[2]);
+      }
+    }
+  }
+  const int32_t* bt = a.bt + static_cast<size_t>(b) * a.bt_stride + p_lo;
+  // ---- scores
+#pragma unroll 1
+  for (int j0 = 0; j0 < count; j0 += 32) {
+    int page = -1;
+    float scale = 0.f;
+    if (j0 + lane < count) {
+      page = __ldg(bt + j0 + lane);
+      if (page < 0 || page >= a.num_pages) {
+        report_error(a.err, kDevErrBadPage);
+        page = -1;
+      } else {
+        scale = __ldg(a.bscale + static_cast<size_t>(page) * a.H + h);
+      }
+    }
+#pragma unroll 1
+    for (int s = 0; s < 2; ++s) {
+      uint4 x[2][KC];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int pg = __shfl_sync(0xffffffffu, page, 16 * s + 8 * e + g);
+        const uint4* src = reinterpret_cast<const uint4*>(a.bounds + (static_cast<size_t>(pg < 0 ? 0 : pg) * a.H + h) * 2 * D) + t;
+#pragma unroll
+        for (int c = 0; c < KC; ++c) x[e][c] = pg < 0 ? make_uint4(0, 0, 0, 0) : __ldg(src + 4 * c);
+      }
+      float d[NB][4] = {};
+#pragma unroll
+      for (int c = 0; c < KC; ++c) {
+        const uint32_t w0[4] = {x[0][c].x, x[0][c].y, x[0][c].z, x[0][c].w};
+        const uint32_t w1[4] = {x[1][c].x, x[1][c].y, x[1][c].z, x[1][c].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t f[4];
+          widen<true>(w0[k], f[0], f[2]);
+          widen<true>(w1[k], f[1], f[3]);
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) mma16816(d[nb], f, qf[nb][4 * c + k][0], qf[nb][4 * c + k][1]);
+        }
+      }
+      // lane (g, t) has pages g, g + 8 of columns 2t, 2t + 1 of each eight: the largest of a token's
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float sc = __shfl_sync(0xffffffffu, scale, 16 * s + 8 * e + g);
+        const int pg = __shfl_sync(0xffffffffu, page, 16 * s + 8 * e + g), j = j0 + 16 * s + 8 * e + g;
+        auto put = [&](int k, float v) {
+          const long long at = at0 + k;
+          const int hi = static_cast<int>(at / a.ps), lo = a.window > 0 ? static_cast<int>(max(0ll, at + 1 - a.window) / a.ps) : 0;
+          const int p = p_lo + j;
+          uint32_t key = 0;
+          if (pg >= 0 && at >= 0 && p >= lo && p <= hi)
+            key = p - lo < a.first || hi - p < a.last ? 0xFFFFFFFFu : key_of(sc == INFINITY ? INFINITY : v * sc);
+          if (k < live && j < count) keys[k * ra.stride + j] = key;
+        };
+        if constexpr (kGp == 1) {
+          if (t < 2) {
+            put(2 * t, d[0][2 * e]);
+            put(2 * t + 1, d[0][2 * e + 1]);
+          }
+        } else if constexpr (kGp == 2) {
+          put(t, fmaxf(d[0][2 * e], d[0][2 * e + 1]));
+        } else {
+          float m[NB];
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            m[nb] = fmaxf(d[nb][2 * e], d[nb][2 * e + 1]);
+            m[nb] = fmaxf(m[nb], __shfl_xor_sync(0xffffffffu, m[nb], 1));
+            if constexpr (kGp >= 8) m[nb] = fmaxf(m[nb], __shfl_xor_sync(0xffffffffu, m[nb], 2));
+          }
+          if constexpr (kGp == 16) {
+            if (t == 0) put(0, fmaxf(m[0], m[1]));
+          } else if constexpr (kGp == 8) {
+            if (t < 2) put(t, t == 0 ? m[0] : m[1]);
+          } else {
+            const float m1 = __shfl_xor_sync(0xffffffffu, m[0], 3), m2 = __shfl_xor_sync(0xffffffffu, m[1], 2);
+            put(t, t == 0 ? m[0] : t == 1 ? m1 : t == 2 ? m2 : m[1]);
+          }
+        }
+      }
+    }
+  }
+  __syncwarp();
+  // ---- each token's choice
+#pragma unroll 1
+  for (int k = 0; k < live; ++k) {
+    const uint32_t* key_of_token = keys + k * ra.stride;
+    uint32_t prefix = 0;
+    int need = a.n;
+#pragma unroll 1
+    for (int pass = 0; pass < 4; ++pass) {
+      const int shift = 24 - 8 * pass;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) hist[32 * i + lane] = 0;
+      __syncwarp();
+      for (int i = lane; i < count; i += 32) {
+        const uint32_t key = key_of_token[i];
+        if (key != 0 && (pass == 0 || key >> (shift + 8) == prefix)) atomicAdd(&hist[key >> shift & 255], 1u);
+      }
+      __syncwarp();
+      int bin[8], mine = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) mine += bin[i] = static_cast<int>(hist[255 - 8 * lane - i]);
+      int upto = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += u;
+      }
+      __syncwarp();
+      if (pass == 0 && __shfl_sync(0xffffffffu, upto, 31) <= a.n) {   // all of them
+        prefix = 0;
+        need = 0;
+        break;
+      }
+      const int who = __ffs(__ballot_sync(0xffffffffu, upto >= need)) - 1;
+      int before = upto - mine, digit = 0, in_bin = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (before + bin[i] >= need) {
+          digit = 255 - 8 * lane - i;
+          in_bin = bin[i];
+          break;
+        }
+        before += bin[i];
+      }
+      need -= __shfl_sync(0xffffffffu, before, who);
+      prefix = prefix << 8 | __shfl_sync(0xffffffffu, digit, who);
+      if (pass < 3 && need == __shfl_sync(0xffffffffu, in_bin, who) && prefix != 0) {   // a bin taken whole
+        prefix = (prefix << shift) - 1;
+        need = 0;
+        break;
+      }
+    }
+    int32_t* out = a.out + (static_cast<size_t>(t0 + i0 + k) * a.H + h) * a.n;
+    int done = 0;
+    for (int i0k = 0; i0k < count; i0k += 32) {
+      const uint32_t key = i0k + lane < count ? key_of_token[i0k + lane] : 0;
+      const uint32_t eq = __ballot_sync(0xffffffffu, key == prefix && key != 0);
+      const int rank = __popc(eq & ((1u << lane) - 1));       // of those that equal the n-th
+      const bool take = key > prefix || (eq >> lane & 1 && rank < need);
+      const uint32_t taken = __ballot_sync(0xffffffffu, take);
+      if (take) out[done + __popc(taken & ((1u << lane) - 1))] = p_lo + i0k + lane;
+      need -= min(need, __popc(eq));
+      done += __popc(taken);
+    }
+    for (int i = done + lane; i < a.n; i += 32) out[i] = -1;
+    __syncwarp();
+  }
+}
+
+template <typename E, int D, int kGp>
+cudaError_t go_rows(RowsArgs r, cudaStream_t stream) {
+  constexpr int kTok = kGp >= 4 ? 16 / kGp : 4;
+  auto kernel = select_rows_kernel<E, D, kGp>;
+  r.tiles = r.s.T / kTok + r.s.B;
+  const size_t smem = static_cast<size_t>(r.warps) * kTok * r.stride * 4;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxKeys * 4);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((r.tiles + r.warps - 1) / r.warps) * r.s.H);
+  cfg.blockDim = dim3(r.warps * 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, r);
+}
+
+template <typename E, int D>
+cudaError_t pick_rows(const RowsArgs& r, int gp, cudaStream_t s) {
+  switch (gp) {
+    case 1: return go_rows<E, D, 1>(r, s);
+    case 2: return go_rows<E, D, 2>(r, s);
+    case 4: return go_rows<E, D, 4>(r, s);
+    case 8: return go_rows<E, D, 8>(r, s);
+    default: return go_rows<E, D, 16>(r, s);
+  }
+}
+
+template <typename E, int D, int NB, int kThreads>
 cudaError_t go(const SelectArgs& a, int C, cudaStream_t stream) {
-  auto kernel = select_pages_kernel<E, D, NB>;
+  auto kernel = select_pages_kernel<E, D, NB, kThreads>;
   const size_t smem = static_cast<size_t>((a.bt_stride + C - 1) / C) * 4;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxKeys * 4);
   if (e != cudaSuccess) return e;
@@ -341,10 +618,13 @@ cudaError_t go(const SelectArgs& a, int C, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-template <typename E>
-cudaError_t pick(const SelectArgs& a, int D, int C, cudaStream_t s) {
-  if (D == 64) return a.G <= 8 ? go<E, 64, 1>(a, C, s) : go<E, 64, 2>(a, C, s);
-  return a.G <= 8 ? go<E, 128, 1>(a, C, s) : go<E, 128, 2>(a, C, s);
+template <typename E, int D>
+cudaError_t pick(const SelectArgs& a, int C, cudaStream_t s) {
+#ifndef V_T
+#define V_T 128
+#endif
+  if (C > 1) return a.G <= 8 ? go<E, D, 1, 256>(a, C, s) : go<E, D, 2, 256>(a, C, s);
+  return a.G <= 8 ? go<E, D, 1, V_T>(a, C, s) : go<E, D, 2, V_T>(a, C, s);
 }
 
 }  // namespace
@@ -361,7 +641,22 @@ cudaError_t launch_select_pages(const qpkv_select_pages_params& p, cudaStream_t 
   const long long rows = static_cast<long long>(a.T) * a.H;
   int C = 1;
   while (C < 8 && ((rows * C * 2 <= 2 * 152 && a.bt_stride / (2 * C) >= 64) || (a.bt_stride + C - 1) / C > kMaxKeys)) C *= 2;
-  return p.dtype == QPKV_DTYPE_F16 ? pick<__half>(a, p.head_dim, C, stream) : pick<__nv_bfloat16>(a, p.head_dim, C, stream);
+  const bool f16 = p.dtype == QPKV_DTYPE_F16;
+  // several queries a sequence, enough of them, and a warp's keys in shared memory
+  int gp = 1;
+  while (gp < a.G) gp *= 2;
+  const int tok = gp >= 4 ? 16 / gp : 4;
+  if (gp <= 16 && p.max_seqlen_q != 1 && a.T >= 2 * a.B && rows >= 2 * 152 * tok && a.bt_stride * tok <= kMaxKeys) {
+    RowsArgs r;
+    r.s = a;
+    r.stride = a.bt_stride;
+    r.warps = kRowWarps;
+    while (r.warps > 1 && r.warps * tok * r.stride > kMaxKeys) r.warps /= 2;
+    if (p.head_dim == 64) return f16 ? pick_rows<__half, 64>(r, gp, stream) : pick_rows<__nv_bfloat16, 64>(r, gp, stream);
+    return f16 ? pick_rows<__half, 128>(r, gp, stream) : pick_rows<__nv_bfloat16, 128>(r, gp, stream);
+  }
+  if (p.head_dim == 64) return f16 ? pick<__half, 64>(a, C, stream) : pick<__nv_bfloat16, 64>(a, C, stream);
+  return f16 ? pick<__half, 128>(a, C, stream) : pick<__nv_bfloat16, 128>(a, C, stream);
 }
 
 }  // namespace qpkv

@@ -238,7 +238,10 @@ def _want_select(c, n, **kw):
     ([(5, 900), (0, 50), (3, 3), (7, 400)], 14, 2, 128, 32, "bf16", 7, dict(last=2)), ([(1, 9000), (2, 5000)], 10, 2, 64, 16, "f16", 64, dict(first=4, last=4)),
     ([(1, 3000)], 24, 2, 64, 48, "bf16", 8, {}), ([(4, 1500)], 33, 1, 128, 16, "bf16", 9, dict(first=1)), ([(3, 2000)], 16, 8, 64, 64, "bf16", 11, {}),
     ([(40, 1000), (90, 90)], 8, 2, 128, 16, "bf16", 10, dict(window=300, first=1)), ([(30, 20)], 2, 2, 64, 16, "bf16", 3, {}),
-    ([(1, 40000)], 4, 1, 64, 16, "bf16", 300, dict(window=20011)), ([(1, 2500)], 2, 1, 128, 16, "f16", 200, {}), ([(130, 2000)], 7, 1, 128, 128, "f16", 4, {})])
+    ([(1, 40000)], 4, 1, 64, 16, "bf16", 300, dict(window=20011)), ([(1, 2500)], 2, 1, 128, 16, "f16", 200, {}), ([(130, 2000)], 7, 1, 128, 128, "f16", 4, {}),
+    ([(700, 900), (0, 9), (3, 40), (500, 450)], 8, 8, 64, 16, "bf16", 5, dict(first=1)), ([(401, 2000), (398, 1200)], 8, 4, 128, 16, "bf16", 9, dict(window=250, last=2)),
+    ([(650, 650)], 8, 2, 64, 32, "f16", 6, {}), ([(350, 1800), (60, 61)], 21, 3, 128, 16, "bf16", 20, dict(first=2)),
+    ([(330, 1000)], 26, 2, 64, 16, "f16", 12, {})])
 @pytest.mark.parametrize("extreme", [False, True])
 def test_select_pages(lib, err, reqs, Hq, H, D, ps, dtype, n, kw, extreme):
     c = _select_case(len(reqs) + n, reqs, Hq, H, D, ps, dtype, pad=2, extreme=extreme)
