@@ -31,6 +31,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 
+constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxKeys = 48 * 1024;      // scores of a block in shared memory
 
 struct SelectArgs {
@@ -192,15 +193,8 @@ struct Search {
   }
 };
 
-#ifndef V_T
-#define V_T 256
-#define V_AO 4
-#define V_AU 1
-#endif
-constexpr int kAUnroll = V_AU;
-template <typename E, int D, int NB, int kThreads>
-__global__ void __launch_bounds__(kThreads, NB == 1 && D == 128 ? V_AO : 1) select_pages_kernel(const __grid_constant__ SelectArgs a) {
-  constexpr int kWarps = kThreads / 32;
+template <typename E, int D, int NB>
+__global__ void __launch_bounds__(kThreads, NB == 1 && D == 128 ? 4 : 1) select_pages_kernel(const __grid_constant__ SelectArgs a) {
   constexpr int KC = D / 32;          // 16-byte chunks of a page's 2 D bounds per thread
   extern __shared__ uint32_t s_key[];
   __shared__ uint32_t s_hist[4][256], s_sum[256];
@@ -282,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, NB == 1 && D == 128 ? V_AO : 1) sele
           scale = __ldg(a.bscale + static_cast<size_t>(page) * a.H + h);
         }
       }
-#pragma unroll kAUnroll
+#pragma unroll 1
       for (int s = 0; s < 2; ++s) {
         uint4 x[2][KC];
 #pragma unroll
@@ -457,7 +451,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 4) select_rows_kernel(const __
   griddep_launch_dependents();
   // ---- the tile: sequence b owns tiles [floor(cu[b-1] / kBlockTok) + b, ...)
   const int h = blockIdx.x % a.H, tile = blockIdx.x / a.H;
-  const int b = warp_last_at_most(a.B, tile, [&](int m) { return static_cast<long long>(__ldg(a.cu + m - 1)) / kBlockTok + m; });
+  const int b = warp_last_at_most(a.B, tile, [&](int m) { return static_cast<long long>(__ldg(a.cu + m - 1) / kBlockTok) + m; });
   const int t0 = seq_begin(a.cu, b), n_q = __ldg(a.cu + b) - t0;
   const int first = (tile - (t0 / kBlockTok + b)) * kBlockTok;
   if (n_q <= 0 || t0 < 0 || first < 0 || first >= n_q) return;
@@ -695,9 +689,9 @@ cudaError_t pick_rows(const RowsArgs& r, int gp, cudaStream_t s) {
   }
 }
 
-template <typename E, int D, int NB, int kThreads>
+template <typename E, int D, int NB>
 cudaError_t go(const SelectArgs& a, int C, cudaStream_t stream) {
-  auto kernel = select_pages_kernel<E, D, NB, kThreads>;
+  auto kernel = select_pages_kernel<E, D, NB>;
   const size_t smem = static_cast<size_t>((a.bt_stride + C - 1) / C) * 4;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxKeys * 4);
   if (e != cudaSuccess) return e;
@@ -719,8 +713,7 @@ cudaError_t go(const SelectArgs& a, int C, cudaStream_t stream) {
 
 template <typename E, int D>
 cudaError_t pick(const SelectArgs& a, int C, cudaStream_t s) {
-  if (C > 1) return a.G <= 8 ? go<E, D, 1, 256>(a, C, s) : go<E, D, 2, 256>(a, C, s);
-  return a.G <= 8 ? go<E, D, 1, V_T>(a, C, s) : go<E, D, 2, V_T>(a, C, s);
+  return a.G <= 8 ? go<E, D, 1>(a, C, s) : go<E, D, 2>(a, C, s);
 }
 
 }  // namespace

@@ -7,12 +7,13 @@
 // and per page and channel the bounds floor(min / u), ceil(max / u) of the keys
 // as they read back.
 //
-// Divisions are IEEE float32.  y / s is done as q = y r, q' = q + (y - q s) r
-// with r = 1 / s rounded (Markstein's correction; y - q s is exact in one fma):
-// q' is the rounded quotient wherever that could matter.  s has 4 significant
-// bits and the codes' midpoints m at most 3, so m s is a float32 and a y that is
-// not m s is off by a step of its own, which keeps y / s further from m than
-// 0.9 of half a step of the quotient; q' is good to half a step and 2^-46.
+// Divisions are IEEE float32 by definition.  y / s is done as q = y r, q' = q + (y -
+// q s) r with r near 1 / s (Markstein's correction; y - q s is exact in one fma):
+// q' gives the code of the rounded quotient.  s has 4 significant bits and the
+// codes' midpoints m at most 3, so m s is a float32, at which q' is exactly m; any
+// other y is off by a step of its own or more, which takes y / s further from m
+// than 1.07 half steps of float32, and q' is good to half a step and 2^-22 of one.
+// amax / 6 the same, with the midpoints of E4M3 (5 bits).
 //
 // HBM-bound: 2 bytes in and 9/16 out per element.  A thread takes 16 channels of
 // a token: one scale, 8 bytes of codes.  What one call adds to a page of a
@@ -44,6 +45,7 @@ struct WriteArgs {
   int8_t* bounds;
   float* bscale;
   int* err;
+  int k_wide, v_wide;        // rows of 16 channels lie on 32 bytes
   int hblocks, heads;        // blocks of a piece's heads, heads of each
   int kv_blocks;             // the first blocks; the others rotate q
   int q_splits, q_heads;     // blocks of a token tile's heads, heads of each
@@ -67,20 +69,51 @@ __device__ __forceinline__ uint32_t f32_pair(float lo, float hi) {
   }
 }
 
+// max(|a|, |b|, |c|) of values of which none or any is NaN: then NaN.
+__device__ __forceinline__ float absmax3(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(fabsf(a)), "f"(fabsf(b)), "f"(fabsf(c)));
+  return d;
+}
+
+// 32 bytes by one access where they lie on 32, else by two.
+__device__ __forceinline__ void load32(const void* p, bool wide, uint4& a, uint4& b) {
+  if (wide) {
+    asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+                 : "l"(p));
+  } else {
+    a = __ldg(static_cast<const uint4*>(p));
+    b = __ldg(static_cast<const uint4*>(p) + 1);
+  }
+}
+__device__ __forceinline__ void store32(void* p, bool wide, const uint32_t (&v)[8]) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]),
+                 "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  } else {
+    static_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    static_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+}
+
 // 16 channels -> codes and scale.
 __device__ __forceinline__ uint2 encode16(const float (&x)[16], uint32_t* scale) {
-  uint32_t top = 0;     // magnitudes are ordered like their bits, NaN above infinity
-#pragma unroll
-  for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-  if (top >= 0x7F800000u) {
+  const float top = absmax3(absmax3(absmax3(x[0], x[1], x[2]), absmax3(x[3], x[4], x[5]), absmax3(x[6], x[7], x[8])),
+                            absmax3(x[9], x[10], x[11]), absmax3(absmax3(x[12], x[13], x[14]), x[15], 0.f));
+  if (!(top < INFINITY)) {
     *scale = 0x7Fu;
     return make_uint2(0, 0);
   }
-  const uint32_t code = f32x2_to_e4m3x2(0.f, __fdiv_rn(__uint_as_float(top), 6.f)) & 0xFFu;
+  constexpr float sixth = 1.f / 6.f;
+  const float t0 = top * sixth;
+  const uint32_t code = f32x2_to_e4m3x2(0.f, fmaf(fmaf(-t0, 6.f, top), sixth, t0)) & 0xFFu;
   *scale = code;
   const float s = e4m3_to_f32(static_cast<uint8_t>(code));
   if (s == 0.f) return make_uint2(0, 0);
-  const float r = __frcp_rn(s);
+  float r;      // good to 2^-23: the correction makes up for it
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
   float y[2][8];
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
@@ -168,7 +201,7 @@ __device__ __forceinline__ void rotate_q(const WriteArgs& a, int block) {
 }
 
 template <typename E, int D>
-__global__ void __launch_bounds__(kThreads) write_group4_kernel(const __grid_constant__ WriteArgs a) {
+__global__ void __launch_bounds__(kThreads, 6) write_group4_kernel(const __grid_constant__ WriteArgs a) {
   using L = Group4<D>;
   constexpr int TPR = D / 16;                 // threads of a token
   constexpr int R = kThreads / TPR;           // tokens of a round
@@ -176,15 +209,16 @@ __global__ void __launch_bounds__(kThreads) write_group4_kernel(const __grid_con
   __shared__ uint32_t s_top[4];
   griddep_wait();
   griddep_launch_dependents();
-  if (static_cast<int>(blockIdx.x) >= a.kv_blocks) {
-    rotate_q<E, D>(a, blockIdx.x - a.kv_blocks);
+  const int block_no = blockIdx.x;
+  if (block_no >= a.kv_blocks) {
+    rotate_q<E, D>(a, block_no - a.kv_blocks);
     return;
   }
   // blocks of a page's heads lie side by side, K before V
-  const int which = blockIdx.x / a.hblocks, hblock = blockIdx.x - which * a.hblocks;
+  const int which = block_no / a.hblocks, hblock = block_no - which * a.hblocks;
   const bool is_v = which & 1;
   const int item = which >> 1, ps = a.ps, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int b = warp_last_at_most(a.B, item, [&](int m) { return static_cast<long long>(__ldg(a.cu + m - 1)) / ps + 2ll * m; });
+  const int b = warp_last_at_most(a.B, item, [&](int m) { return static_cast<long long>(__ldg(a.cu + m - 1) / ps) + 2ll * m; });
   const int t0 = seq_begin(a.cu, b), t1 = __ldg(a.cu + b);
   const int start = a.start != nullptr ? __ldg(a.start + b) : 0;
   const int nth = item - (t0 / ps + 2 * b);             // which page of the sequence's new tokens
@@ -223,32 +257,51 @@ __global__ void __launch_bounds__(kThreads) write_group4_kernel(const __grid_con
   const int from = bounds ? 0 : o0 / R * R;
   const float* muls = is_v ? a.v_mul : a.k_mul;
   const int h0 = hblock * a.heads, h1 = min(a.H, h0 + a.heads);
-  for (int h = h0; h < h1; ++h) {
-    uint8_t* pool = (is_v ? a.v_pool : a.k_pool) + (static_cast<size_t>(page) * a.H + h) * (ps / 16) * L::kBlock;
-    const E* src = src0 + h * sh;
+  // a round's inputs, loaded while the one before is worked on: new tokens' values,
+  // kept tokens' codes and scales
+  const bool wide = is_v ? a.v_wide : a.k_wide;
+  struct In {
+    uint4 x0, x1;
+    uint2 codes;
+    uint32_t scale;
+  };
+  const size_t head_bytes = static_cast<size_t>(ps / 16) * L::kBlock;
+  uint8_t* pool = (is_v ? a.v_pool : a.k_pool) + (static_cast<size_t>(page) * a.H + h0) * head_bytes;
+  // slot r + row lies in block r / 16 (and one on, for the upper half of 32)
+  const int codes_off = (row >> 4) * L::kBlock + (row & 15) * L::kRow + 8 * g;
+  const int scale_off = (row >> 4) * L::kBlock + L::kScaleAt + (row & 15) * L::kScales + g;
+  const E* src_row = src0 + (tok0 + from + row) * st;      // of the round that is loaded next
+  auto load = [&](const E* src, const uint8_t* base, int r) {
+    In in = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0), make_uint2(0, 0), 0};
+    const int slot = r + row;
+    if (slot >= o0 && slot < end) {
+      load32(src, wide, in.x0, in.x1);
+    } else if (bounds && slot < o0) {
+      const uint8_t* block = base + (r >> 4) * L::kBlock;
+      in.codes = *reinterpret_cast<const uint2*>(block + codes_off);
+      in.scale = block[scale_off];
+    }
+    return in;
+  };
+  const E* src_h = src_row + h0 * sh;
+  In in = load(src_h, pool, from);
+  for (int h = h0; h < h1; ++h, pool += head_bytes) {
     const float mul = muls != nullptr ? __ldg(muls + h) : 1.f;
     uint32_t mn[8], mx[8], nan = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) mn[i] = 0x7C007C00u, mx[i] = 0xFC00FC00u;
+    const E* src = src_h;
+    src_h += sh;
     for (int r = from; r < end; r += R) {
       const int slot = r + row;
       const bool fresh = slot >= o0 && slot < end, kept = bounds && slot < o0;
-      uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
-      if (fresh) {
-        const uint4* p = reinterpret_cast<const uint4*>(src + (tok0 + slot) * st);
-        x0 = __ldg(p);
-        x1 = __ldg(p + 1);
-      }
-      uint8_t* block = pool + (slot >> 4) * L::kBlock;
-      uint2* codes_at = reinterpret_cast<uint2*>(block + (slot & 15) * L::kRow + 8 * g);
-      uint8_t* scale_at = block + L::kScaleAt + (slot & 15) * L::kScales + g;
-      uint2 codes = make_uint2(0, 0);
-      uint32_t scale = 0;
-      if (kept) {
-        codes = *codes_at;
-        scale = *scale_at;
-      }
-      const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+      const In now = in;
+      src += R * st;
+      if (r + R < end) in = load(src, pool, r + R);
+      else if (h + 1 < h1) in = load(src_h, pool + head_bytes, from);
+      uint2 codes = now.codes;
+      uint32_t scale = now.scale;
+      const uint32_t w[8] = {now.x0.x, now.x0.y, now.x0.z, now.x0.w, now.x1.x, now.x1.y, now.x1.z, now.x1.w};
       float x[16];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -277,13 +330,25 @@ __global__ void __launch_bounds__(kThreads) write_group4_kernel(const __grid_con
         }
       }
       if (muls != nullptr) {
+        if (mul > 0x1p-100f && mul < 0x1p100f) {
+          // x / mul, rounded: two of Markstein's corrections, as mul has 24 significant bits.
+          // (Where they underflow the group is zero beside its scale's smallest step.)
+          const float r = __frcp_rn(mul);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = __fdiv_rn(x[i], mul);
+          for (int i = 0; i < 16; ++i) {
+            const float q0 = x[i] * r, q1 = fmaf(fmaf(-q0, mul, x[i]), r, q0);
+            x[i] = fmaf(fmaf(-q1, mul, x[i]), r, q1);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[i] = __fdiv_rn(x[i], mul);
+        }
       }
       if (fresh) {
         codes = encode16(x, &scale);
-        *codes_at = codes;
-        *scale_at = static_cast<uint8_t>(scale);
+        uint8_t* block = pool + (r >> 4) * L::kBlock;
+        *reinterpret_cast<uint2*>(block + codes_off) = codes;
+        block[scale_off] = static_cast<uint8_t>(scale);
       }
       if (bounds && (fresh || kept)) {
         if (e4m3_is_nan(scale)) {
@@ -400,6 +465,7 @@ __global__ void __launch_bounds__(kThreads) read_group4_kernel(const __grid_cons
   const size_t step = static_cast<size_t>(blocks) * L::kBlock;
   E* out = static_cast<E*>(is_v ? a.v_out : a.k_out) + (static_cast<size_t>(tok) * a.H + h0) * D + 16 * g;
   const float* muls = is_v ? a.v_mul : a.k_mul;
+  const bool wide = reinterpret_cast<uintptr_t>(is_v ? a.v_out : a.k_out) % 32 == 0;
 #pragma unroll 4
   for (int h = h0; h < h1; ++h, block += step, out += D) {
     const uint2 codes = __ldg(reinterpret_cast<const uint2*>(block + (slot & 15) * L::kRow + 8 * g));
@@ -414,9 +480,7 @@ __global__ void __launch_bounds__(kThreads) read_group4_kernel(const __grid_cons
       const float2 v = pair_f32<__half>(f[i >> 2][i & 3]);
       o[i] = f32_pair<E>(v.x * s * mul, v.y * s * mul);     // code times scale is exact
     }
-    uint4* to = reinterpret_cast<uint4*>(out);
-    to[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    to[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    store32(out, wide, o);
   }
 }
 
@@ -450,14 +514,20 @@ cudaError_t launch_write_group4(const qpkv_write_group4_params& p, cudaStream_t 
   a.k_pool = static_cast<uint8_t*>(p.k_pool), a.v_pool = static_cast<uint8_t*>(p.v_pool);
   a.bounds = static_cast<int8_t*>(p.k_bounds), a.bscale = p.bound_scale;
   a.err = p.error_word;
-  // heads one after another in a block while every SM keeps eight blocks
+  auto wide = [](const void* x, long long t, long long h) {
+    return reinterpret_cast<uintptr_t>(x) % 32 == 0 && t % 16 == 0 && h % 16 == 0;
+  };
+  a.k_wide = wide(p.k, a.ks_t, a.ks_h), a.v_wide = wide(p.v, a.vs_t, a.vs_h);
+  // two heads one after another in a block while every SM keeps eight blocks (8
+  // prompts, 18,803 tokens of 8 heads: K and V alone 49 us with one head, 46 with
+  // two, 52 with four, whose blocks make two waves); eight of q (all: 79 us)
   const long long pieces = (a.T / a.ps + 2ll * a.B) * 2;
-  a.heads = 8;
+  a.heads = 2;
   while (a.heads > 1 && (a.H < a.heads || pieces * (a.H / a.heads) < 152 * 8)) a.heads /= 2;
   a.hblocks = (a.H + a.heads - 1) / a.heads;
   a.kv_blocks = static_cast<int>(pieces * a.hblocks);
   const int R = kThreads / (p.head_dim / 16), tiles = (a.T + R - 1) / R;
-  a.q_heads = 16;
+  a.q_heads = 8;
   while (a.q_heads > 1 && (a.Hq < a.q_heads || static_cast<long long>(tiles) * (a.Hq / a.q_heads) < 152 * 4)) a.q_heads /= 2;
   a.q_splits = a.Hq > 0 ? (a.Hq + a.q_heads - 1) / a.q_heads : 0;
   const long long grid = a.kv_blocks + static_cast<long long>(tiles) * a.q_splits;
