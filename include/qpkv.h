@@ -988,9 +988,8 @@ qpkv_status qpkv_select_pages(const qpkv_select_pages_params* params, void* stre
  * twice counts twice.  A NaN scale makes NaN what sees its token: a K scale the
  * whole row, a V scale the 16 channels; rows that do not see the token are not
  * touched by it.
- * Calls with `selected`, and those with bt_stride * page_size <= 4096 and at most
- * 24 query rows of a (sequence, kv head) by max_seqlen_q, use no workspace: it may
- * be NULL (elsewhere that is WORKSPACE_TOO_SMALL).  UNSUPPORTED too: num_pages *
+ * Calls with `selected` use no workspace, nor do some on short caches: it may be
+ * NULL (WORKSPACE_TOO_SMALL where one is needed).  UNSUPPORTED too: num_pages *
  * Hkv * page_size / 16 above 2^31 - 1; with `selected` T * Hq or num_selected *
  * page_size above that. */
 typedef struct qpkv_attend_group4_params {

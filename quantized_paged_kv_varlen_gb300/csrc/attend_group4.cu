@@ -87,13 +87,13 @@ __device__ __forceinline__ Span span_of(const Page8Args& a, int tile, int b, int
 // and the ring gets what shared memory the warps leave.
 template <int D, int NB>
 struct Shape {
-  static constexpr int kBlocks = NB <= 2 ? 3 : 2;
-  static constexpr int kPair = NB == 1 ? 2 : 1;       // groups of a step
-  static constexpr int kStages = NB == 1 ? 2 : 4;
+  static constexpr int kBlocks = NB == 1 ? 4 : NB == 2 ? 3 : 2;
+  static constexpr int kPair = 2;       // groups of a step
+  static constexpr int kStages = 2;
   static constexpr int kBlock = Group4<D>::kBlock;
   static constexpr int kStage = 2 * kPair * kBlock;  // K and V of its groups
   // three tiles keep the query fragments, each lane's own, in shared memory
-  static constexpr bool kQShared = NB == 3;
+  static constexpr bool kQShared = NB >= 2;
   static constexpr int kQBytes = kQShared ? NB * (D / 16) * 32 * 8 : 0;
   static constexpr int kWarpBytes = kStages * kStage;
   static constexpr int kBytes = kWarps * (kWarpBytes + kQBytes) + 1024;
@@ -853,7 +853,6 @@ constexpr int kBlocks[3] = {Shape<128, 1>::kBlocks, Shape<128, 2>::kBlocks, Shap
 
 // Calls whose rows have few keys by what the host knows: lists, and caches whose
 // table rows are short, with few query rows.
-constexpr int kWholeKeys = 4096;
 struct Whole {
   long long tasks;     // 0: not such a call
   int nt, tile, cluster;
@@ -866,13 +865,16 @@ Whole whole_plan(const qpkv_attend_group4_params& p, int sms) {
                                 : static_cast<long long>(p.bt_stride) * p.page_size;
   const int max_q = p.max_seqlen_q > 0 && p.max_seqlen_q < p.num_tokens ? p.max_seqlen_q : p.num_tokens;
   const long long rows = listed ? G : static_cast<long long>(max_q) * G;
-  if (!listed && (keys > kWholeKeys || rows > kSplitRows)) return w;
+  if (!listed && rows > kSplitRows) return w;
   w.tile = 8 * (rows <= 8 ? 1 : rows <= 16 ? 2 : 3);
   w.nt = static_cast<int>((rows + w.tile - 1) / w.tile);
   w.tasks = static_cast<long long>(listed ? p.num_tokens : p.num_seqs) * p.num_heads_kv * w.nt;
-  // blocks of a task while the SMs have room for three and a warp two steps
+  // blocks of a task while the SMs have room for them and a warp two steps
   w.cluster = 1;
   while (w.cluster < 8 && w.tasks * w.cluster * 2 <= 3ll * sms && keys / 16 >= 2 * w.cluster * kWarps * 2) w.cluster *= 2;
+  // all keys: a warp's share is 16 groups at most (32 requests of 2,500 tokens with
+  // three drafts, 64 groups a warp: 70 us, in the split form 34)
+  if (!listed && keys > 16ll * 16 * w.cluster * kWarps) w.tasks = 0;
   return w;
 }
 
@@ -891,7 +893,12 @@ size_t attend_group4_workspace_bytes(int B, int T, int Hq, int Hkv, int D) {
   return n > most ? n : most;
 }
 
-bool attend_group4_needs_workspace(const qpkv_attend_group4_params& p) { return whole_plan(p, 152).tasks == 0; }
+static int attend_sms() {
+  const int sms = sm_count();
+  return sms > kAttendMaxSms ? kAttendMaxSms : sms;
+}
+
+bool attend_group4_needs_workspace(const qpkv_attend_group4_params& p) { return whole_plan(p, attend_sms()).tasks == 0; }
 
 cudaError_t launch_attend_group4(const qpkv_attend_group4_params& p, cudaStream_t stream) {
   SplitArgs a;
@@ -912,8 +919,7 @@ cudaError_t launch_attend_group4(const qpkv_attend_group4_params& p, cudaStream_
   x.k = static_cast<const uint8_t*>(p.k_pool), x.v = static_cast<const uint8_t*>(p.v_pool);
   x.o = p.o, x.lse = p.lse, x.err = p.error_word;
   a.sel = p.selected, a.n_sel = p.num_selected;
-  int sms = sm_count();
-  if (sms > kAttendMaxSms) sms = kAttendMaxSms;
+  const int sms = attend_sms();
   const bool f16 = p.dtype == QPKV_DTYPE_F16;
   const Whole whole = whole_plan(p, sms);
   a.tasks = whole.tasks, a.nt = whole.nt, a.cluster = whole.cluster;

@@ -448,7 +448,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
     constexpr int kVecs = kN * kRowVecs / kLoad;     // vectors of a tile per thread
     constexpr int kRowsPer = kLoad / kRowVecs;       // rows of one round, a multiple of 8:
                                                      // the swizzles are the same in every round
-    const int row0 = tid / kRowVecs, c = tid % kRowVecs;
+    // (4 bits, D = 128: eight lanes in a row are two vectors of one 64-column half of
+    // four rows, whose chunks cover all banks when they are stored)
+    constexpr bool kMix = kFmt == kE2m1 && D == 128;
+    const int row0 = kMix ? (tid >> 1 & 3) | tid >> 4 << 2 : tid / kRowVecs;
+    const int c = kMix ? (tid & 1) | (tid >> 3 & 1) << 1 : tid % kRowVecs;
     const uint32_t in0 = D == 128 ? row0 * 128 + (((c ^ row0) & 7) << 4) : row0 * 64 + (((c ^ (row0 >> 1)) & 3) << 4);
     // A vector's 16 codes are two 16-byte chunks of f16; the lanes of the second
     // 64-column half store theirs in the other order, so that the eight lanes of
@@ -474,10 +478,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
         *reinterpret_cast<uint4*>(dst + off1 + k * kRowsPer * 128) = make_uint4(o[4], o[5], o[6], o[7]);
       }
     };
-    // 4 bits: a vector's 32 codes are four chunks, with two scales.  The lanes of the
-    // second 64-column half take them in the order 2, 3, 0, 1: two rows' lanes
-    // then cover all banks.
-    const int half4 = c >> 1, swap4 = 2 * half4;
+    // 4 bits: a vector's 32 codes are four chunks, with two scales
+    const uint32_t off4 = (c >> 1) * kHalfKv + row0 * 128 + (((4 * (c & 1)) ^ (row0 & 7)) << 4);
     [[maybe_unused]] auto store4 = [&](uint8_t* dst, const uint8_t* src, const Step& s, bool all, int step, bool is_v) {
 #pragma unroll
       for (int k = 0; k < kVecs; ++k) {
@@ -486,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
         uint4 w = *reinterpret_cast<const uint4*>(block + (r & 15) * Group4<D>::kRow + 16 * c);
         uint32_t sc = *reinterpret_cast<const uint16_t*>(block + Group4<D>::kScaleAt + (r & 15) * Group4<D>::kScales + 2 * c);
         if (!all && (s.j0 + r >= s.len || s.at[r >> 4] < 0)) w = make_uint4(0, 0, 0, 0), sc = 0;
-        if (is_v && __builtin_expect(e4m3_is_nan(sc) || e4m3_is_nan(sc >> 8), 0)) {
+        if (is_v && __builtin_expect(((sc & 0x7F7Fu) + 0x0101u) & 0x8080u, 0)) {      // a scale is NaN
           const int bits = (e4m3_is_nan(sc) ? 1 : 0) | (e4m3_is_nan(sc >> 8) ? 2 : 0);
           uint32_t* word = reinterpret_cast<uint32_t*>(sh.v_nan[step % kSteps]) + (r >> 2);
           atomicOr(word, static_cast<uint32_t>(bits) << (2 * c + 8 * (r & 3)));
@@ -495,17 +497,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
         }
         const uint32_t both = e4m3x2_to_f16x2(static_cast<uint16_t>(sc));
         const uint32_t s0 = __byte_perm(both, 0, 0x1010), s1 = __byte_perm(both, 0, 0x3232);
-        if (swap4) w = make_uint4(w.z, w.w, w.x, w.y);
         const uint32_t words[4] = {w.x, w.y, w.z, w.w};
-        uint8_t* out = dst + half4 * kHalfKv + r * 128;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           uint32_t o[4];
           e2m1x8_to_f16(words[i], o);
-          const uint32_t f = (i >> 1) == (swap4 >> 1) ? s0 : s1;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[e] = f16x2_mul(o[e], f);
-          *reinterpret_cast<uint4*>(out + ((((4 * (c & 1) + (i ^ swap4)) ^ r) & 7) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+          for (int e = 0; e < 4; ++e) o[e] = f16x2_mul(o[e], i < 2 ? s0 : s1);
+          *reinterpret_cast<uint4*>(dst + (off4 ^ (i << 4)) + k * kRowsPer * 128) = make_uint4(o[0], o[1], o[2], o[3]);
         }
       }
     };

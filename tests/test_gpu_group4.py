@@ -611,7 +611,7 @@ def test_bindings_refuse(lib):
     for kw in (dict(selected=i32(np.zeros((4, H, 0)))), dict(selected=i32(np.zeros((3, H, 2)))), dict(workspace=pool[:, :1]), dict(v_mul=bs)):
         with pytest.raises((ValueError, TypeError)):
             lib.attend_group4(x, pool, pool, table, cu, cu, **kw)
-    wide = i32(np.zeros((1, 300)))
+    wide = i32(np.zeros((1, 3000)))
     with pytest.raises(lib.QpkvError):
         lib.attend_group4(x, pool, pool, wide, cu, cu, workspace=pool)
     e = torch.empty(0, H, D, dtype=torch.bfloat16, device="cuda")      # nothing to do

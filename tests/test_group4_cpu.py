@@ -96,7 +96,7 @@ def _attend(q):
     n = q.load().qpkv_attend_group4_workspace_bytes(2, 5, 8, 2, 128)
     assert n > 0
     return _fill(q.AttendGroup4Params(), num_seqs=2, num_tokens=5, num_heads_q=8, num_heads_kv=2, head_dim=128, page_size=16,
-                 num_pages=4, bt_stride=300, num_selected=3, workspace_bytes=n)
+                 num_pages=4, bt_stride=3000, num_selected=3, workspace_bytes=n)
 
 
 @pytest.mark.parametrize("change,want", SHARED + [
