@@ -839,7 +839,8 @@ qpkv_status qpkv_attend_page8(const qpkv_attend_page8_params* params, void* stre
  * to its type.  For each 16 channels x of a token, x / mul first where given,
  *   s = E4M3(min(448, amax / 6)),  code = E2M1(x / s)  (both to nearest, ties
  *   to even, divisions IEEE float32); s = 0 gives zero codes; a NaN or an
- *   infinity among the 16 gives s = NaN, which all 16 then read as.
+ *   infinity among the 16 (after rotation and division) gives s = NaN, which
+ *   all 16 then read as.
  * With k_bounds the pages written get the bounds of their cached keys (those
  * at positions below start_pos[b] + the new tokens) in units of the pool: per
  * channel floor(min / u) and ceil(max / u) with u, the smallest 2^e >= 2^-10
@@ -899,8 +900,8 @@ typedef struct qpkv_write_group4_params {
 qpkv_status qpkv_write_group4(const qpkv_write_group4_params* params, void* stream);
 
 /* Cached tokens back: row t of sequence b is the token at position
- * start_pos[b] + (t - begin_b) (start_pos NULL: zero), code * scale * mul
- * rounded once to dtype.  k_out, v_out [T, Hkv, D], contiguous; either may be
+ * start_pos[b] + (t - begin_b) (start_pos NULL: zero), code * scale (exact)
+ * times mul in float32, rounded to dtype.  k_out, v_out [T, Hkv, D], contiguous; either may be
  * NULL.  Rows of a sequence that starts at -1, of a bad page
  * (QPKV_DEV_ERR_BAD_PAGE), past the table row or with lengths that do not fit
  * (QPKV_DEV_ERR_BAD_LENGTH), and behind the last sequence are left as they are.

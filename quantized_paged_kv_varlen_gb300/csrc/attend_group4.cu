@@ -874,7 +874,7 @@ Whole whole_plan(const qpkv_attend_group4_params& p, int sms) {
   while (w.cluster < 8 && w.tasks * w.cluster * 2 <= 3ll * sms && keys / 16 >= 2 * w.cluster * kWarps * 2) w.cluster *= 2;
   // all keys: a warp's share is 16 groups at most (32 requests of 2,500 tokens with
   // three drafts, 64 groups a warp: 70 us, in the split form 34)
-  if (!listed && keys > 16ll * 16 * w.cluster * kWarps) w.tasks = 0;
+  if (!listed && (keys > 16ll * 16 * w.cluster * kWarps || w.tasks > INT_MAX)) w.tasks = 0;
   return w;
 }
 

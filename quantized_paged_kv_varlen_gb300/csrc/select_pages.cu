@@ -66,24 +66,38 @@ __device__ __forceinline__ float to_f32(uint32_t half_word) {
   }
 }
 
-// c of an element: RNE(q * 127 / a), with r = 1 / a rounded.  q has 11 significant
+// c of an element: RNE(q * 127 / a), with 1 / a rounded.  q has 11 significant
 // bits at most, so q * 127 is exact; the corrected quotient (as in write_group4.cu)
 // meets a tie exactly where there is one, and elsewhere the distance to the next
 // is a thousand times its error.
+struct Unit {
+  float a, r;       // the largest magnitude times k, and one over it
+  float k;          // 127 times the power of two that keeps both in range
+  bool scored;
+};
+__device__ __forceinline__ Unit unit_of(float amax) {
+  Unit u;
+  u.scored = amax > 0.f && amax < INFINITY;
+  const float p = amax > 0x1p60f ? 0x1p-64f : amax < 0x1p-60f ? 0x1p64f : 1.f;
+  u.a = amax * p;
+  u.r = u.scored ? __frcp_rn(u.a) : 0.f;
+  u.k = 127.f * p;
+  return u;
+}
 template <typename E>
-__device__ __forceinline__ float code_of(uint32_t half_word, float a, float r) {
-  const float x = to_f32<E>(half_word) * 127.f, y = x * r;
-  return rintf(fmaf(fmaf(-y, a, x), r, y));
+__device__ __forceinline__ float code_of(uint32_t half_word, const Unit& u) {
+  const float x = to_f32<E>(half_word) * u.k, y = x * u.r;
+  return rintf(fmaf(fmaf(-y, u.a, x), u.r, y));
 }
 
 // A piece of q as f16 codes: the positive ones beside the maxima, the negative
 // ones beside the minima.
 template <typename E>
-__device__ __forceinline__ uint2 codes_of(uint2 w, float a, float r, bool scored, bool is_max) {
+__device__ __forceinline__ uint2 codes_of(uint2 w, const Unit& u, bool is_max) {
   float x[4] = {0.f, 0.f, 0.f, 0.f};
-  if (scored) {
-    x[0] = code_of<E>(w.x & 0xFFFFu, a, r), x[1] = code_of<E>(w.x >> 16, a, r);
-    x[2] = code_of<E>(w.y & 0xFFFFu, a, r), x[3] = code_of<E>(w.y >> 16, a, r);
+  if (u.scored) {
+    x[0] = code_of<E>(w.x & 0xFFFFu, u), x[1] = code_of<E>(w.x >> 16, u);
+    x[2] = code_of<E>(w.y & 0xFFFFu, u), x[3] = code_of<E>(w.y >> 16, u);
   }
 #pragma unroll
   for (int e = 0; e < 4; ++e) x[e] = is_max ? fmaxf(x[e], 0.f) : fminf(x[e], 0.f);
@@ -249,8 +263,7 @@ __global__ void __launch_bounds__(kThreads, NB == 1 && D == 128 ? 4 : 1) select_
     for (int w = 0; w < kWarps; ++w) all = max(all, __float_as_uint(s_amax[w]));
     amax = to_f32<E>(all);
   }
-  const bool scored = amax > 0.f && amax < INFINITY;
-  const float rcp = scored ? __frcp_rn(amax) : 0.f;
+  const Unit unit = unit_of(amax);
 
   // ---- scores
   for (int c0 = 0; c0 < a.G; c0 += 8 * NB) {
@@ -260,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, NB == 1 && D == 128 ? 4 : 1) select_
       const int l = i % 32, c = i / 128 % KC, w4 = i / 32 % 4, nb = i / (128 * KC);
       const uint16_t* qh = q + static_cast<size_t>((c0 + 8 * nb + (l >> 2)) % a.G) * D;
       const uint2 w = __ldg(reinterpret_cast<const uint2*>(qh + (16 * ((l & 3) + 4 * c)) % D + 4 * w4));
-      s_q[nb][4 * c + w4][l] = codes_of<E>(w, amax, rcp, scored, c >= KC / 2);
+      s_q[nb][4 * c + w4][l] = codes_of<E>(w, unit, c >= KC / 2);
     }
     __syncthreads();
     for (int i0 = warp * 32; i0 < count; i0 += kWarps * 32) {
@@ -490,15 +503,14 @@ __global__ void __launch_bounds__(kRowWarps * 32, 4) select_rows_kernel(const __
     float top = amax[0];
 #pragma unroll
     for (int x = 1; x < kTok; ++x) top = k == x ? amax[x] : top;
-    const bool scored = top > 0.f && top < INFINITY;
-    const float rcp = scored ? __frcp_rn(top) : 0.f;
+    const Unit unit = unit_of(top);
     const uint16_t* qh = q + (static_cast<size_t>(k) * a.Hq + h * a.G + (col % kGp) % a.G) * D;
 #pragma unroll
     for (int c = 0; c < KC; ++c) {
 #pragma unroll
       for (int w4 = 0; w4 < 4; ++w4) {
         const uint2 w = __ldg(reinterpret_cast<const uint2*>(qh + (16 * (t + 4 * c)) % D + 4 * w4));
-        qf[nb][4 * c + w4] = codes_of<E>(w, top, rcp, scored, c >= KC / 2);
+        qf[nb][4 * c + w4] = codes_of<E>(w, unit, c >= KC / 2);
       }
     }
   }

@@ -284,6 +284,22 @@ def test_select_pages_with_odd_inputs(lib, err):
         assert np.array_equal(got, want) and 5 in got[0, 0] and 5 in got[0, 1]
         assert n == 4 or 20 in got[0, 1]      # with n = 4 three places are sure and one is left, for 5
         assert int(err) == lib.DEV_ERR_BAD_PAGE
+    # the same for tokens of a prompt, and queries at the ends of bf16's range
+    c = _select_case(13, [(400, 900), (300, 300)], 4, 2, 64, 16, "bf16")
+    c["bscale"][c["table"][0, 5]] = np.inf
+    c["q"][0:700:7] = 0
+    c["q"][1:700:7, 1, 3] = float("nan")
+    c["q"][2:700:7, 2, 5] = float("inf")
+    c["q"][3:700:7] *= 2.0 ** 122
+    c["q"][4:700:7] *= 2.0 ** -124
+    c["table"][0, 30], c["table"][1, 4] = -1, 99999
+    for first in (0, 2):
+        got = _run_select(lib, c, err, 6, first=first).cpu().numpy()
+        assert np.array_equal(got, _want_select(c, 6, first=first)) and int(err) == lib.DEV_ERR_BAD_PAGE
+    c = _select_case(14, [(1, 900)] * 4, 4, 2, 64, 16, "bf16")
+    c["q"][0] *= 2.0 ** 122
+    c["q"][1] *= 2.0 ** -124
+    assert np.array_equal(_run_select(lib, c, err, 6).cpu().numpy(), _want_select(c, 6))
     err.zero_()
     c = _select_case(4, [(1, 40), (1, 40)], 2, 1, 64, 16, "bf16")
     c["lens"][0], c["cu"] = 16 * c["table"].shape[1] + 1, np.array([1, 3], np.int32)
@@ -563,6 +579,35 @@ def test_a_serving_step(lib, err, D, ps, dtype):
         check(xs, at, got)
         at = [a + 1 for a in at]
     assert lens.tolist() == at and int(err) == 0
+
+
+def test_offsets_beyond_32_bits(lib, err):
+    """A pool of 4.6 GB (and bounds to match): its last pages are written, read
+    back, chosen and attended to, the first ones are left alone."""
+    H, D, ps, P = 8, 128, 16, 500_000
+    k, v = (torch.zeros(P, H, 1, 9 * D, dtype=torch.uint8, device="cuda") for _ in range(2))
+    bd, bs = torch.zeros(P, H, 2, D, dtype=torch.int8, device="cuda"), torch.zeros(P, H, device="cuda")
+    n, L = 40, 40
+    table = np.array([[P - 1, P - 2, P - 3]], np.int32)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(n, 2 * H, D, generator=g, device="cuda").bfloat16()
+    q = torch.randn(n, 2 * H, D, generator=g, device="cuda").bfloat16()
+    lib.write_cache_group4(x[:, :H], x[:, H:], i32([n]), i32(table), k, v, k_bounds=bd, bound_scale=bs, error_word=err)
+    pools = [np.zeros((3, H, 1, 9 * D), np.uint8) for _ in range(2)]
+    small, sb, ss = np.array([[2, 1, 0]], np.int32), np.zeros((3, H, 2, D), np.int8), np.zeros((3, H), np.float32)
+    f = x.float().cpu().numpy()
+    group4.write(f[:, :H], f[:, H:], [n], [0], small, pools, bounds=sb, bscale=ss)
+    assert same_pool(k[-3:], pools[0]) and same_pool(v[-3:], pools[1]) and np.array_equal(bd[-3:].cpu().numpy(), sb)
+    back = lib.read_cache_group4(k, v, i32([n]), i32(table), n, error_word=err)
+    assert np.array_equal(f64(back[1]), group4.tokens(pools[1], small[0], L))
+    sel = lib.select_pages(q, bd, bs, i32(table), i32([n]), i32([L]), ps, 2, error_word=err)
+    assert np.array_equal(sel.cpu().numpy(), group4.select(q.double().cpu().numpy(), sb, ss, small, [n], [L], ps, 2))
+    case = dict(q=q.cpu(), pools=pools, table=small, cu=[n], lens=[L], T=n, prefix=None, slopes=None, mul=[None, None])
+    for kw in (dict(), dict(selected=sel), dict(max_seqlen_q=n)):
+        case["selected"] = sel.cpu().numpy() if kw.get("selected") is not None else None
+        lse = torch.empty(n, 2 * H, device="cuda")
+        _check_attend(case, lib.attend_group4(q, k, v, i32(table), i32([n]), i32([L]), lse=lse, error_word=err, **kw), lse)
+    assert int(k[:-3].max()) == 0 and int(v[:-3].max()) == 0 and int(err) == 0
 
 
 def test_two_streams_and_workspaces(lib, err):
