@@ -377,8 +377,10 @@ __device__ __forceinline__ bool attend_groups(const SplitArgs& sa, const Task& t
                 o = fmaf(q.slope, static_cast<float>(j0[p] + pg + 8 * e - sp.len) - q.at, o);
               }
               if constexpr (kCap) {
+                // for any cap good to 2^-19 of the score itself, which shows where a row
+                // sees few keys (71 -> 74 us for two long contexts)
                 const float c = v * sc[nb][x];
-                z[p][nb][2 * e + x] = fmaf(a.cap_log2, a.far_cap ? tanh_far(c) : tanh_of(c), o);
+                z[p][nb][2 * e + x] = fmaf(a.cap_log2, tanh_far(c), o);
               } else {
                 z[p][nb][2 * e + x] = fmaf(v, sc[nb][x], o);
               }
