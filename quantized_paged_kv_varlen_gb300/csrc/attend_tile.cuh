@@ -860,30 +860,73 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
       tmem_ld32(srow + 32, v[1]);
       float rvs[kGroups], top = -INFINITY;
       tmem_ld_wait();
-      if constexpr (kCap == kFar) {
-        // 16 columns at a time through TMEM: unrolled, all 64 do not fit the instruction
-        // cache (a prompt of 8192 with a cap of 1000: 1.53 ms against 1.18)
-#pragma unroll 1
+      // Over 4 bits: where no score comes near the cap the series alone, which is good to
+      // 2^-19 of a score and needs no exponential.
+      bool series = false;
+      if constexpr (kCap == kFar && kFmt == kE2m1) {
+        float big = 0.f;
+#pragma unroll
         for (int q = 0; q < kGroups; ++q) {
-          uint32_t w[16];
-          tmem_ld16(srow + 16 * q, w);
+          const uint32_t(&w)[32] = v[q >> 1];
           const float4 s4 = gs[q];
-          const bool bad = __float_as_uint(s4.x) == kBadPageMark;
-          const float f = bad ? 0.f : sc * s4.x, off = bad ? -INFINITY : s4.y - m;
-          tmem_ld_wait();
+          float t4 = 0.f;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float o = kBias ? fmaf(slope, static_cast<float>(j0 + 16 * q + i - at), off) : off;
-            w[i] = __float_as_uint(fmaf(a.cap_log2, tanh_far(__uint_as_float(w[i]) * f), o));
-          }
-          tmem_st16(srow + 16 * q, w);
+          for (int i = 16 * (q & 1); i < 16 * (q & 1) + 16; i += 2)
+            t4 = fmax3(t4, fabsf(__uint_as_float(w[i])), fabsf(__uint_as_float(w[i + 1])));
+          if (__float_as_uint(s4.x) != kBadPageMark) big = fmaxf(big, t4 * fabsf(sc * s4.x));
         }
-        tmem_st_wait();
-        tmem_ld32(srow, v[0]);
-        tmem_ld32(srow + 32, v[1]);
+        series = __all_sync(0xffffffffu, !live || big < 0.5f);
+        if (series) {
+          const uint64_t cap2 = f32x2_pack(a.cap_log2, a.cap_log2);
 #pragma unroll
-        for (int q = 0; q < kGroups; ++q) rvs[q] = gs[q].z;
-        tmem_ld_wait();
+          for (int q = 0; q < kGroups; ++q) {
+            uint32_t(&w)[32] = v[q >> 1];
+            const float4 s4 = gs[q];
+            rvs[q] = s4.z;
+            const bool bad = __float_as_uint(s4.x) == kBadPageMark;
+            const float f = bad ? 0.f : sc * s4.x, off = bad ? -INFINITY : s4.y - m;
+            const uint64_t f2 = f32x2_pack(f, f);
+#pragma unroll
+            for (int i = 16 * (q & 1); i < 16 * (q & 1) + 16; i += 2) {
+              uint64_t o2 = f32x2_pack(off, off);
+              if constexpr (kBias) {
+                const float at0 = static_cast<float>(j0 + 32 * (q >> 1) + i - at), at1 = static_cast<float>(j0 + 32 * (q >> 1) + i + 1 - at);
+                o2 = f32x2_fma(f32x2_pack(slope, slope), f32x2_pack(at0, at1), o2);
+              }
+              const uint64_t x = f32x2_mul(f32x2_pack(__uint_as_float(w[i]), __uint_as_float(w[i + 1])), f2);
+              const float2 z = f32x2_unpack(f32x2_fma(cap2, tanh_series2(x), o2));
+              w[i] = __float_as_uint(z.x);
+              w[i + 1] = __float_as_uint(z.y);
+            }
+          }
+        }
+      }
+      if constexpr (kCap == kFar) {
+        if (!series) {
+          // 16 columns at a time through TMEM: unrolled, all 64 do not fit the instruction
+          // cache (a prompt of 8192 with a cap of 1000: 1.53 ms against 1.18)
+#pragma unroll 1
+          for (int q = 0; q < kGroups; ++q) {
+            uint32_t w[16];
+            tmem_ld16(srow + 16 * q, w);
+            const float4 s4 = gs[q];
+            const bool bad = __float_as_uint(s4.x) == kBadPageMark;
+            const float f = bad ? 0.f : sc * s4.x, off = bad ? -INFINITY : s4.y - m;
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float o = kBias ? fmaf(slope, static_cast<float>(j0 + 16 * q + i - at), off) : off;
+              w[i] = __float_as_uint(fmaf(a.cap_log2, tanh_far(__uint_as_float(w[i]) * f), o));
+            }
+            tmem_st16(srow + 16 * q, w);
+          }
+          tmem_st_wait();
+          tmem_ld32(srow, v[0]);
+          tmem_ld32(srow + 32, v[1]);
+#pragma unroll
+          for (int q = 0; q < kGroups; ++q) rvs[q] = gs[q].z;
+          tmem_ld_wait();
+        }
       } else {
 #pragma unroll
         for (int q = 0; q < kGroups; ++q) {
@@ -1061,8 +1104,13 @@ cudaError_t go_tiles(const TileArgs& a, int sms, cudaStream_t stream) {
 template <typename E, int D, int kFmt>
 cudaError_t pick_tiles(const TileArgs& a, int sms, cudaStream_t s) {
   const bool cap = a.p.cap_log2 > 0.f, bias = a.p.slopes != nullptr;
-  if (a.p.far_cap) return bias ? go_tiles<E, D, kFmt, kFar, true>(a, sms, s) : go_tiles<E, D, kFmt, kFar, false>(a, sms, s);
-  if (cap) return bias ? go_tiles<E, D, kFmt, kNear, true>(a, sms, s) : go_tiles<E, D, kFmt, kNear, false>(a, sms, s);
+  // over 4 bits every cap in the form that is good to 2^-19 of a score itself, which
+  // shows where rows see few keys
+  if (a.p.far_cap || (kFmt == kE2m1 && cap))
+    return bias ? go_tiles<E, D, kFmt, kFar, true>(a, sms, s) : go_tiles<E, D, kFmt, kFar, false>(a, sms, s);
+  if constexpr (kFmt != kE2m1) {
+    if (cap) return bias ? go_tiles<E, D, kFmt, kNear, true>(a, sms, s) : go_tiles<E, D, kFmt, kNear, false>(a, sms, s);
+  }
   return bias ? go_tiles<E, D, kFmt, kNone, true>(a, sms, s) : go_tiles<E, D, kFmt, kNone, false>(a, sms, s);
 }
 

@@ -173,6 +173,17 @@ __device__ __forceinline__ float tanh_far(float x) {
   return fabsf(x) < 0.5f ? fmaf(x * t, p, x) : tanh_of(x);
 }
 
+// The series of tanh_far for two values below 1/2.
+__device__ __forceinline__ uint64_t tanh_series2(uint64_t x) {
+  auto both = [](float c) { return f32x2_pack(c, c); };
+  const uint64_t t = f32x2_mul(x, x);
+  uint64_t p = f32x2_fma(both(-1382.f / 155925.f), t, both(62.f / 2835.f));
+  p = f32x2_fma(p, t, both(-17.f / 315.f));
+  p = f32x2_fma(p, t, both(2.f / 15.f));
+  p = f32x2_fma(p, t, both(-1.f / 3.f));
+  return f32x2_fma(f32x2_mul(x, t), p, x);
+}
+
 // The power of two that takes a row of bf16 values with the given largest
 // magnitude to [2^14, 2^15), and its inverse: f16 then holds the row's values
 // (8 significant bits) exactly down to 2^-31 of the largest.
