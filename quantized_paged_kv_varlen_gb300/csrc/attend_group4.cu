@@ -361,33 +361,48 @@ __device__ __forceinline__ bool attend_groups(const SplitArgs& sa, const Task& t
           }
         }
       }
+      // y - m in log2 units.  A capped score is good to 2^-19 of itself at any cap, which
+      // shows where a row sees few keys; where none comes near the cap its series is enough.
+      auto score = [&](auto series) {
 #pragma unroll
-      for (int p = 0; p < kPair; ++p) {
-        // y - m in log2 units
+        for (int p = 0; p < kPair; ++p) {
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
+          for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
+            for (int x = 0; x < 2; ++x) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float v = s[p][nb][2 * e + x];
-              float o = -m[nb][x];
-              if constexpr (kBias) {
-                const RowInfo& q = ri[8 * nb + 2 * t + x];
-                o = fmaf(q.slope, static_cast<float>(j0[p] + pg + 8 * e - sp.len) - q.at, o);
-              }
-              if constexpr (kCap) {
-                // for any cap good to 2^-19 of the score itself, which shows where a row
-                // sees few keys (71 -> 74 us for two long contexts)
-                const float c = v * sc[nb][x];
-                z[p][nb][2 * e + x] = fmaf(a.cap_log2, tanh_far(c), o);
-              } else {
-                z[p][nb][2 * e + x] = fmaf(v, sc[nb][x], o);
+              for (int e = 0; e < 2; ++e) {
+                const float v = s[p][nb][2 * e + x];
+                float o = -m[nb][x];
+                if constexpr (kBias) {
+                  const RowInfo& q = ri[8 * nb + 2 * t + x];
+                  o = fmaf(q.slope, static_cast<float>(j0[p] + pg + 8 * e - sp.len) - q.at, o);
+                }
+                if constexpr (kCap) {
+                  const float c = v * sc[nb][x];
+                  z[p][nb][2 * e + x] = fmaf(a.cap_log2, decltype(series)::value ? tanh_series(c) : tanh_far(c), o);
+                } else {
+                  z[p][nb][2 * e + x] = fmaf(v, sc[nb][x], o);
+                }
               }
             }
           }
         }
+      };
+      bool near = true;
+      if constexpr (kCap) {
+        bool small = true;
+#pragma unroll
+        for (int p = 0; p < kPair; ++p) {
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) small &= fabsf(s[p][nb][e] * sc[nb][e & 1]) < 0.5f;
+          }
+        }
+        near = __all_sync(0xffffffffu, small);
       }
+      if (near) score(std::true_type()); else score(std::false_type());
       if (part) {
 #pragma unroll
         for (int p = 0; p < kPair; ++p) {

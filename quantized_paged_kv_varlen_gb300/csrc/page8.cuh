@@ -173,7 +173,15 @@ __device__ __forceinline__ float tanh_far(float x) {
   return fabsf(x) < 0.5f ? fmaf(x * t, p, x) : tanh_of(x);
 }
 
-// The series of tanh_far for two values below 1/2.
+// The series of tanh_far for values below 1/2, for one and for two.
+__device__ __forceinline__ float tanh_series(float x) {
+  const float t = x * x;
+  float p = fmaf(-1382.f / 155925.f, t, 62.f / 2835.f);
+  p = fmaf(p, t, -17.f / 315.f);
+  p = fmaf(p, t, 2.f / 15.f);
+  p = fmaf(p, t, -1.f / 3.f);
+  return fmaf(x * t, p, x);
+}
 __device__ __forceinline__ uint64_t tanh_series2(uint64_t x) {
   auto both = [](float c) { return f32x2_pack(c, c); };
   const uint64_t t = f32x2_mul(x, x);

@@ -387,7 +387,8 @@ CASES = [
     ([(300, 300)], 8, 2, 128, 16, "bf16", {}, {}), ([(190, 700), (1, 90), (33, 40)], 14, 2, 128, 32, "f16", dict(prefix=[100, 0, 40]), {}),
     ([(257, 257)], 4, 4, 64, 16, "bf16", dict(mul=True), dict(window=70)), ([(100, 800)], 7, 1, 64, 48, "bf16", dict(slopes=True), dict(logit_cap=30.0)),
     ([(150, 600), (1, 5)], 5, 1, 128, 16, "bf16", {}, dict(causal=False)), ([(90, 50)], 8, 1, 128, 16, "f16", {}, {}), ([(130, 400)], 2, 2, 128, 128, "bf16", {}, dict(logit_cap=500.0)),
-    ([(40, 300)], 130, 1, 64, 16, "bf16", {}, {})]
+    ([(40, 300)], 130, 1, 64, 16, "bf16", {}, {}), ([(150, 300), (2, 50), (1, 400)], 6, 2, 128, 16, "bf16", dict(size=6.0), dict(logit_cap=5.0)),
+    (DECODE, 8, 2, 64, 16, "f16", dict(size=6.0, slopes=True), dict(logit_cap=3.0))]
 
 
 @pytest.mark.parametrize("reqs,Hq,H,D,ps,dtype,case_kw,kw", CASES)
