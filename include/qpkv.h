@@ -936,7 +936,7 @@ qpkv_status qpkv_read_group4(const qpkv_read_group4_params* params, void* stream
  * heads that share it and c = RNE(q * 127 / a) (0 where a is 0 or not finite),
  *   score(page) = bound_scale[page] * max over the G heads of
  *                 sum_d max(c_d * min_d, c_d * max_d)
- * (whole numbers below 2^24, one float32 product; +inf where the scale is inf):
+ * (whole numbers below 2^24, one float32 product; +inf where the scale is not finite):
  * a bound, in units of its own, on what any key of the page can score.  The
  * `first` first and the `last` last candidates are taken, then the highest
  * scores, of equal ones the lower page.

@@ -152,7 +152,7 @@ def select(q, bounds, bscale, table, cu, lens, ps, n, first=0, last=1, window=0,
                         continue
                     mn, mx = bounds[pg, h].astype(np.int64)
                     s = int(np.maximum(c * mn, c * mx).sum(1).max())
-                    s = np.inf if np.isinf(bscale[pg, h]) else float(F32(F32(s) * bscale[pg, h]))
+                    s = float(F32(F32(s) * bscale[pg, h])) if np.isfinite(bscale[pg, h]) else np.inf
                     sure = p - lo < first or hi - p < last
                     scored.append((not sure, -s, p))
                 ids = sorted(p for _, _, p in sorted(scored)[:n])

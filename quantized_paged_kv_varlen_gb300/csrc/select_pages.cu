@@ -56,6 +56,11 @@ __device__ __forceinline__ uint32_t key_of(float s) {
   const uint32_t u = __float_as_uint(s);
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
+// A page's key, of its sum and scale: one that is not finite (of a NaN in the page,
+// or bounds never made) counts as +inf, as a NaN's bits would be those of kSure.
+__device__ __forceinline__ uint32_t key_of(float sum, float scale) {
+  return key_of(fabsf(scale) < INFINITY ? sum * scale : INFINITY);
+}
 
 template <typename E>
 __device__ __forceinline__ float to_f32(uint32_t half_word) {
@@ -172,7 +177,8 @@ struct Search {
       return false;
     }
     need = n - x.sure;
-    if (need == 0) {
+    if (need <= 0) {
+      need = 0;
       above = kSure - 1;
       return false;
     }
@@ -336,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, NB == 1 && D == 128 ? 4 : 1) select_
           uint32_t key = 0;
           if (pg >= 0) {
             key = p - p_lo < a.first || p_hi - p < a.last ? kSure
-                  : key_of(sc == INFINITY ? INFINITY : (t == 0 ? m0 : m1) * sc);
+                  : key_of(t == 0 ? m0 : m1, sc);
           }
           s_key[i] = c0 == 0 ? key : max(key, s_key[i]);
         }
@@ -596,7 +602,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 4) select_rows_kernel(const __
             const int p = p_lo + j;
             uint32_t key = 0;
             if (pg >= 0 && p >= lo[x] && p <= hi[x])
-              key = p - lo[x] < a.first || hi[x] - p < a.last ? kSure : key_of(sc == INFINITY ? INFINITY : v * sc);
+              key = p - lo[x] < a.first || hi[x] - p < a.last ? kSure : key_of(v, sc);
             if (mine + x < live && j < count) keys[(mine + x) * ra.stride + j] = key;
           };
           if constexpr (kGp == 1) {

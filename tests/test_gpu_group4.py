@@ -306,6 +306,26 @@ def test_select_pages_with_odd_inputs(lib, err):
     assert (_run_select(lib, c, err, 2).cpu().numpy() == -1).all() and int(err) == lib.DEV_ERR_BAD_LENGTH
 
 
+@pytest.mark.parametrize("reqs,ps", [([(1, 500), (1, 33)], 16), ([(1, 6000)], 16), ([(400, 900), (300, 300)], 32)])
+@pytest.mark.parametrize("value", [float("nan"), -float("nan"), -np.inf, np.inf])
+@pytest.mark.parametrize("share", [0.05, 0.5, 1.0])
+def test_select_pages_with_scales_that_are_no_numbers(lib, err, reqs, ps, value, share):
+    """Scales that are NaN or infinite count as +inf: candidates before those with a
+    finite score, and no more pages are written than a row has places for, with
+    every place sure and with places left (one block, a cluster, prompts)."""
+    H = 2
+    c = _select_case(21, reqs, 4, H, 64, ps, "bf16")
+    rng = np.random.default_rng(int(100 * share))
+    c["bscale"][rng.random(c["bscale"].shape) < share] = value
+    for n, kw in ((3, dict(first=1, last=2)), (1, {}), (6, dict(first=2, last=1))):
+        room = torch.full((4096 + c["T"] * H * n + 4096,), 55, dtype=torch.int32, device="cuda")
+        out = room[4096:-4096].view(c["T"], H, n)
+        got = _run_select(lib, c, err, n, out=out, **kw)
+        assert np.array_equal(got.cpu().numpy(), _want_select(c, n, **kw))
+        assert (room[:4096] == 55).all() and (room[-4096:] == 55).all()
+    assert int(err) == 0
+
+
 # --------------------------------------------------------------- the attention
 
 def _attend_case(seed, reqs, Hq, H, D, ps, dtype, slopes=False, prefix=None, mul=False, n_sel=0, pad=0, size=1.0):
