@@ -776,23 +776,25 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<D, NB>::kBlocks)) attend_w
           for (int n = 0; n < NT / 2; ++n)
             out[n] = make_float4(sums.O[nb][2 * n][c], sums.O[nb][2 * n][2 + c], sums.O[nb][2 * n + 1][c], sums.O[nb][2 * n + 1][2 + c]);
         }
-        if (g == 0) s_ml[warp][r] = make_float2(lsum == 0.f ? -INFINITY : sums.m[nb][c], lsum);
+        if (g == 0) s_ml[warp][r] = make_float2(lsum == 0.f ? -INFINITY : sums.m[nb][c], any ? lsum : -1.f);
       }
     }
     if (C > 1) cluster.sync(); else __syncthreads();
-    // ---- weights: a lane to a part
+    // ---- weights: a lane to a part.  -inf: a part that stored no sums.  Those of every
+    // other one are added, however small its weight: O may hold a NaN of V.
     const float vmul = a.vs != nullptr ? __ldg(a.vs + k.h) : 1.f;
     auto place = [&](int r) {      // row r of o and lse
       const int rr = k.rt * kRows + r, i = listed ? k.token_i : rr / a.G, head = k.h * a.G + (listed ? rr : rr - i * a.G);
       return static_cast<size_t>(k.sp.t0 + i) * a.Hq + head;
     };
     for (int r = warp; r < k.live_rows; r += kWarps) {
-      float2 ml = make_float2(-INFINITY, 0.f);
+      float2 ml = make_float2(-INFINITY, -1.f);
       if (lane < parts) ml = *cluster.map_shared_rank(&s_ml[lane % kWarps][r], lane / kWarps);
       const float M = warp_max(ml.x);
-      const float f = ml.y == 0.f ? 0.f : fast_exp2(ml.x - M);    // a part that saw nothing has no sums either
-      const float sum = warp_sum(ml.y == 0.f ? 0.f : ml.y * f);
-      if (lane < parts) s_w[r][lane] = ml.y == 0.f ? 0.f : f * (vmul / sum);
+      const bool none = ml.y <= 0.f;      // it saw nothing (NaN: it did)
+      const float f = none ? 0.f : fast_exp2(ml.x - M);
+      const float sum = warp_sum(none ? 0.f : ml.y * f);
+      if (lane < parts) s_w[r][lane] = ml.y < 0.f ? -INFINITY : none ? 0.f : f * (vmul / sum);
       if (rank == 0 && lane == 0 && a.lse != nullptr) a.lse[place(r)] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * kLn2;
     }
     __syncthreads();
@@ -801,7 +803,7 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<D, NB>::kBlocks)) attend_w
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int p = 0; p < parts; ++p) {
         const float w = s_w[r][p];
-        if (w == 0.f) continue;         // nothing was stored there
+        if (w == -INFINITY) continue;
         const float4 v = *cluster.map_shared_rank(reinterpret_cast<float4*>(s_o + ((p % kWarps) * kRows + r) * D + d), p / kWarps);
         o.x = fmaf(v.x, w, o.x), o.y = fmaf(v.y, w, o.y), o.z = fmaf(v.z, w, o.z), o.w = fmaf(v.w, w, o.w);
       }

@@ -531,6 +531,36 @@ def test_attend_nan_reaches_those_who_see_it(lib, err, n, D, listed):
     assert int(err) == 0
 
 
+@pytest.mark.parametrize("n,D,listed", [(1, 128, False), (1, 64, True), (5, 64, False), (3, 128, True), (90, 128, False)])
+def test_attend_nan_of_a_value_without_weight(lib, err, n, D, listed):
+    """With a distance bias an old token's weight is zero in float32, and a NaN scale
+    of its value makes its channels NaN all the same, in every form (a narrow and a
+    wide table, a prompt, lists), in all rows that see it and in no others."""
+    ps, L, H, Hq = 16, 900, 2, 4
+    c = _attend_case(9, [(n, L), (n, 60)], Hq, H, D, ps, "bf16")
+    c["slopes"] = np.array([0.5, 4.0, 0.5, 0.25], np.float32)     # times 800 tokens: e^-200 and less
+    if listed:
+        c["selected"] = np.array([[list(range(0, 57, 2))] * H] * n + [[list(range(4)) + [-1] * 25] * H] * n, np.int32)
+    W = c["table"].shape[1]
+    for width in (W, 5000):
+        c["table"] = np.concatenate([c["table"][:, :W], np.full((2, width - W), -1, np.int32)], 1)
+        lse = torch.empty(2 * n, Hq, device="cuda")
+        clean = _run_attend(lib, c, err, max_q=n, lse=lse).clone()
+        clean_lse = lse.clone()
+        assert torch.isfinite(clean).all()
+        for j in (0, 3, 35, 100):
+            codes, scales = group4.rows_of(c["pools"][1])
+            scales[c["table"][0, j // ps], 1, j % ps, 2] = 0x7F
+            c2 = dict(c, pools=[c["pools"][0], group4.pool_of(codes, scales)])
+            got = _run_attend(lib, c2, err, max_q=n, lse=lse)
+            want = np.zeros((2 * n, Hq, D), bool)
+            want[:n, 2:, 32:48] = True
+            assert np.array_equal(torch.isnan(got).cpu().numpy(), want)
+            rest = ~torch.tensor(want).cuda()
+            assert torch.equal(got[rest], clean[rest]) and torch.equal(lse, clean_lse)
+    assert int(err) == 0
+
+
 # ------------------------------------------------------------------- all of them
 
 @pytest.mark.parametrize("D,ps,dtype", [(128, 16, "bf16"), (64, 32, "f16")])
