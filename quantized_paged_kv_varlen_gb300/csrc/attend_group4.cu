@@ -751,8 +751,9 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<D, NB>::kBlocks)) attend_w
   }
   // (the next row tile only where a sequence has more queries than the call's bound says)
   Ring ring = {smem + warp * Sh::kWarpBytes, s_full[warp], 0, 0, 0};
-  for (; k.rt * kRows < (listed ? a.G : k.sp.n * a.G); k.rt += sa.nt) {
-    k.live_rows = min(kRows, (listed ? a.G : k.sp.n * a.G) - k.rt * kRows);
+  const int rows = listed ? a.G : k.sp.n * a.G;
+  for (; k.rt * kRows < rows; k.rt += sa.nt) {
+    k.live_rows = min(kRows, rows - k.rt * kRows);
     // ---- this warp's share
     const int parts = C * kWarps, me = rank * kWarps + warp;
     const int share = (ng + parts * Sh::kPair - 1) / (parts * Sh::kPair) * Sh::kPair;
@@ -809,6 +810,8 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<D, NB>::kBlocks)) attend_w
       }
       *reinterpret_cast<uint2*>(static_cast<E*>(a.o) + place(r) * D + d) = make_uint2(pack_out<E>(o.y, o.x), pack_out<E>(o.w, o.z));
     }
+    // the next row tile's copies land where this thread has stored sums
+    if (rows - k.rt * kRows > sa.nt * kRows) fence_proxy_async_smem();
     if (C > 1) cluster.sync(); else __syncthreads();     // nobody leaves while its sums are read
   }
 }

@@ -561,6 +561,23 @@ def test_attend_nan_of_a_value_without_weight(lib, err, n, D, listed):
     assert int(err) == 0
 
 
+@pytest.mark.parametrize("Hq,H,D,max_q", [(4, 1, 64, 1), (16, 2, 128, 1), (10, 1, 64, 2), (8, 8, 128, 3)])
+def test_attend_more_queries_than_the_bound(lib, err, Hq, H, D, max_q):
+    """The one-kernel form with a bound of one to three queries and sequences of many:
+    a block takes row tile after row tile, whose copies land where the sums of the one
+    before lay."""
+    c = _attend_case(10, [(40, 700), (3, 9), (25, 400), (1, 650)], Hq, H, D, 16, "bf16", mul=True, slopes=True)
+    lse = torch.empty(c["T"], Hq, device="cuda")
+    wanted = _want_attend(c)
+    first = None
+    for _ in range(10):
+        got = _run_attend(lib, c, err, max_q=max_q, lse=lse)
+        first = got if first is None else first
+        assert torch.equal(got, first)
+    _check_attend(c, got, lse, wanted)
+    assert int(err) == 0
+
+
 # ------------------------------------------------------------------- all of them
 
 @pytest.mark.parametrize("D,ps,dtype", [(128, 16, "bf16"), (64, 32, "f16")])
