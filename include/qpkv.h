@@ -986,7 +986,8 @@ qpkv_status qpkv_select_pages(const qpkv_select_pages_params* params, void* stre
  * num_selected], from qpkv_select_pages or elsewhere) a row sees only keys of
  * the pages listed for its token and kv head; -1 lists none, a place that holds
  * no key of the sequence is skipped (QPKV_DEV_ERR_BAD_INDEX), a page listed
- * twice counts twice.  Capped scores are good to 2^-19 of themselves at any cap.
+ * twice counts twice.  Capped scores are good to 2^-19 of themselves at any cap;
+ * caps above 1e20 are refused (INVALID_ARG), as the scores over them leave float32.
  * A NaN scale makes NaN what sees its token: a K scale the
  * whole row, a V scale the 16 channels; rows that do not see the token are not
  * touched by it.

@@ -1328,7 +1328,7 @@ def attend_group4(q, k_pool, v_pool, block_table, cu_seqlens_q, seqlens_kv, max_
     ``attend_page8``, and: k_mul, v_mul float32 [Hkv], those the cache was
     written with; selected int32 [T, Hkv, n]: each row sees only keys of the
     pages listed for its token and kv head (``select_pages``; -1 lists none, a
-    page listed twice counts twice)."""
+    page listed twice counts twice).  logit_cap: 1e-20 to 1e20, 0: none."""
     torch = _torch()
     lib = load()
     i32, f32 = torch.int32, torch.float32

@@ -116,8 +116,11 @@ size_t qpkv_attend_group4_workspace_bytes(int32_t num_seqs, int32_t num_tokens, 
 
 qpkv_status qpkv_attend_group4(const qpkv_attend_group4_params* p, void* stream) {
   if (p == nullptr || p->num_seqs < 0 || p->num_tokens < 0 || p->num_heads_q < 1 || p->window < 0 ||
-      !(p->logit_cap >= 0.f) || !std::isfinite(p->logit_cap) || !std::isfinite(p->sm_scale) ||
-      (p->logit_cap > 0.f && p->logit_cap < 1e-20f) ||   // its reciprocal times a score must stay finite
+      !(p->logit_cap >= 0.f) || !std::isfinite(p->sm_scale) ||
+      // its reciprocal times a score must stay finite.  At the other end the products' factor over the
+      // cap falls below float32's normal numbers; its error of 2^-150, times a product below 2^34,
+      // times this cap is 2^-49 of a score, and at 1e38, beside an infinite cap * log2(e), 2^10
+      (p->logit_cap > 0.f && p->logit_cap < 1e-20f) || p->logit_cap > 1e20f ||
       (p->selected != nullptr && p->num_selected < 1))
     return QPKV_ERR_INVALID_ARG;
   const qpkv_status st = check_cache(p->head_dim, p->page_size, p->num_pages, p->bt_stride, p->num_heads_kv, p->dtype);

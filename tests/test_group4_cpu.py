@@ -110,6 +110,12 @@ def test_attend_refuses(q, change, want):
     assert _call(q.load().qpkv_attend_group4, _attend(q), **change) == want
 
 
+@pytest.mark.parametrize("cap,want", [(1e20, 0), (1e-20, 0), (50.0, 0), (1.01e20, INVALID), (1e30, INVALID), (2.4e38, INVALID), (3.4e38, INVALID)])
+def test_attend_takes_caps_whose_scores_stay_in_float32(q, cap, want):
+    # no tokens: the checks alone
+    assert _call(q.load().qpkv_attend_group4, _attend(q), logit_cap=cap, num_tokens=0) == want
+
+
 def test_attend_workspace_sizes(q):
     f = q.load().qpkv_attend_group4_workspace_bytes
     assert f(-1, 5, 8, 2, 128) == f(2, -1, 8, 2, 128) == f(2, 5, 7, 2, 128) == f(2, 5, 8, 2, 96) == 0
