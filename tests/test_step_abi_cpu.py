@@ -103,6 +103,11 @@ def test_attend_page8_refuses(q, change, want):
     assert _call(q.load().qpkv_attend_page8, _attend(q), **change) == want
 
 
+@pytest.mark.parametrize("cap,want", [(2.3e38, 0), (1e9, 0), (2.4e38, INVALID), (3.4e38, INVALID)])
+def test_attend_page8_refuses_caps_that_log2_units_do_not_hold(q, cap, want):
+    assert _call(q.load().qpkv_attend_page8, _attend(q), logit_cap=cap, num_tokens=0) == want
+
+
 def test_attend_workspace_sizes(q):
     f = q.load().qpkv_attend_page8_workspace_bytes
     assert f(-1, 5, 8, 2, 128) == f(2, -1, 8, 2, 128) == f(2, 5, 7, 2, 128) == f(2, 5, 8, 2, 96) == 0
