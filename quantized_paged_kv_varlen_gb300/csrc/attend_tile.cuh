@@ -78,7 +78,7 @@ constexpr int kOverhead = 9;
 // One step of the CTA: a key tile of one (item, kv head).
 enum : int { kFirst = 1, kLast = 2, kHasB = 4, kWholeTask = 8, kEnd = 16, kAllKeys = 32 };
 struct Step {
-  float4 sc[kGroups]; // per 16 keys: ks, log2 vs, 1 / vs
+  float4 sc[kGroups]; // per 16 keys: ks, log2 vs, 1 / vs (E2M1: ks alone)
   int at[kGroups];    // per 16 keys: first pool row, -1: no keys
   int flags;          // and the segment's number % 4 << 8
   int j0;             // first key
@@ -627,10 +627,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
         const int pg = gi / gpp;
         const int page = __ldg(a.bt + static_cast<size_t>(w.it.b) * a.bt_stride + pg);
         if (page >= 0 && page < a.num_pages) {
-          if constexpr (kFmt == kE2m1) {     // a block of 16 tokens; the heads' factors
+          // (4 bits: a block of 16 tokens, and the head's factor of K; that of V, the same for
+          // all keys, enters with the results: as a scale of keys it would end at kMinScale)
+          if constexpr (kFmt == kE2m1) {
             x.at = (page * a.Hkv + x.h) * gpp + (gi - pg * gpp);
             x.ks = a.ks != nullptr ? __ldg(a.ks + x.h) : 1.f;
-            x.vs = a.vs != nullptr ? __ldg(a.vs + x.h) : 1.f;
+            x.vs = 1.f;
           } else {
             x.at = (a.hnd ? page * a.Hkv + x.h : page) * a.ps + (gi - pg * gpp) * 16;
             const size_t sx = static_cast<size_t>(page) * a.Hkv + x.h;
@@ -820,6 +822,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
     int hi = 0, lo = 0, at = 0;
     bool live = false;
     size_t row = 0;                               // its row of o or of the workspace
+    [[maybe_unused]] float vmul = 1.f;            // E2M1: the head's factor of V
     [[maybe_unused]] uint32_t nan = 0;            // E2M1: groups of 16 channels with a NaN that the row sees
     while (true) {
       if (!warp_await(&sh.s_full[x][cnt & 1], (cnt >> 1) & 1, sh, a.err)) break;
@@ -844,6 +847,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
         m = l = 0.f;
         seen = !live;         // dead rows never wait for a key
         nan = 0;
+        if constexpr (kFmt == kE2m1) {
+          if (a.vs != nullptr) vmul = __ldg(a.vs + st.h);
+        }
       }
       const float4* gs = st.sc;
       const int j0 = st.j0;
@@ -882,9 +888,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
           for (int q = 0; q < kGroups; ++q) {
             uint32_t(&w)[32] = v[q >> 1];
             const float4 s4 = gs[q];
-            rvs[q] = s4.z;
+            rvs[q] = kFmt == kE2m1 ? 1.f : s4.z;
             const bool bad = __float_as_uint(s4.x) == kBadPageMark;
-            const float f = bad ? 0.f : sc * s4.x, off = bad ? -INFINITY : s4.y - m;
+            const float f = bad ? 0.f : sc * s4.x, off = bad ? -INFINITY : (kFmt == kE2m1 ? 0.f : s4.y) - m;
             const uint64_t f2 = f32x2_pack(f, f);
 #pragma unroll
             for (int i = 16 * (q & 1); i < 16 * (q & 1) + 16; i += 2) {
@@ -911,7 +917,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
             tmem_ld16(srow + 16 * q, w);
             const float4 s4 = gs[q];
             const bool bad = __float_as_uint(s4.x) == kBadPageMark;
-            const float f = bad ? 0.f : sc * s4.x, off = bad ? -INFINITY : s4.y - m;
+            const float f = bad ? 0.f : sc * s4.x, off = bad ? -INFINITY : (kFmt == kE2m1 ? 0.f : s4.y) - m;
             tmem_ld_wait();
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -924,7 +930,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
           tmem_ld32(srow, v[0]);
           tmem_ld32(srow + 32, v[1]);
 #pragma unroll
-          for (int q = 0; q < kGroups; ++q) rvs[q] = gs[q].z;
+          for (int q = 0; q < kGroups; ++q) rvs[q] = kFmt == kE2m1 ? 1.f : gs[q].z;
           tmem_ld_wait();
         }
       } else {
@@ -932,9 +938,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
         for (int q = 0; q < kGroups; ++q) {
           uint32_t(&w)[32] = v[q >> 1];
           const float4 s4 = gs[q];
-          rvs[q] = s4.z;
+          rvs[q] = kFmt == kE2m1 ? 1.f : s4.z;
           const bool bad = __float_as_uint(s4.x) == kBadPageMark;
-          const float f = bad ? 0.f : sc * s4.x, off = bad ? -INFINITY : s4.y - m;
+          const float f = bad ? 0.f : sc * s4.x, off = bad ? -INFINITY : (kFmt == kE2m1 ? 0.f : s4.y) - m;
           const int w0 = 16 * (q & 1);
           if constexpr (!kCap && !kBias) {
             const uint64_t f2 = f32x2_pack(f, f), o2 = f32x2_pack(off, off);
@@ -1011,7 +1017,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
             pk[i] = f32x2_to_f16x2(p1, p0);
           }
           const float2 ls = f32x2_unpack(ls2);
-          l = fmaf(ls.x + ls.y, rvs[2 * c + q], l);
+          l = kFmt == kE2m1 ? l + (ls.x + ls.y) : fmaf(ls.x + ls.y, rvs[2 * c + q], l);
         }
         tmem_st16(srow + 16 * c, pk);
       }
@@ -1026,7 +1032,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
         // l = 0: no key seen; NaN (of a NaN score, which moves no m) goes into o and lse
         const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
         if (flags & kWholeTask) {
-          const float so = l == 0.f ? 0.f : 1.f / l;
+          const float so = l == 0.f ? 0.f : vmul / l;
           E* out = static_cast<E*>(a.o) + row * D;
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
@@ -1058,7 +1064,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
             if (live) {
               uint4* o4 = reinterpret_cast<uint4*>(out + 32 * c);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) o4[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+              for (int i = 0; i < 8; ++i) {
+                if constexpr (kFmt == kE2m1) {
+#pragma unroll
+                  for (int k = 4 * i; k < 4 * i + 4; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * vmul);
+                }
+                o4[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+              }
             }
           }
           if (live) ta.part_ml[row] = make_float2(l == 0.f ? -INFINITY : m, l);

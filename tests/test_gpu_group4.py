@@ -578,6 +578,23 @@ def test_attend_more_queries_than_the_bound(lib, err, Hq, H, D, max_q):
     assert int(err) == 0
 
 
+@pytest.mark.parametrize("reqs", [[(1, 300), (1, 30)], [(5, 400), (2, 20)], [(150, 150), (1, 40)], [(60, 700)]])
+@pytest.mark.parametrize("D,listed", [(128, False), (64, False), (64, True)])
+def test_attend_factors_far_from_one(lib, err, reqs, D, listed):
+    """Factors of V from 2^-90 to 2^60 beside each other (bf16 holds what they give),
+    in every form: they scale their head's outputs and nothing else."""
+    c = _attend_case(17, reqs, 8, 4, D, 16, "bf16", n_sel=7 if listed else 0)
+    c["mul"] = [np.array([1.0, 0.75, 2.0, 1.0], np.float32), np.array([2.0 ** -90, 2.0 ** 60, 2.0 ** -83 * 1.3, 1e-20], np.float32)]
+    wanted = _want_attend(c)
+    W, T = c["table"].shape[1], c["T"]
+    for width in (W, 5000):
+        c["table"] = np.concatenate([c["table"][:, :W], np.full((len(reqs), width - W), -1, np.int32)], 1)
+        lse = torch.empty(T, 8, device="cuda")
+        got = _run_attend(lib, c, err, max_q=max(n for n, _ in reqs), lse=lse)
+        _check_attend(c, got, lse, wanted)
+    assert int(err) == 0
+
+
 # ------------------------------------------------------------------- all of them
 
 @pytest.mark.parametrize("D,ps,dtype", [(128, 16, "bf16"), (64, 32, "f16")])
