@@ -595,6 +595,56 @@ def test_attend_factors_far_from_one(lib, err, reqs, D, listed):
     assert int(err) == 0
 
 
+@pytest.mark.parametrize("cap", [20.0, 50.0, 500.0, 1e6, 1e20])
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("f16", 64)])
+@pytest.mark.parametrize("scores", ["small", "mixed", "large"])
+def test_capped_scores_are_good_to_a_share_of_themselves(lib, err, cap, dtype, D, scores):
+    """Rows that see one key, no bias: the lse is the capped score, c = cap tanh(x / cap),
+    for scores far below the cap, on both sides of half of it, and about it, in every form.
+
+    q and K have one channel each, so the product is exact.  The score is good to 2^-19
+    of itself by definition.  Then, in log2 units: m + 7 is the score y, z = y - m is
+    rounded at 7 (2^-22), its exponential is good to 2^-22 (1.45 times that in the
+    logarithm), log2 of it at 7 to a step (2^-21), the sum to 2^-24 |y|, ln 2 and the
+    last product to 2^-24 each: 2^-19 |c| + 2^-22 |c| + ln 2 (2^-22 + 1.45 * 2^-22 +
+    2^-21 = 1.07e-6) < 2^-19 |c| + 2^-22 |c| + 2^-20.  (An exponential form good to 3e-7
+    of the cap is off by 6e-6 at 20, a series of six terms by 8e-6 c at x = 0.6 cap.)"""
+    cap = float(np.float32(cap))
+    rng = np.random.default_rng(30)
+    ps, H, Hq, scale, ch = 16, 2, 8, 0.125, 5
+    for reqs, max_q, width, listed in (([(1, 70), (1, 5), (1, 400)], 1, 0, False), ([(1, 70), (1, 5), (1, 400)], 1, 5000, False),
+                                       ([(5, 90), (6, 6)], 6, 0, False), ([(5, 90), (6, 6)], 6, 5000, False),
+                                       ([(130, 300), (70, 70)], 130, 0, False), ([(9, 200), (1, 30)], 9, 0, True)):
+        c = _attend_case(31, reqs, Hq, H, D, ps, dtype)
+        T = c["T"]
+        k = np.zeros((len(c["pools"][0]), H, ps, D), np.float32)
+        k[..., ch] = 6.0
+        c["pools"][0] = group4.pool_of(*group4.encode(k))
+        part = np.exp(rng.uniform(np.log(1e-5), np.log(0.45), (T, Hq)))           # of the cap
+        if scores == "mixed":
+            half = rng.random((T, Hq)) < 0.5
+            part[half] = rng.uniform(0.4, 0.75, half.sum())
+        if scores == "large":
+            part = rng.uniform(0.55, 4.0, (T, Hq))
+        q = np.zeros((T, Hq, D))
+        q[..., ch] = part * rng.choice([-1, 1], part.shape) * cap / (6 * scale)
+        if dtype == "f16":
+            q = np.clip(q, -60000, 60000)
+        c["q"] = torch.tensor(q).to(DT[dtype])
+        x = c["q"].double().numpy()[..., ch] * 6 * scale
+        want = cap * np.tanh(x / cap)
+        if listed:
+            at = np.concatenate([np.arange(L - n, L) for n, L in reqs])
+            c["selected"] = np.stack([at // ps, np.full(T, -1)], 1)[:, None].repeat(H, 1).astype(np.int32)
+        W = c["table"].shape[1]
+        c["table"] = np.concatenate([c["table"], np.full((len(reqs), max(0, width - W)), -1, np.int32)], 1)
+        lse = torch.empty(T, Hq, device="cuda")
+        _run_attend(lib, c, err, max_q=max_q, lse=lse, sm_scale=scale, logit_cap=cap, window=1)
+        off = np.abs(f64(lse) - want) / ((2.0 ** -19 + 2.0 ** -22) * np.abs(want) + 2.0 ** -20)
+        assert off.max() <= 1, (reqs, width, listed, off.max())
+    assert int(err) == 0
+
+
 # ------------------------------------------------------------------- all of them
 
 @pytest.mark.parametrize("D,ps,dtype", [(128, 16, "bf16"), (64, 32, "f16")])
