@@ -857,7 +857,7 @@ qpkv_status qpkv_attend_page8(const qpkv_attend_page8_params* params, void* stre
  * A sequence whose rows do not fit T, or whose positions leave the rope
  * tables, is left out (QPKV_DEV_ERR_BAD_LENGTH), so are positions past the
  * table row; page ids outside [0, num_pages) are skipped
- * (QPKV_DEV_ERR_BAD_PAGE).
+ * (QPKV_DEV_ERR_BAD_PAGE).  q is rotated whether or not a position has a page.
  * Errors: INVALID_ARG (null pointers, non-positive sizes, one of the tables or
  * of k_bounds / bound_scale without the other, q without tables or q_out,
  * pointers not 16-byte aligned (scales and mul: 4), strides not multiples of 8
@@ -946,12 +946,16 @@ qpkv_status qpkv_read_group4(const qpkv_read_group4_params* params, void* stream
  *                 -1 behind the last; all -1 for a row without keys; rows behind
  *                 the last sequence are left as they are
  *   max_seqlen_q  a bound on any n (<= 0: unknown); picks the kernel only
+ * Candidates are those of causal attention without a prefix: the pages behind a
+ * token's own, which qpkv_attend_group4 shows it with prefix_lens or causal = 0,
+ * are never chosen.
  * A page id outside [0, num_pages) is no candidate (QPKV_DEV_ERR_BAD_PAGE); a
  * sequence whose rows or length do not fit has none (QPKV_DEV_ERR_BAD_LENGTH).
  * Errors: INVALID_ARG (null or misaligned pointers, negative sizes, first < 0,
  * last < 1, first + last > num_selected), UNSUPPORTED (D, page_size, Hq % Hkv,
- * Hq / Hkv above 128, dtype, bt_stride above 2^18, bt_stride * page_size above
- * 2^31 - 65, T * Hkv * num_selected or T * Hq above 2^31), CUDA. */
+ * Hq / Hkv above 128, dtype, bt_stride above 2^18, bt_stride * page_size or T *
+ * Hq / Hkv above 2^31 - 65, T * Hkv * 8 or T * Hkv * num_selected above 2^31 - 1,
+ * T * Hq above 2^33 - 4, Hkv above 65535), CUDA. */
 typedef struct qpkv_select_pages_params {
   int32_t num_seqs;
   int32_t num_tokens;
@@ -993,8 +997,8 @@ qpkv_status qpkv_select_pages(const qpkv_select_pages_params* params, void* stre
  * touched by it.
  * Calls with `selected` use no workspace, nor do some on short caches: it may be
  * NULL (WORKSPACE_TOO_SMALL where one is needed).  UNSUPPORTED too: num_pages *
- * Hkv * page_size / 16 above 2^31 - 1; with `selected` T * Hq or num_selected *
- * page_size above that. */
+ * Hkv * page_size / 16 above 2^31 - 1, Hkv above 65535; with `selected` T * Hq above
+ * 2^31 - 1 or num_selected * page_size above 2^31 - 65. */
 typedef struct qpkv_attend_group4_params {
   int32_t num_seqs;
   int32_t num_tokens;

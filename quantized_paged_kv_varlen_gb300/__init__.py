@@ -1275,15 +1275,16 @@ def select_pages(q, k_bounds, bound_scale, block_table, cu_seqlens_q, seqlens_kv
                  error_word=None):
     """The pages that each query token attends to: int32 [T, Hkv,
     num_selected], places in the sequence's row of block_table, ascending, -1
-    behind the last (also the form of ``mla_sparse_decode``'s block lists).
-    q [T, Hq, D] (bf16 or f16); k_bounds int8 [P, Hkv, 2, D] and bound_scale
-    float32 [P, Hkv] as ``write_cache_group4`` keeps them; cu_seqlens_q,
-    seqlens_kv as for ``attend_group4``.  Candidates are the pages up to the
-    token's own (of the last ``window`` keys only, with a window); the
-    ``first`` first and ``last`` last of them are always taken, then those
-    with the highest bound on what a query of the kv head's group can score in
-    them, ties to the lower page.  max_seqlen_q: a bound on the queries of a
-    sequence (0: T); it picks the kernel only."""
+    behind the last, as ``attend_group4`` takes them.  q [T, Hq, D] (bf16 or
+    f16); k_bounds int8 [P, Hkv, 2, D] and bound_scale float32 [P, Hkv] as
+    ``write_cache_group4`` keeps them; cu_seqlens_q, seqlens_kv as for
+    ``attend_group4``.  Candidates are the pages up to the token's own (of the
+    last ``window`` keys only, with a window), never those behind it that a
+    prefix or causal=False would show; the ``first`` first and ``last`` last
+    of them are always taken, then those with the highest bound on what a
+    query of the kv head's group can score in them, ties to the lower page.
+    max_seqlen_q: a bound on the queries of a sequence (0: T); it picks the
+    kernel only."""
     torch = _torch()
     lib = load()
     i32 = torch.int32

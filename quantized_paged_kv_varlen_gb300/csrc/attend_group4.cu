@@ -92,7 +92,7 @@ struct Shape {
   static constexpr int kStages = 2;
   static constexpr int kBlock = Group4<D>::kBlock;
   static constexpr int kStage = 2 * kPair * kBlock;  // K and V of its groups
-  // three tiles keep the query fragments, each lane's own, in shared memory
+  // two tiles and three keep the query fragments, each lane's own, in shared memory
   static constexpr bool kQShared = NB >= 2;
   static constexpr int kQBytes = kQShared ? NB * (D / 16) * 32 * 8 : 0;
   static constexpr int kWarpBytes = kStages * kStage;
@@ -895,7 +895,7 @@ Whole whole_plan(const qpkv_attend_group4_params& p, int sms) {
   w.cluster = 1;
   while (w.cluster < 8 && w.tasks * w.cluster * 2 <= 3ll * sms && keys / 16 >= 2 * w.cluster * kWarps * 2) w.cluster *= 2;
   // all keys: a warp's share is 16 groups at most (32 requests of 2,500 tokens with
-  // three drafts, 64 groups a warp: 70 us, in the split form 34)
+  // three drafts, 64 groups a warp: 49 us, in the split form 47; with five 49 and 58)
   if (!listed && (keys > 16ll * 16 * w.cluster * kWarps || w.tasks > INT_MAX)) w.tasks = 0;
   return w;
 }

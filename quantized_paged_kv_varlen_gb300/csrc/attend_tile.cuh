@@ -17,8 +17,9 @@
 //               3,600 cycles a step to issue 24 of them)
 //   warp 13     walks the work: writes for every step what the others need (the
 //               item, the scales) into a ring of eight, and issues the copies of
-//               its keys, a TMA box for 16 of them, into the raw ring (loads into
-//               registers by warps 0-3 took them 1,100 cycles a step to issue)
+//               its keys into the raw ring: for 16 of them a TMA box, or over 4 bits an
+//               untiled copy of their block (loads into registers by warps 0-3 took
+//               them 1,100 cycles a step to issue)
 // (With the walk in every role the registers spilled, into an L1 that shared
 // memory leaves 20 KB: 3.3 ms for a prompt of 8192, 32 heads.)
 // TMEM: two S of 64 columns for each tile, O_A, O_B of 128; a step's f16 P
@@ -38,13 +39,14 @@
 // last piece may be partial and go to the workspace for the join kernel.  Each
 // (item, kv head) counts kOverhead units more than its key tiles, for its
 // queries' load and its results' store (a causal prompt begins with many items
-// of one key tile).  9: the prompt of 8192 took 534 us when this was measured (516
-// now), against 680 (4), 631 (5), 575 (6), 544 (7), 541 (12); over thirteen
+// of one key tile).  9, over 8 bits: the prompt of 8192 took 534 us when this was measured
+// (516 now), against 680 (4), 631 (5), 575 (6), 544 (7), 541 (12); over thirteen
 // batches of prompts and pieces 7 to 12 were within 1 %.
 //
-// The prompt of 8192 with options, us: plain 516, window of 1024 204, bias 627,
-// cap of 50 864 (an exponential and a reciprocal a score more), both 1027, a cap
-// above kNearCap 1183.
+// The prompt of 8192 with options, us, over 8 bits and over 4: plain 516 and 537,
+// window of 1024 204 and 220, bias 627 and 710, cap of 50 864 (an exponential and a
+// reciprocal a score more) and 913 (the series where no score comes near the cap),
+// cap and bias 1027 and 968, a cap above kNearCap 1183 and 911.
 #pragma once
 #include <climits>
 

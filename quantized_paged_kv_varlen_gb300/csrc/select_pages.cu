@@ -441,8 +441,8 @@ __global__ void __launch_bounds__(kThreads, NB == 1 && D == 128 ? 4 : 1) select_
 // of its four warps up to 16 columns of queries (`kTok` tokens), scores all their
 // pages and chooses for each.  32 pages at a time the block widens their bounds
 // to f16 once, into fragments in shared memory that all warps read, while the
-// next 32 are on their way.  (A block a token: 4 pieces of 250 tokens over 10,000,
-// 28 heads, 147 us; a warp for itself, each widening its pages, 49.)
+// next 32 are on their way.  (4 pieces of 250 tokens over 10,000, 28 heads: 43 us;
+// a block a token 72; a warp for itself, each widening its pages, 49.)
 constexpr int kRowWarps = 4;
 constexpr int kRowKeys = 44 * 1024;      // scores of a block beside its fragments
 
@@ -749,7 +749,11 @@ cudaError_t launch_select_pages(const qpkv_select_pages_params& p, cudaStream_t 
   int C = 1;
   while (C < 8 && ((rows * C * 2 <= 2 * 152 && a.bt_stride / (2 * C) >= 64) || (a.bt_stride + C - 1) / C > kMaxKeys)) C *= 2;
   const bool f16 = p.dtype == QPKV_DTYPE_F16;
-  // several queries a sequence, enough of them, and a warp's keys in shared memory
+  // several queries a sequence, enough of them, and a warp's keys in shared memory, by
+  // the width of the table.  4 pieces, 28 heads over 4: 43 us, a block a token 72; behind
+  // wider tables, which leave an SM fewer blocks, 62 (1,408 pages) and 102 (2,800), from
+  // 5,633 on a block a token.  Drafts of 64 requests come here too, and not always for
+  // their good: of 2, 5 and 8, 64 heads over 8: 56, 60 and 64, a block a token 30, 58 and 87
   int gp = 1;
   while (gp < a.G) gp *= 2;
   const int tok = gp >= 4 ? 16 / gp : 4;
